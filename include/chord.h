@@ -1,6 +1,7 @@
 /*
- * chord.h -- C ABI of libchord.so, a W4A16 mixture-of-experts layer for
- * AMD Instinct MI355X (gfx950).
+ * chord.h -- C ABI of libchord.so, mixture-of-experts layers for AMD Instinct
+ * MI355X (gfx950): W4A16 (below), its W8A8 form in 8-bit floating point, the
+ * router in front of both, and the dense 8-bit matrix product next to them.
  *
  * The layer: BF16 activations, unsigned 4-bit weight codes with one BF16 scale
  * per group of 32 along K, dequantised as (q - 8) * s.  Each routed row goes
@@ -481,6 +482,163 @@ chord_status chord_w4a16_moe_grouped_masked(const chord_bf16* a, int E, int max_
                                             void* workspace, size_t ws_bytes,
                                             const chord_schedule* override, uint32_t flags,
                                             void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The router
+ * ------------------------------------------------------------------------- */
+
+typedef enum { CHORD_DTYPE_F32 = 0, CHORD_DTYPE_BF16 = 1, CHORD_DTYPE_F16 = 2 } chord_dtype;
+typedef enum { CHORD_SCORE_SOFTMAX = 0, CHORD_SCORE_SIGMOID = 1 } chord_scoring;
+
+/*
+ * The k experts of each token and their weights, in the form that
+ * chord_moe_align, the dispatch and the layer calls take.
+ *
+ *   score(e)  = softmax over the token's experts, or sigmoid, of the logits
+ *   choice(e) = score(e) + bias(e)             (the bias balances load: it moves
+ *                                               the choice, never the weight)
+ *   groups    : n_group groups of E / n_group neighbouring experts.  A group's
+ *               score is the sum of its two best choices with a bias (of one,
+ *               if it has no more) and its best choice without; only the
+ *               topk_group best groups stay.
+ *   ids       = the k best choices left, descending
+ *   weight(j) = score(ids[j]) [/ (sum of the k scores + 1e-20)] * scaling
+ *
+ * The order is that of the exact values: of the logits without a bias, of the
+ * choices in 64 bits with one.  Ties go to the lowest expert (or group).
+ *
+ * An expert whose logit, or bias, is -inf or NaN is not available: it is never
+ * chosen and adds nothing to a softmax.  Slots that find no expert get id -1
+ * and weight 0; the layer calls, align and dispatch skip such slots.  A logit or
+ * bias of +inf counts as the largest finite number.
+ *
+ * logits:       device [T, ld] of `dtype` (fp32, bf16, fp16), ld >= E; the first
+ *               E values of a row are read.
+ * bias:         device fp32 [E], or NULL.
+ * topk_ids:     device int32 [T, k] out; topk_weights: device fp32 [T, k] out.
+ * 1 <= E <= 1024; 1 <= k <= min(32, topk_group * E / n_group); n_group divides
+ * E, is at most 64, and 1 <= topk_group <= n_group (1, 1: no groups).  T == 0 is
+ * a no-op.  Enqueued on `stream`; needs no workspace.
+ */
+chord_status chord_moe_route(const void* logits, int dtype, int64_t ld, int T, int E,
+                             const float* bias, int k, int scoring, int n_group, int topk_group,
+                             int renormalize, float scaling, int32_t* topk_ids,
+                             float* topk_weights, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * 8-bit floating point (OCP e4m3fn codes) with one fp32 scale for each 128
+ * columns of an activation row and each 128 x 128 block of a weight.
+ * ------------------------------------------------------------------------- */
+
+typedef uint8_t chord_f8;
+
+/* Role of an 8-bit weight: inside the layer, or on its own (chord_f8_gemm). */
+#define CHORD_ROLE_PLAIN 2
+
+#define CHORD_F8_WEIGHT_MAGIC 0x57384538u /* "8E8W" */
+#define CHORD_F8_WEIGHT_VERSION 1u
+
+/* Host handle of a packed 8-bit weight; `data` as in chord_w4a16_weight. */
+typedef struct {
+  uint32_t magic;
+  uint32_t version;
+  int32_t role;       /* CHORD_ROLE_GATE_UP, CHORD_ROLE_DOWN or CHORD_ROLE_PLAIN */
+  int32_t num_experts;
+  int32_t n;
+  int32_t k;
+  int32_t block;      /* always 128 */
+  int32_t reserved;
+  void* data;
+  size_t bytes;
+} chord_f8_weight;
+
+/* Bytes of device memory chord_f8_pack writes; 0 if the shape is unsupported. */
+size_t chord_f8_packed_bytes(int role, int E, int N, int K);
+
+/*
+ * Repacks an 8-bit weight into the library's gfx950 layout.
+ *
+ * codes:   device, e4m3fn [E, N, K].
+ * scales:  device, fp32 [E, ceil(N/128), ceil(K/128)]; weight = code * scale of
+ *          its block.
+ * role:    CHORD_ROLE_GATE_UP (N = 2*I, gate rows first), CHORD_ROLE_DOWN, or
+ *          CHORD_ROLE_PLAIN (a weight of chord_f8_gemm; E = 1, any N and K).
+ * dst:     device, chord_f8_packed_bytes(...) bytes, 16-byte aligned,
+ *          caller-owned; it must outlive every call that uses `handle`.
+ *
+ * Supported: block == 128; N * K rounded up to whole blocks below 2^31 per
+ * expert; for the layer roles N, K (and I) multiples of 128.  Enqueued on
+ * `stream`.
+ */
+chord_status chord_f8_pack(int role, const chord_f8* codes, const float* scales, int E, int N,
+                           int K, int block, void* dst, size_t dst_bytes,
+                           chord_f8_weight* handle, void* stream);
+
+/*
+ * Quantises activation rows, one scale for each 128 columns (the last group of
+ * a row may be shorter).  For a group with largest magnitude A:
+ *
+ *   scale = A / 448;  code = e4m3(448 x / A), rounded to nearest even
+ *
+ * exactly (no code is off because of a rounded quotient or reciprocal).  A
+ * group with A < 2^-100 is held as zeros with scale 0; a group with an infinity
+ * or NaN has scale NaN and zero codes, which makes the outputs that use it NaN.
+ *
+ * x:      device bf16 [T, ld], ld >= K; any K >= 1 and any 2-byte alignment (16-byte
+ *         aligned rows with K % 8 == 0 are read with wide loads).
+ * codes:  device [T, ceil(K/128)*128] out, 16-byte aligned; columns from K on are 0.
+ * scales: device fp32 [T, ceil(K/128)] out.
+ * Enqueued on `stream`; needs no workspace.
+ */
+chord_status chord_f8_quantize(const chord_bf16* x, int64_t T, int K, int64_t ld, chord_f8* codes,
+                               float* scales, void* stream);
+
+/*
+ * Matrix product of quantised activations with a packed weight:
+ *
+ *   out[m, n] = bf16( sum over blocks c of scale_a[m, c] * scale_w[n / 128, c] *
+ *                     sum over k in c of a[m, k] * w[n, k] )
+ *
+ * accumulated in fp32, rounded once.
+ *
+ * codes, scales: chord_f8_quantize's outputs for rows of length K (codes
+ *          16-byte aligned).
+ * w:       handle packed with CHORD_ROLE_PLAIN, [N, K].
+ * out:     device bf16 [M, ld], ld >= N; columns from N on are left as they are.
+ * Enqueued on `stream`; needs no workspace.  M == 0 is a no-op.
+ */
+chord_status chord_f8_gemm(const chord_f8* codes, const float* scales, int64_t M,
+                           const chord_f8_weight* w, chord_bf16* out, int64_t ld, void* stream);
+
+/* Workspace bytes of chord_f8_moe; 0 for bad arguments. */
+size_t chord_f8_moe_workspace_bytes(int T, int k, int E_l, int H, int I);
+
+/*
+ * The W8A8 layer: the indexed layer above with 8-bit weights and activations.
+ *
+ *   out[t] = bf16( sum over local j of topk_weights[t,j] * y_tj ),
+ *   y_tj = W2_e h~,  h = silu(W1_e x~_t) * (W3_e x~_t), both in fp32,
+ *
+ * x~ and h~ being x and h quantised as chord_f8_quantize does.  The call
+ * quantises x and aligns the routing itself.
+ *
+ * x:        device bf16 [T, H], 16-byte aligned.
+ * w13, w2:  handles packed with roles GATE_UP (N = 2I, K = H) and DOWN (N = H,
+ *           K = I), same number of experts; H and I multiples of 128.
+ * topk_ids, topk_weights: device [T, k] int32 / fp32; ids outside
+ *           [expert_begin, expert_begin + E_l) are not local and are left out.
+ *           The same expert may stand in several slots of a token.
+ * num_global_experts: as for chord_w4a16_moe_indexed (a hint for the schedule).
+ * out:      device bf16 [T, H], 16-byte aligned; every row is written.
+ * workspace: chord_f8_moe_workspace_bytes(...) bytes, 256-byte aligned,
+ *           caller-owned; calls that may overlap need one each.
+ * T*k*H must stay below 2^30.  T == 0 is a no-op.
+ */
+chord_status chord_f8_moe(const chord_bf16* x, int T, int H, int I, const chord_f8_weight* w13,
+                          const chord_f8_weight* w2, const int32_t* topk_ids,
+                          const float* topk_weights, int k, int expert_begin,
+                          int num_global_experts, chord_bf16* out, void* workspace,
+                          size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -8,6 +8,7 @@ library is missing this module raises on import -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -20,7 +21,8 @@ STATUS_NAMES = {0: "CHORD_OK", 1: "CHORD_ERR_INVALID_ARGUMENT", 2: "CHORD_ERR_UN
                 3: "CHORD_ERR_LAYOUT_MISMATCH", 4: "CHORD_ERR_WORKSPACE", 5: "CHORD_ERR_ROUTING",
                 6: "CHORD_ERR_HIP"}
 MODE_INDEXED, MODE_CONTIGUOUS, MODE_MASKED = 0, 1, 2
-ROLE_GATE_UP, ROLE_DOWN = 0, 1
+ROLE_GATE_UP, ROLE_DOWN, ROLE_PLAIN = 0, 1, 2
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 FLAG_VALIDATE = 1
 
 EXPORTED = [
@@ -32,7 +34,8 @@ EXPORTED = [
     "chord_w4a16_moe_grouped_contiguous", "chord_w4a16_moe_grouped_masked",
     "chord_moe_dispatch_contiguous_rows", "chord_moe_dispatch_workspace_bytes",
     "chord_moe_dispatch_contiguous", "chord_moe_dispatch_masked", "chord_moe_combine",
-    "chord_w4a16_moe_plan",
+    "chord_w4a16_moe_plan", "chord_moe_route", "chord_f8_packed_bytes", "chord_f8_pack",
+    "chord_f8_quantize", "chord_f8_gemm", "chord_f8_moe_workspace_bytes", "chord_f8_moe",
 ]
 
 
@@ -49,6 +52,13 @@ class Weight(ctypes.Structure):
                 ("bytes", ctypes.c_size_t)]
 
 
+class F8Weight(ctypes.Structure):
+    _fields_ = [("magic", ctypes.c_uint32), ("version", ctypes.c_uint32), ("role", ctypes.c_int32),
+                ("num_experts", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("block", ctypes.c_int32), ("reserved", ctypes.c_int32), ("data", ctypes.c_void_p),
+                ("bytes", ctypes.c_size_t)]
+
+
 class Schedule(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int32), ("tokens", ctypes.c_int32),
                 ("gate_up_nt", ctypes.c_int32), ("gate_up_wk", ctypes.c_int32),
@@ -62,7 +72,8 @@ def _load():
                           "(or __graft_entry__.build()); there is no fallback path")
     lib = ctypes.CDLL(_LIB_PATH)
     P, I, I64, SZ, U32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_uint32
-    WP = ctypes.POINTER(Weight)
+    WP, FP = ctypes.POINTER(Weight), ctypes.POINTER(F8Weight)
+    F = ctypes.c_float
     sig = {
         "chord_status_string": (ctypes.c_char_p, [I]),
         "chord_last_error": (ctypes.c_char_p, []),
@@ -93,6 +104,13 @@ def _load():
         "chord_moe_combine": (I, [P, I64, I, P, P, I, I, P, P]),
         "chord_w4a16_moe_plan": (I, [I, I, I, I, I, I, I, I, I64, I, ctypes.POINTER(Schedule),
                                      ctypes.c_char_p, SZ]),
+        "chord_moe_route": (I, [P, I, I64, I, I, P, I, I, I, I, I, F, P, P, P]),
+        "chord_f8_packed_bytes": (SZ, [I, I, I, I]),
+        "chord_f8_pack": (I, [I, P, P, I, I, I, I, P, SZ, FP, P]),
+        "chord_f8_quantize": (I, [P, I64, I, I64, P, P, P]),
+        "chord_f8_gemm": (I, [P, P, I64, FP, P, I64, P]),
+        "chord_f8_moe_workspace_bytes": (SZ, [I, I, I, I, I]),
+        "chord_f8_moe": (I, [P, I, I, I, FP, FP, P, P, I, I, I, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -371,4 +389,201 @@ def chord_moe_combine(rows, flat_to_row, topk_weights, out=None, stream=None):
         out = torch.empty((T, H), dtype=torch.bfloat16, device=rows.device)
     _check(lib.chord_moe_combine(_ptr(rows), n_rows, H, _ptr(flat_to_row), _ptr(topk_weights), T, k,
                                  _ptr(out), _stream(stream)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# router and 8-bit floating point
+#
+# These wrappers check types, shapes, layouts and devices (the C ABI sees only
+# addresses), run on the device of their first tensor whichever is current, and
+# take scratch memory and outputs from torch's allocator on the stream they run
+# on, call by call: two calls, streams or captured graphs share no memory.
+# ---------------------------------------------------------------------------
+
+def _require(ok: bool, what: str):
+    if not ok:
+        raise ChordError(1, what)
+
+
+def _tensor(t, name: str, dtype, shape, device, contiguous: bool = True):
+    _require(isinstance(t, torch.Tensor), f"{name} must be a tensor")
+    _require(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
+    _require(tuple(t.shape) == tuple(shape), f"{name} must be {list(shape)}, not {list(t.shape)}")
+    _require(t.device == device, f"{name} is on {t.device}, expected {device}")
+    _require(not contiguous or t.is_contiguous(), f"{name} must be contiguous")
+
+
+def _rows(t, name: str, dtypes):
+    """A device matrix whose rows are contiguous; returns its row stride."""
+    _require(isinstance(t, torch.Tensor) and t.is_cuda, f"{name} must be a tensor on the GPU")
+    _require(t.dtype in dtypes, f"{name} has type {t.dtype}")
+    _require(t.dim() == 2, f"{name} must have two dimensions")
+    T, K = t.shape
+    _require(K >= 1, f"{name} has no columns")
+    _require(K == 1 or T == 0 or t.stride(1) == 1, f"{name} must have contiguous rows")
+    ld = t.stride(0) if T > 1 else K
+    _require(ld >= K, f"{name} has overlapping rows")
+    return ld
+
+
+def _on_device(fn):
+    """Runs fn(first, ..., stream) on the device of its first tensor and on
+    `stream`: a raw handle is passed on, and what fn allocates belongs to it."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        _require(isinstance(first, torch.Tensor) and first.is_cuda, "the first tensor must be on the GPU")
+        dev = first.device
+        if stream is not None:
+            _require(stream.device == dev, f"the stream is on {stream.device}, the tensors on {dev}")
+            with torch.cuda.stream(stream):
+                return fn(first, *args, stream=stream.cuda_stream, **kw)
+        if dev.index != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                return fn(first, *args, stream=torch.cuda.current_stream().cuda_stream, **kw)
+        return fn(first, *args, stream=torch.cuda.current_stream().cuda_stream, **kw)
+    return call
+
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+F8_BLOCK = 128
+
+
+@_on_device
+def chord_moe_route(logits, k: int, scoring: int = SCORE_SOFTMAX, bias=None, n_group: int = 1,
+                    topk_group: int = 1, renormalize: bool = True, scaling: float = 1.0, out=None,
+                    stream=None):
+    """The k experts of each row of `logits` [T, E] (fp32, bf16 or fp16; rows may
+    be strided) and their weights: (topk_ids int32 [T, k], topk_weights fp32
+    [T, k]).  Experts with a logit or bias of -inf or NaN are not available;
+    slots without an expert get id -1 and weight 0."""
+    ld = _rows(logits, "logits", _DTYPES)
+    T, E = logits.shape
+    dev = logits.device
+    if bias is not None:
+        _tensor(bias, "bias", torch.float32, (E,), dev)
+    _require(1 <= k <= 32, f"k={k} (1..32)")
+    if out is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    else:
+        ids, weights = out
+        _tensor(ids, "topk_ids", torch.int32, (T, k), dev)
+        _tensor(weights, "topk_weights", torch.float32, (T, k), dev)
+    _check(lib.chord_moe_route(logits.data_ptr(), _DTYPES[logits.dtype], ld, T, E,
+                               None if bias is None else bias.data_ptr(), k, scoring, n_group,
+                               topk_group, renormalize, scaling, ids.data_ptr(), weights.data_ptr(),
+                               stream))
+    return ids, weights
+
+
+class F8PackedWeight:
+    """A packed 8-bit weight: the host handle plus the buffer that owns its bytes."""
+
+    def __init__(self, handle: F8Weight, buf: torch.Tensor):
+        self.handle = handle
+        self.ref = ctypes.byref(handle)
+        self.buf = buf
+
+    @property
+    def num_experts(self):
+        return self.handle.num_experts
+
+
+def chord_f8_packed_bytes(role: int, E: int, N: int, K: int) -> int:
+    return lib.chord_f8_packed_bytes(role, E, N, K)
+
+
+def chord_f8_pack(role: int, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> F8PackedWeight:
+    """codes float8_e4m3fn [E, N, K], scales fp32 [E, ceil(N/128), ceil(K/128)]."""
+    return _f8_pack(codes, scales, role, stream=stream)
+
+
+@_on_device
+def _f8_pack(codes, scales, role, stream=None):
+    _require(codes.dim() == 3, "codes must be [E, N, K]")
+    E, N, K = codes.shape
+    _tensor(codes, "codes", torch.float8_e4m3fn, (E, N, K), codes.device)
+    _tensor(scales, "scales", torch.float32, (E, -(-N // F8_BLOCK), -(-K // F8_BLOCK)), codes.device)
+    nbytes = lib.chord_f8_packed_bytes(role, E, N, K)
+    buf = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=codes.device)
+    h = F8Weight()
+    _check(lib.chord_f8_pack(role, codes.data_ptr(), scales.data_ptr(), E, N, K, F8_BLOCK,
+                             buf.data_ptr(), nbytes, ctypes.byref(h), stream))
+    return F8PackedWeight(h, buf)
+
+
+@_on_device
+def chord_f8_quantize(x, out=None, stream=None):
+    """Codes float8_e4m3fn [T, ceil(K/128)*128] and scales fp32 [T, ceil(K/128)] of
+    the bf16 rows x [T, K] (rows may be strided)."""
+    ld = _rows(x, "x", (torch.bfloat16,))
+    T, K = x.shape
+    groups = -(-K // F8_BLOCK)
+    if out is None:
+        q = torch.empty((T, groups * F8_BLOCK), dtype=torch.float8_e4m3fn, device=x.device)
+        s = torch.empty((T, groups), dtype=torch.float32, device=x.device)
+    else:
+        q, s = out
+        _tensor(q, "codes", torch.float8_e4m3fn, (T, groups * F8_BLOCK), x.device)
+        _tensor(s, "scales", torch.float32, (T, groups), x.device)
+    _check(lib.chord_f8_quantize(x.data_ptr(), T, K, ld, q.data_ptr(), s.data_ptr(), stream))
+    return q, s
+
+
+@_on_device
+def chord_f8_gemm(codes, scales, w: F8PackedWeight, out=None, stream=None):
+    """bf16 [M, N]: chord_f8_quantize's (codes, scales) times the packed weight
+    [N, K].  `out` may have strided rows."""
+    _require(isinstance(w, F8PackedWeight), "w must be a packed 8-bit weight")
+    _require(codes.dim() == 2, "codes must have two dimensions")
+    M = codes.shape[0]
+    N, groups = w.handle.n, -(-w.handle.k // F8_BLOCK)
+    _tensor(codes, "codes", torch.float8_e4m3fn, (M, groups * F8_BLOCK), codes.device)
+    _tensor(scales, "scales", torch.float32, (M, groups), codes.device)
+    _require(w.buf.device == codes.device, f"w is on {w.buf.device}, codes on {codes.device}")
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=codes.device)
+        ld = N
+    else:
+        ld = _rows(out, "out", (torch.bfloat16,))
+        _tensor(out, "out", torch.bfloat16, (M, N), codes.device, contiguous=False)
+    _check(lib.chord_f8_gemm(codes.data_ptr(), scales.data_ptr(), M, w.ref, out.data_ptr(), ld, stream))
+    return out
+
+
+def chord_f8_moe_workspace_bytes(T: int, k: int, E_l: int, H: int, I: int) -> int:
+    return lib.chord_f8_moe_workspace_bytes(T, k, E_l, H, I)
+
+
+@_on_device
+def chord_f8_moe(x, w13: F8PackedWeight, w2: F8PackedWeight, topk_ids, topk_weights,
+                 expert_begin: int = 0, num_global_experts: int = 0, out=None, workspace=None,
+                 stream=None):
+    """The W8A8 layer over this GPU's experts: bf16 [T, H]."""
+    _require(isinstance(w13, F8PackedWeight) and isinstance(w2, F8PackedWeight),
+             "w13 and w2 must be packed 8-bit weights")
+    dev = x.device
+    _require(x.dim() == 2, "x must have two dimensions")
+    T, H = x.shape
+    _tensor(x, "x", torch.bfloat16, (T, w13.handle.k), dev)
+    _require(topk_ids.dim() == 2, "topk_ids must have two dimensions")
+    k = topk_ids.shape[1]
+    _tensor(topk_ids, "topk_ids", torch.int32, (T, k), dev)
+    _tensor(topk_weights, "topk_weights", torch.float32, (T, k), dev)
+    _require(w13.buf.device == dev and w2.buf.device == dev, f"the weights must be on {dev}")
+    I = w2.handle.k
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    else:
+        _tensor(out, "out", torch.bfloat16, (T, H), dev)
+    need = lib.chord_f8_moe_workspace_bytes(T, k, w13.handle.num_experts, H, I)
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    else:
+        _require(workspace.dtype == torch.uint8 and workspace.is_contiguous() and workspace.device == dev,
+                 f"workspace must be contiguous bytes on {dev}")
+    _check(lib.chord_f8_moe(x.data_ptr(), T, H, I, w13.ref, w2.ref, topk_ids.data_ptr(),
+                            topk_weights.data_ptr(), k, expert_begin, num_global_experts,
+                            out.data_ptr(), workspace.data_ptr(), workspace.numel(), stream))
     return out

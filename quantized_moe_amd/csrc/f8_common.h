@@ -1,0 +1,56 @@
+// Device helpers of the 8-bit floating point kernels.
+#pragma once
+
+#include "device_common.h"
+
+namespace chord {
+
+typedef __attribute__((ext_vector_type(8))) int i32x8_t;
+
+constexpr float kF8Tiny = 0x1p-100f;  // a group below it is held as zeros
+
+// Codes and scale of a group whose largest magnitude is A (its bits, so that
+// an infinity or NaN is seen).  448 x / A = (0.875 x) / (A 2^-9), factors that
+// neither overflow nor round for bf16 x.  The quotient is refined once from
+// the hardware reciprocal, which makes it exact wherever it has few bits: a
+// quotient that lies on a border of two codes is found there, and one that
+// does not lies 2^-13 or more away from it.  So every code is the nearest one,
+// at three operations a value.
+struct F8Group {
+  float scale, den, inv;
+};
+__device__ __forceinline__ F8Group f8_group(uint32_t abs_bits) {
+  const float A = __uint_as_float(abs_bits);
+  F8Group g;
+  g.den = A * 0x1p-9f;
+  g.inv = __builtin_amdgcn_rcpf(g.den);
+  g.scale = A / 448.0f;
+  if (!(A >= kF8Tiny) || abs_bits >= 0x7F800000u) {
+    g.den = 0.f;
+    g.inv = 0.f;  // codes 0
+    g.scale = abs_bits >= 0x7F800000u ? __builtin_nanf("") : 0.f;
+  }
+  return g;
+}
+__device__ __forceinline__ float f8_value(const F8Group& g, float x) {
+  const float n = 0.875f * x;
+  const float y = n * g.inv;
+  return __builtin_fmaf(__builtin_fmaf(-y, g.den, n), g.inv, y);
+}
+// Four values of at most 448 -> four codes, nearest even.
+__device__ __forceinline__ uint32_t f8_pack4(float a, float b, float c, float d) {
+  int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
+}
+
+// Unsigned maximum over the 16 lanes of a row, in every lane (register moves:
+// neighbours 1 and 2 away, then the mirrored half row and row).
+__device__ __forceinline__ uint32_t row_max16(uint32_t x) {
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xF, 0xF, true));
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, true));
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xF, 0xF, true));
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x140, 0xF, 0xF, true));
+  return x;
+}
+
+}  // namespace chord

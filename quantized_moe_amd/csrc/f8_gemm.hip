@@ -1,0 +1,203 @@
+// 8-bit GEMM with block scales, weight-streaming form: every workgroup streams
+// its packed weight tiles from HBM straight into registers; waves split K and
+// add up through LDS.
+//
+// One v_mfma_f32_16x16x128_f8f6f4 covers exactly one block of 128 along K, so
+// its result (from a zero accumulator) is the block's partial product, and
+// acc += scale_a * scale_w * partial applies both scales in fp32: four
+// multiply-adds a lane beside 32 cycles of matrix work.  Weights are the A
+// operand (16 output features), tokens the B operand, so a lane's four results
+// belong to one token and share its scale.
+#include "f8_common.h"
+
+namespace chord {
+namespace {
+
+__device__ __forceinline__ uint4 load_stream(const uint8_t* p) {
+  const u32x4_t v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p));
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ i32x8_t operand(uint4 a, uint4 b) {
+  return i32x8_t{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+}
+
+// Four neighbouring outputs, as wide as their place allows.
+__device__ __forceinline__ void store4(uint16_t* out, int64_t row, int64_t ld, int n, int N,
+                                       f32x4_t v, bool wide) {
+  uint16_t* p = out + row * ld + n;
+  if (wide && n + 4 <= N) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (n + i < N) p[i] = to_bf16(v[i]);
+}
+
+template <int NT, int MT, int WK, int PF>
+__global__ __launch_bounds__(64 * WK) void f8_stream(F8GemmArgs a) {
+  __shared__ f32x4_t red[WK > 1 ? WK : 1][NT * MT][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane >> 4, col = lane & 15;
+  const int nc = a.n_chunks;
+  const int c_lo = nc * wave / WK, c_hi = nc * (wave + 1) / WK;
+  const bool wide = a.ld % 4 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 7) == 0;
+  const int groups = (a.n_tiles + NT - 1) / NT;
+  const int64_t pitch = (int64_t)nc * kF8Block;
+  int64_t ntok;  // token tiles
+  if (a.kind == kF8Plain) {
+    ntok = (a.a_rows + MT * 16 - 1) / (MT * 16);
+  } else {
+    const int64_t used = max((int64_t)0, min((int64_t)*a.ntpp, a.max_padded));
+    ntok = used / a.block_m;
+  }
+  for (int64_t item = blockIdx.x; item < ntok * groups; item += gridDim.x) {
+    const int ti = (int)(item / groups);
+    const int tile0 = (int)(item % groups) * NT;
+    int e = 0;
+    int64_t row0 = (int64_t)ti * MT * 16;
+    if (a.kind != kF8Plain) {
+      e = a.expert_ids[ti];
+      row0 = (int64_t)ti * a.block_m;
+      if (e < 0 || e >= a.num_experts) continue;  // uniform
+    }
+    // Rows of this lane's tokens; lanes without one read row 0 and store
+    // nothing (their results touch no other token).
+    int64_t src[MT], dst[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int64_t r = row0 + m * 16 + col;
+      src[m] = 0;
+      dst[m] = -1;
+      if (a.kind == kF8Plain) {
+        if (r < a.a_rows) src[m] = dst[m] = r;
+      } else if (m * 16 + col < a.block_m) {
+        const int64_t f = a.sorted_ids[r];
+        if (f >= 0 && f < a.n_flat) {
+          src[m] = a.kind == kF8GateUp ? f / a.topk : r;
+          dst[m] = a.kind == kF8GateUp ? r : f;
+        }
+      }
+    }
+    const uint8_t* wp[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int t = min(tile0 + n, a.n_tiles - 1);
+      wp[n] = a.wq + ((int64_t)e * a.n_tiles + t) * nc * kF8BlockBytes + lane * 16;
+    }
+    // NT divides 8, so the tiles of an item share their block(s) of scales.
+    const float* s0;
+    const float* s1;
+    if (a.kind == kF8GateUp) {
+      s0 = a.ws + ((int64_t)e * a.nb + tile0 / 16) * nc;
+      s1 = s0 + (int64_t)(a.nb / 2) * nc;
+    } else {
+      s0 = s1 = a.ws + ((int64_t)e * a.nb + tile0 / 8) * nc;
+    }
+    const uint8_t* xp[MT];
+    const float* sp[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      xp[m] = a.aq + src[m] * pitch + q * 32;
+      sp[m] = a.as + src[m] * nc;
+    }
+    f32x4_t acc[NT][MT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) acc[n][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+    uint4 w[PF][NT][2], x[PF][MT][2];
+    float sx[PF][MT], sw0[PF], sw1[PF];
+    auto load = [&](int p, int c) {
+      c = min(c, c_hi - 1);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        w[p][n][0] = load_stream(wp[n] + (int64_t)c * kF8BlockBytes);
+        w[p][n][1] = load_stream(wp[n] + (int64_t)c * kF8BlockBytes + 1024);
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        x[p][m][0] = *reinterpret_cast<const uint4*>(xp[m] + c * kF8Block);
+        x[p][m][1] = *reinterpret_cast<const uint4*>(xp[m] + c * kF8Block + 16);
+        sx[p][m] = sp[m][c];
+      }
+      sw0[p] = s0[c];
+      sw1[p] = s1[c];
+    };
+    auto compute = [&](int p) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const i32x8_t av = operand(w[p][n][0], w[p][n][1]);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+          const f32x4_t r = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              av, operand(x[p][m][0], x[p][m][1]), zero, 0, 0, 0, 0, 0, 0);
+          const float f0 = sx[p][m] * sw0[p], f1 = sx[p][m] * sw1[p];
+          acc[n][m][0] = __builtin_fmaf(r[0], f0, acc[n][m][0]);
+          acc[n][m][1] = __builtin_fmaf(r[1], f1, acc[n][m][1]);
+          acc[n][m][2] = __builtin_fmaf(r[2], f0, acc[n][m][2]);
+          acc[n][m][3] = __builtin_fmaf(r[3], f1, acc[n][m][3]);
+        }
+      }
+    };
+    if (c_lo < c_hi) {
+#pragma unroll
+      for (int p = 0; p < PF; ++p) load(p, c_lo + p);
+      for (int c = c_lo; c < c_hi; c += PF) {
+#pragma unroll
+        for (int p = 0; p < PF; ++p) {
+          if (c + p < c_hi) compute(p);
+          load(p, c + p + PF);
+        }
+      }
+    }
+    if (WK > 1) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) red[wave][n * MT + m][lane] = acc[n][m];
+      __syncthreads();
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int j = n * MT + m;
+        if (j % WK != wave) continue;
+        f32x4_t v = acc[n][m];
+        if (WK > 1) {
+          v = red[0][j][lane];
+#pragma unroll
+          for (int u = 1; u < WK; ++u) v += red[u][j][lane];
+        }
+        if (dst[m] < 0 || tile0 + n >= a.n_tiles) continue;
+        if (a.kind == kF8GateUp) {
+          float* h = static_cast<float*>(a.out) + dst[m] * a.ld + (tile0 + n) * 8 + 2 * q;
+          *reinterpret_cast<float2*>(h) = make_float2(silu_mul(v[0], v[1]), silu_mul(v[2], v[3]));
+        } else if (a.kind == kF8Down) {
+          float* y = static_cast<float*>(a.out) + dst[m] * a.ld + (tile0 + n) * 16 + 4 * q;
+          *reinterpret_cast<f32x4_t*>(y) = v;
+        } else {
+          store4(static_cast<uint16_t*>(a.out), dst[m], a.ld, (tile0 + n) * 16 + 4 * q, a.N, v, wide);
+        }
+      }
+    if (WK > 1) __syncthreads();
+  }
+}
+
+}  // namespace
+
+hipError_t launch_f8_gemm(const F8GemmArgs& a, hipStream_t stream) {
+  constexpr int NT = 2, MT = 1, WK = 4, PF = 4;
+  const int64_t tiles = a.kind == kF8Plain ? (a.a_rows + 15) / 16 : a.max_padded / a.block_m + 1;
+  const int64_t items = tiles * ((a.n_tiles + NT - 1) / NT);
+  const int64_t most = (int64_t)a.num_cus * 4;
+  hipLaunchKernelGGL((f8_stream<NT, MT, WK, PF>), dim3((unsigned)(items < most ? items : most)),
+                     dim3(64 * WK), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace chord

@@ -1,0 +1,350 @@
+// Host side of the router and the 8-bit floating point entry points: argument
+// checks (before any HIP call), workspace layout and launch sequences.
+#include <algorithm>
+#include <cmath>
+
+#include "host.h"
+
+using namespace chord;
+
+namespace {
+
+constexpr int kRouteMaxK = 32;
+constexpr int kRouteMaxGroups = 64;
+// Codes of one expert are addressed with 32-bit offsets.
+constexpr int64_t kMaxOperand = ((int64_t)1 << 31) - 1;
+
+bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+chord_status check_shape(int role, int E, int N, int K) {
+  if (role != CHORD_ROLE_GATE_UP && role != CHORD_ROLE_DOWN && role != CHORD_ROLE_PLAIN)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "role %d", role);
+  if (E < 1 || N < 1 || K < 1) return fail(CHORD_ERR_INVALID_ARGUMENT, "E=%d N=%d K=%d", E, N, K);
+  if (role == CHORD_ROLE_PLAIN) {
+    if (E != 1) return fail(CHORD_ERR_UNSUPPORTED, "a plain weight has one matrix, not %d", E);
+  } else {
+    if (E > kMaxExperts) return fail(CHORD_ERR_UNSUPPORTED, "more than %d local experts", kMaxExperts);
+    if (N % kF8Block != 0 || K % kF8Block != 0)
+      return fail(CHORD_ERR_UNSUPPORTED, "N=%d and K=%d must be multiples of 128", N, K);
+    if (role == CHORD_ROLE_GATE_UP && N % (2 * kF8Block) != 0)
+      return fail(CHORD_ERR_UNSUPPORTED, "gate_up N=%d: I must be a multiple of 128", N);
+  }
+  if ((int64_t)f8_tiles(N) * f8_chunks(K) * kF8BlockBytes > kMaxOperand)
+    return fail(CHORD_ERR_UNSUPPORTED, "a weight of [%d, %d] exceeds 2 GiB", N, K);
+  return CHORD_OK;
+}
+
+chord_status check_f8_weight(const chord_f8_weight* w, const char* name, int role) {
+  if (!w) return fail(CHORD_ERR_INVALID_ARGUMENT, "%s is NULL", name);
+  if (w->magic != CHORD_F8_WEIGHT_MAGIC || w->version != CHORD_F8_WEIGHT_VERSION)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "%s is not a packed 8-bit weight handle", name);
+  if (!w->data) return fail(CHORD_ERR_INVALID_ARGUMENT, "%s has no data", name);
+  if (w->role != role)
+    return fail(CHORD_ERR_LAYOUT_MISMATCH, "%s has role %d, expected %d", name, w->role, role);
+  if (w->block != kF8Block) return fail(CHORD_ERR_UNSUPPORTED, "%s block size %d", name, w->block);
+  CHORD_CHECK(check_shape(w->role, w->num_experts, w->n, w->k));
+  if (w->bytes < f8_packed_bytes(w->num_experts, w->n, w->k))
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "%s byte count too small", name);
+  return CHORD_OK;
+}
+
+// The weight's part of a GEMM's arguments.
+F8GemmArgs weight_args(const chord_f8_weight* w, int kind, int cus) {
+  F8GemmArgs g{};
+  g.kind = kind;
+  g.wq = static_cast<const uint8_t*>(w->data);
+  g.ws = reinterpret_cast<const float*>(g.wq + f8_code_bytes(w->num_experts, w->n, w->k));
+  g.n_tiles = (int)f8_tiles(w->n);
+  g.n_chunks = (int)f8_chunks(w->k);
+  g.nb = (w->n + kF8Block - 1) / kF8Block;
+  g.N = w->n;
+  g.num_cus = cus;
+  g.num_experts = w->num_experts;
+  return g;
+}
+
+// ---- layer workspace --------------------------------------------------------
+constexpr int kF8BlockM = 16;  // rows per alignment block
+
+struct F8Ws {
+  size_t align, sorted, experts, ntpp, xq, xs, h, hq, hs, y, total;
+  int64_t max_padded;
+};
+
+F8Ws f8_ws(int T, int k, int E_l, int H, int I) {
+  F8Ws w{};
+  w.max_padded = chord_moe_align_max_padded(T, k, E_l, kF8BlockM);
+  size_t off = 0;
+  auto take = [&](int64_t bytes) {
+    const size_t o = off;
+    off += ((size_t)bytes + 255) & ~(size_t)255;
+    return o;
+  };
+  w.align = take((int64_t)chord_moe_align_workspace_bytes(T, k, E_l, kF8BlockM));
+  w.sorted = take(w.max_padded * 4);
+  w.experts = take((w.max_padded + kF8BlockM - 1) / kF8BlockM * 4);
+  w.ntpp = take(4);
+  w.xq = take((int64_t)T * H);
+  w.xs = take((int64_t)T * f8_chunks(H) * 4);
+  w.h = take(w.max_padded * I * 4);
+  w.hq = take(w.max_padded * I);
+  w.hs = take(w.max_padded * f8_chunks(I) * 4);
+  w.y = take((int64_t)T * k * H * 4);
+  w.total = off;
+  return w;
+}
+
+chord_status check_moe_sizes(int T, int k, int E_l, int H, int I) {
+  if (T < 0 || k < 1 || E_l < 1 || H < 1 || I < 1)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "T=%d k=%d E_l=%d H=%d I=%d", T, k, E_l, H, I);
+  if (H % kF8Block != 0 || I % kF8Block != 0)
+    return fail(CHORD_ERR_UNSUPPORTED, "H=%d and I=%d must be multiples of 128", H, I);
+  if (E_l > kMaxExperts) return fail(CHORD_ERR_UNSUPPORTED, "more than %d local experts", kMaxExperts);
+  const int64_t slots = (int64_t)T * k;
+  if (slots >= (int64_t)1 << 30 || slots * H * 2 > kMaxOperand)
+    return fail(CHORD_ERR_UNSUPPORTED, "T*k*H exceeds 2^30");
+  const int64_t rows = chord_moe_align_max_padded(T, k, E_l, kF8BlockM);
+  if (rows * I > kMaxOperand) return fail(CHORD_ERR_UNSUPPORTED, "rows of h exceed 2 GiB");
+  return CHORD_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+chord_status chord_moe_route(const void* logits, int dtype, int64_t ld, int T, int E,
+                             const float* bias, int k, int scoring, int n_group, int topk_group,
+                             int renormalize, float scaling, int32_t* topk_ids,
+                             float* topk_weights, void* stream) {
+  clear_last_error();
+  if (dtype != CHORD_DTYPE_F32 && dtype != CHORD_DTYPE_BF16 && dtype != CHORD_DTYPE_F16)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "dtype %d", dtype);
+  if (scoring != CHORD_SCORE_SOFTMAX && scoring != CHORD_SCORE_SIGMOID)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "scoring %d", scoring);
+  if (T < 0) return fail(CHORD_ERR_INVALID_ARGUMENT, "T=%d", T);
+  if (E < 1 || E > kMaxExperts)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "E=%d (1..%d)", E, kMaxExperts);
+  if (ld < E) return fail(CHORD_ERR_INVALID_ARGUMENT, "row stride %lld below E=%d", (long long)ld, E);
+  if (n_group < 1 || n_group > kRouteMaxGroups || E % n_group != 0)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "n_group=%d must divide E=%d (1..%d)", n_group, E,
+                kRouteMaxGroups);
+  if (topk_group < 1 || topk_group > n_group)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "topk_group=%d (1..n_group=%d)", topk_group, n_group);
+  if (k < 1 || k > kRouteMaxK || k > topk_group * (E / n_group))
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "k=%d (1..min(%d, %d experts to choose from))", k,
+                kRouteMaxK, topk_group * (E / n_group));
+  if (!std::isfinite(scaling))
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "scaling is not finite");
+  if (T == 0) return CHORD_OK;
+  if (!logits || !topk_ids || !topk_weights)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "null pointer argument");
+  CHORD_CHECK(check_device(nullptr));
+  RouteArgs a{};
+  a.logits = logits;
+  a.dtype = dtype;
+  a.ld = ld;
+  a.T = T;
+  a.E = E;
+  a.k = k;
+  a.bias = bias;
+  a.sigmoid = scoring == CHORD_SCORE_SIGMOID;
+  a.n_group = n_group;
+  a.topk_group = topk_group;
+  const uint32_t per = (uint32_t)(E / n_group);
+  a.group_magic = ((1u << 20) + per - 1) / per;
+  a.renorm = renormalize != 0;
+  a.scaling = scaling;
+  a.ids = topk_ids;
+  a.weights = topk_weights;
+  HIP_TRY(launch_route(a, static_cast<hipStream_t>(stream)), "route launch");
+  return CHORD_OK;
+}
+
+size_t chord_f8_packed_bytes(int role, int E, int N, int K) {
+  clear_last_error();
+  return check_shape(role, E, N, K) == CHORD_OK ? f8_packed_bytes(E, N, K) : 0;
+}
+
+chord_status chord_f8_pack(int role, const chord_f8* codes, const float* scales, int E, int N,
+                           int K, int block, void* dst, size_t dst_bytes,
+                           chord_f8_weight* handle, void* stream) {
+  clear_last_error();
+  if (!codes || !scales || !dst || !handle)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (block != kF8Block)
+    return fail(CHORD_ERR_UNSUPPORTED, "block size %d (only 128 is supported)", block);
+  CHORD_CHECK(check_shape(role, E, N, K));
+  if (!aligned(dst, 16)) return fail(CHORD_ERR_INVALID_ARGUMENT, "dst must be 16-byte aligned");
+  const size_t need = f8_packed_bytes(E, N, K);
+  if (dst_bytes < need)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "dst has %zu bytes, %zu needed", dst_bytes, need);
+  CHORD_CHECK(check_device(nullptr));
+  HIP_TRY(launch_f8_pack(codes, scales, E, N, K, role == CHORD_ROLE_GATE_UP ? 1 : 0,
+                         static_cast<uint8_t*>(dst), static_cast<hipStream_t>(stream)),
+          "8-bit pack launch");
+  *handle = chord_f8_weight{};
+  handle->magic = CHORD_F8_WEIGHT_MAGIC;
+  handle->version = CHORD_F8_WEIGHT_VERSION;
+  handle->role = role;
+  handle->num_experts = E;
+  handle->n = N;
+  handle->k = K;
+  handle->block = kF8Block;
+  handle->data = dst;
+  handle->bytes = need;
+  return CHORD_OK;
+}
+
+chord_status chord_f8_quantize(const chord_bf16* x, int64_t T, int K, int64_t ld, chord_f8* codes,
+                               float* scales, void* stream) {
+  clear_last_error();
+  if (T < 0 || K < 1) return fail(CHORD_ERR_INVALID_ARGUMENT, "T=%lld K=%d", (long long)T, K);
+  if (ld < K)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "row stride %lld below K=%d", (long long)ld, K);
+  if (T == 0) return CHORD_OK;
+  if (T > (int64_t)1 << 40 || K > 1 << 30)
+    return fail(CHORD_ERR_UNSUPPORTED, "T=%lld K=%d", (long long)T, K);
+  if (!x || !codes || !scales) return fail(CHORD_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (!aligned(codes, 16)) return fail(CHORD_ERR_INVALID_ARGUMENT, "codes must be 16-byte aligned");
+  CHORD_CHECK(check_device(nullptr));
+  F8QuantArgs q{};
+  q.x = x;
+  q.T = T;
+  q.ld = ld;
+  q.K = K;
+  q.q = codes;
+  q.s = scales;
+  HIP_TRY(launch_f8_quantize(q, static_cast<hipStream_t>(stream)), "quantize launch");
+  return CHORD_OK;
+}
+
+chord_status chord_f8_gemm(const chord_f8* codes, const float* scales, int64_t M,
+                           const chord_f8_weight* w, chord_bf16* out, int64_t ld, void* stream) {
+  clear_last_error();
+  CHORD_CHECK(check_f8_weight(w, "w", CHORD_ROLE_PLAIN));
+  if (M < 0) return fail(CHORD_ERR_INVALID_ARGUMENT, "M=%lld", (long long)M);
+  if (ld < w->n)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "row stride %lld below N=%d", (long long)ld, w->n);
+  if (M == 0) return CHORD_OK;
+  if (M >= (int64_t)1 << 31) return fail(CHORD_ERR_UNSUPPORTED, "M=%lld", (long long)M);
+  if (!codes || !scales || !out) return fail(CHORD_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (!aligned(codes, 16)) return fail(CHORD_ERR_INVALID_ARGUMENT, "codes must be 16-byte aligned");
+  int cus = 0;
+  CHORD_CHECK(check_device(&cus));
+  F8GemmArgs g = weight_args(w, kF8Plain, cus);
+  g.aq = codes;
+  g.as = scales;
+  g.a_rows = M;
+  g.out = out;
+  g.ld = ld;
+  HIP_TRY(launch_f8_gemm(g, static_cast<hipStream_t>(stream)), "8-bit GEMM launch");
+  return CHORD_OK;
+}
+
+size_t chord_f8_moe_workspace_bytes(int T, int k, int E_l, int H, int I) {
+  clear_last_error();
+  if (check_moe_sizes(T, k, E_l, H, I) != CHORD_OK) return 0;
+  return f8_ws(T, k, E_l, H, I).total;
+}
+
+chord_status chord_f8_moe(const chord_bf16* x, int T, int H, int I, const chord_f8_weight* w13,
+                          const chord_f8_weight* w2, const int32_t* topk_ids,
+                          const float* topk_weights, int k, int expert_begin,
+                          int num_global_experts, chord_bf16* out, void* workspace,
+                          size_t ws_bytes, void* stream) {
+  clear_last_error();
+  CHORD_CHECK(check_f8_weight(w13, "w13", CHORD_ROLE_GATE_UP));
+  CHORD_CHECK(check_f8_weight(w2, "w2", CHORD_ROLE_DOWN));
+  const int E_l = w13->num_experts;
+  CHORD_CHECK(check_moe_sizes(T, k, E_l, H, I));
+  if (w13->n != 2 * I || w13->k != H)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "w13 is [%d,%d], expected [2I=%d, H=%d]", w13->n, w13->k,
+                2 * I, H);
+  if (w2->n != H || w2->k != I)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "w2 is [%d,%d], expected [H=%d, I=%d]", w2->n, w2->k, H, I);
+  if (w2->num_experts != E_l)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "w13 has %d experts, w2 %d", E_l, w2->num_experts);
+  if (T == 0) return CHORD_OK;
+  if (!x || !topk_ids || !topk_weights || !out)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (!aligned(x, 16) || !aligned(out, 16))
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "x and out must be 16-byte aligned");
+  const F8Ws ws = f8_ws(T, k, E_l, H, I);
+  if (!workspace || ws_bytes < ws.total)
+    return fail(CHORD_ERR_WORKSPACE, "workspace %zu bytes, %zu needed", ws_bytes, ws.total);
+  if (!aligned(workspace, 256))
+    return fail(CHORD_ERR_WORKSPACE, "the workspace must be 256-byte aligned");
+  (void)num_global_experts;
+  int cus = 0;
+  CHORD_CHECK(check_device(&cus));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  uint8_t* p = static_cast<uint8_t*>(workspace);
+  int32_t* sorted = reinterpret_cast<int32_t*>(p + ws.sorted);
+  int32_t* experts = reinterpret_cast<int32_t*>(p + ws.experts);
+  int32_t* ntpp = reinterpret_cast<int32_t*>(p + ws.ntpp);
+
+  F8QuantArgs q{};
+  q.x = x;
+  q.T = T;
+  q.ld = H;
+  q.K = H;
+  q.q = p + ws.xq;
+  q.s = reinterpret_cast<float*>(p + ws.xs);
+  HIP_TRY(launch_f8_quantize(q, st), "quantize launch");
+  CHORD_CHECK(chord_moe_align(topk_ids, T, k, expert_begin, E_l, kF8BlockM, sorted, experts, ntpp,
+                              ws.max_padded, p + ws.align,
+                              chord_moe_align_workspace_bytes(T, k, E_l, kF8BlockM), 0, st));
+  auto rows_of = [&](F8GemmArgs& g) {
+    g.sorted_ids = sorted;
+    g.expert_ids = experts;
+    g.ntpp = ntpp;
+    g.block_m = kF8BlockM;
+    g.max_padded = ws.max_padded;
+    g.topk = k;
+    g.n_flat = (int64_t)T * k;
+  };
+  F8GemmArgs g = weight_args(w13, kF8GateUp, cus);
+  rows_of(g);
+  g.aq = q.q;
+  g.as = q.s;
+  g.a_rows = T;
+  g.out = p + ws.h;
+  g.ld = I;
+  HIP_TRY(launch_f8_gemm(g, st), "gate_up launch");
+
+  F8QuantArgs hq{};
+  hq.x = p + ws.h;
+  hq.is_f32 = 1;
+  hq.T = ws.max_padded;
+  hq.rows = ntpp;
+  hq.ld = I;
+  hq.K = I;
+  hq.q = p + ws.hq;
+  hq.s = reinterpret_cast<float*>(p + ws.hs);
+  HIP_TRY(launch_f8_quantize(hq, st), "quantize launch");
+
+  F8GemmArgs d = weight_args(w2, kF8Down, cus);
+  rows_of(d);
+  d.aq = hq.q;
+  d.as = hq.s;
+  d.a_rows = ws.max_padded;
+  d.out = p + ws.y;
+  d.ld = H;
+  HIP_TRY(launch_f8_gemm(d, st), "down launch");
+
+  F8CombineArgs c{};
+  c.y = reinterpret_cast<const float*>(p + ws.y);
+  c.topk_ids = topk_ids;
+  c.topk_weights = topk_weights;
+  c.T = T;
+  c.k = k;
+  c.H = H;
+  c.expert_begin = expert_begin;
+  c.num_experts = E_l;
+  c.out = reinterpret_cast<uint16_t*>(out);
+  HIP_TRY(launch_f8_combine(c, st), "combine launch");
+  set_last_plan("f8 moe: streaming GEMMs");
+  return CHORD_OK;
+}
+
+}  // extern "C"

@@ -224,6 +224,96 @@ struct DispatchArgs {
   int32_t* flat_to_row;       // [T * k]
 };
 
+// ---------------------------------------------------------------------------
+// Packed 8-bit weight layout (gfx950).
+//
+// A weight [E, N, K] is cut into 16-row tiles and 128-wide K chunks (both
+// padded with zero codes).  Each (expert, tile, chunk) is one 2048-byte block,
+// tile-major, in the operand order of v_mfma_f32_16x16x128_f8f6f4: piece h
+// (1 KB), lane l, 16 bytes: tile row r = l % 16, k = chunk * 128 +
+// (l / 16) * 32 + 16 h + [0, 16).  A wave streaming a tile along K reads
+// contiguous memory, and a block copied to LDS as it is gives operand reads
+// without bank conflicts.  The block scales, fp32 [E, ceil(N / 128), chunks],
+// follow the codes.
+//
+// Gate_up weights interleave gate and up rows as the 4-bit layout does: tile t,
+// row r = 4q + w holds feature f = 8t + 2q + (w >> 1); w even = gate row f,
+// w odd = up row I + f.  16 tiles then hold one block of 128 features, gate and
+// up, so one workgroup can quantise that block of h.
+// ---------------------------------------------------------------------------
+constexpr int kF8Block = 128;
+constexpr int kF8BlockBytes = kTileRows * kF8Block;
+__host__ __device__ inline int64_t f8_tiles(int N) { return (N + kTileRows - 1) / kTileRows; }
+__host__ __device__ inline int64_t f8_chunks(int K) { return (K + kF8Block - 1) / kF8Block; }
+__host__ __device__ inline size_t f8_code_bytes(int E, int N, int K) {
+  return (size_t)E * f8_tiles(N) * f8_chunks(K) * kF8BlockBytes;
+}
+inline size_t f8_packed_bytes(int E, int N, int K) {
+  return f8_code_bytes(E, N, K) +
+         (size_t)E * ((N + kF8Block - 1) / kF8Block) * f8_chunks(K) * sizeof(float);
+}
+
+struct RouteArgs {
+  const void* logits;  // [T, ld]
+  int dtype;           // chord_dtype
+  int64_t ld;
+  int T, E, k;
+  const float* bias;   // [E] or null
+  int sigmoid;
+  int n_group, topk_group;
+  uint32_t group_magic;  // ceil(2^20 / (E / n_group)): expert -> group for e < 1024
+  int renorm;
+  float scaling;
+  int32_t* ids;
+  float* weights;
+};
+
+struct F8QuantArgs {
+  const void* x;    // bf16 or fp32 [T, ld]
+  int is_f32;
+  int64_t T, ld;
+  int K;
+  const int32_t* rows;  // device row count (<= T), or null: T
+  uint8_t* q;       // [T, chunks * 128]
+  float* s;         // [T, chunks]
+};
+
+// Arguments of one 8-bit GEMM launch.
+enum F8Kind : int { kF8Plain = 0, kF8GateUp = 1, kF8Down = 2 };
+struct F8GemmArgs {
+  int kind;
+  const uint8_t* wq;   // packed codes
+  const float* ws;     // block scales [E, nb, n_chunks]
+  int n_tiles, n_chunks, nb;
+  int N;               // output columns (plain, down) / rows of the weight
+  const uint8_t* aq;   // activation codes [a_rows, n_chunks * 128]
+  const float* as;     // activation scales [a_rows, n_chunks]
+  int64_t a_rows;
+  int num_cus;
+  // gate_up, down: one token tile per alignment block
+  const int32_t* sorted_ids;
+  const int32_t* expert_ids;
+  const int32_t* ntpp;
+  int block_m;
+  int64_t max_padded;
+  int num_experts;
+  int topk;
+  int64_t n_flat;
+  // output: bf16 [*, ld] by row (plain), fp32 h [rows, ld] by aligned row
+  // (gate_up), fp32 y [slots, ld] by flat slot (down)
+  void* out;
+  int64_t ld;
+};
+
+struct F8CombineArgs {
+  const float* y;           // [T * k, H], rows of local slots
+  const int32_t* topk_ids;  // [T, k]
+  const float* topk_weights;
+  int T, k, H;
+  int expert_begin, num_experts;
+  uint16_t* out;            // bf16 [T, H]
+};
+
 // Launchers (defined in the .hip files).  All enqueue on `stream` and return
 // hipSuccess or the launch error.
 hipError_t launch_pack(const int32_t* q, const uint16_t* s, int E, int N, int K, int gate_up,
@@ -249,6 +339,12 @@ hipError_t launch_combine(const CombineArgs& a, hipStream_t stream);
 hipError_t launch_gather_contiguous(const DispatchArgs& a, hipStream_t stream);
 hipError_t launch_gather_masked(const DispatchArgs& a, hipStream_t stream);
 hipError_t launch_zero(uint16_t* p, int64_t n, hipStream_t stream);
+hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
+hipError_t launch_f8_pack(const uint8_t* q, const float* s, int E, int N, int K, int gate_up,
+                          uint8_t* dst, hipStream_t stream);
+hipError_t launch_f8_quantize(const F8QuantArgs& a, hipStream_t stream);
+hipError_t launch_f8_gemm(const F8GemmArgs& a, hipStream_t stream);
+hipError_t launch_f8_combine(const F8CombineArgs& a, hipStream_t stream);
 
 constexpr int kAlignSingle = 8192;      // align in one workgroup up to this many entries
 constexpr int kAlignMinChunk = 1024;    // entries per align workgroup (at least)

@@ -16,7 +16,7 @@
 #include <unordered_map>
 #include <vector>
 
-#include "internal.h"
+#include "host.h"
 
 using namespace chord;
 
@@ -24,6 +24,19 @@ namespace {
 
 thread_local std::string g_last_error;
 thread_local std::string g_last_plan;
+
+struct DeviceInfo {
+  bool checked = false;
+  bool ok = false;
+  int cus = 0;
+  char arch[64] = {0};
+};
+std::mutex g_dev_mu;
+DeviceInfo g_dev[64];
+
+}  // namespace
+
+namespace chord {
 
 chord_status fail(chord_status s, const char* fmt, ...) {
   char buf[512];
@@ -39,27 +52,9 @@ chord_status hip_fail(hipError_t e, const char* what) {
   return fail(CHORD_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-#define CHORD_CHECK(expr)                    \
-  do {                                       \
-    chord_status _s = (expr);                \
-    if (_s != CHORD_OK) return _s;           \
-  } while (0)
+void clear_last_error() { g_last_error.clear(); }
 
-#define HIP_TRY(expr, what)                       \
-  do {                                            \
-    hipError_t _e = (expr);                       \
-    if (_e != hipSuccess) return hip_fail(_e, what); \
-  } while (0)
-
-// ---- device check ---------------------------------------------------------
-struct DeviceInfo {
-  bool checked = false;
-  bool ok = false;
-  int cus = 0;
-  char arch[64] = {0};
-};
-std::mutex g_dev_mu;
-DeviceInfo g_dev[64];
+void set_last_plan(const char* text) { g_last_plan = text; }
 
 chord_status check_device(int* cus) {
   int dev = 0;
@@ -81,6 +76,10 @@ chord_status check_device(int* cus) {
   if (cus) *cus = d.cus;
   return CHORD_OK;
 }
+
+}  // namespace chord
+
+namespace {
 
 // ---- environment overrides (parsed once) ----------------------------------
 struct EnvOverrides {

@@ -82,3 +82,48 @@ class W4A16MoE:
         return C.chord_w4a16_moe_grouped_masked(a3, masked_m, expected_m, self.w13, self.w2,
                                                 row_weights, out, workspace=ws, flags=flags,
                                                 stream=stream)
+
+
+class W8A8MoE:
+    """One GPU's share of a W8A8 MoE layer (e4m3 codes, fp32 block scales).
+
+    q13: float8_e4m3fn [E_l, 2I, H], s13: fp32 [E_l, 2I/128, H/128] (gate rows first)
+    q2:  float8_e4m3fn [E_l, H, I],  s2:  fp32 [E_l, H/128, I/128]
+    Activations are quantised inside the call, one scale for each 128 columns
+    of a row.  Scratch memory is taken from torch's allocator call by call, so
+    one layer may serve several streams and captured graphs.
+    """
+
+    def __init__(self, q13, s13, q2, s2):
+        self.E_l, n13, self.H = q13.shape
+        self.I = n13 // 2
+        self.w13 = C.chord_f8_pack(C.ROLE_GATE_UP, q13, s13)
+        self.w2 = C.chord_f8_pack(C.ROLE_DOWN, q2, s2)
+
+    def indexed(self, x, topk_ids, topk_weights, expert_begin=0, num_global_experts=0, out=None,
+                workspace=None, stream=None):
+        return C.chord_f8_moe(x, self.w13, self.w2, topk_ids, topk_weights, expert_begin,
+                              num_global_experts, out=out, workspace=workspace, stream=stream)
+
+    def routed(self, x, logits, k, expert_begin=0, stream=None, out=None, **routing):
+        """The layer behind its router: `logits` [T, E_global] choose the experts
+        (`routing`: the arguments of chord_moe_route)."""
+        ids, weights = C.chord_moe_route(logits, k, stream=stream, **routing)
+        return self.indexed(x, ids, weights, expert_begin, logits.shape[1], out=out, stream=stream)
+
+
+class F8Linear:
+    """y = x W^T with an 8-bit weight: codes float8_e4m3fn [N, K], scales fp32
+    [ceil(N/128), ceil(K/128)].  x bf16 [M, K] is quantised for the call; to
+    use one quantised x with several weights, call chord_f8_quantize and
+    chord_f8_gemm."""
+
+    def __init__(self, codes, scales):
+        self.N, self.K = codes.shape
+        self.w = C.chord_f8_pack(C.ROLE_PLAIN, codes.unsqueeze(0), scales.unsqueeze(0))
+
+    def __call__(self, x, out=None, stream=None):
+        if x.dim() != 2 or x.shape[1] != self.K:
+            raise C.ChordError(1, f"x must be [M, {self.K}], not {list(x.shape)}")
+        q, s = C.chord_f8_quantize(x, stream=stream)
+        return C.chord_f8_gemm(q, s, self.w, out=out, stream=stream)
