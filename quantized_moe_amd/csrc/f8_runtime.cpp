@@ -14,6 +14,10 @@ constexpr int kRouteMaxGroups = 64;
 // Codes of one expert are addressed with 32-bit offsets.
 constexpr int64_t kMaxOperand = ((int64_t)1 << 31) - 1;
 
+// Rows (of the product; of an expert on average) from which the LDS-tiled
+// kernel takes over from the streaming one.
+constexpr int kTileMinRows = 64;
+
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 chord_status check_shape(int role, int E, int N, int K) {
@@ -29,6 +33,7 @@ chord_status check_shape(int role, int E, int N, int K) {
     if (role == CHORD_ROLE_GATE_UP && N % (2 * kF8Block) != 0)
       return fail(CHORD_ERR_UNSUPPORTED, "gate_up N=%d: I must be a multiple of 128", N);
   }
+  if (K > 1 << 22) return fail(CHORD_ERR_UNSUPPORTED, "K=%d above 2^22", K);
   if ((int64_t)f8_tiles(N) * f8_chunks(K) * kF8BlockBytes > kMaxOperand)
     return fail(CHORD_ERR_UNSUPPORTED, "a weight of [%d, %d] exceeds 2 GiB", N, K);
   return CHORD_OK;
@@ -67,8 +72,9 @@ F8GemmArgs weight_args(const chord_f8_weight* w, int kind, int cus) {
 constexpr int kF8BlockM = 16;  // rows per alignment block
 
 struct F8Ws {
-  size_t align, sorted, experts, ntpp, xq, xs, h, hq, hs, y, total;
+  size_t align, sorted, experts, ntpp, status, tiles, xq, xs, h, hq, hs, y, total;
   int64_t max_padded;
+  int max_tiles;
 };
 
 F8Ws f8_ws(int T, int k, int E_l, int H, int I) {
@@ -84,6 +90,9 @@ F8Ws f8_ws(int T, int k, int E_l, int H, int I) {
   w.sorted = take(w.max_padded * 4);
   w.experts = take((w.max_padded + kF8BlockM - 1) / kF8BlockM * 4);
   w.ntpp = take(4);
+  w.status = take(sizeof(DevStatus));
+  w.max_tiles = (int)(w.max_padded / kF8TileRows) + E_l + 1;
+  w.tiles = take(w.max_tiles * sizeof(TileDesc));
   w.xq = take((int64_t)T * H);
   w.xs = take((int64_t)T * f8_chunks(H) * 4);
   w.h = take(w.max_padded * I * 4);
@@ -237,7 +246,8 @@ chord_status chord_f8_gemm(const chord_f8* codes, const float* scales, int64_t M
   g.a_rows = M;
   g.out = out;
   g.ld = ld;
-  HIP_TRY(launch_f8_gemm(g, static_cast<hipStream_t>(stream)), "8-bit GEMM launch");
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  HIP_TRY(M >= kTileMinRows ? launch_f8_tile(g, st) : launch_f8_gemm(g, st), "8-bit GEMM launch");
   return CHORD_OK;
 }
 
@@ -303,34 +313,64 @@ chord_status chord_f8_moe(const chord_bf16* x, int T, int H, int I, const chord_
     g.topk = k;
     g.n_flat = (int64_t)T * k;
   };
+  // Expected rows per expert pick the kernel.
+  const int eg = num_global_experts > E_l ? num_global_experts : E_l;
+  const bool tiled = (double)T * k / eg >= kTileMinRows;
+  if (tiled) {
+    TileBuildArgs tb{};
+    tb.layout = kIndexed;
+    tb.num_experts = E_l;
+    tb.tile_tokens = kF8BlockM;
+    tb.big_tokens = kF8TileRows;
+    tb.max_tiles_b = ws.max_tiles;
+    tb.max_ksplit = 2;
+    tb.expert_ids = experts;
+    tb.ntpp = ntpp;
+    tb.block_m = kF8BlockM;
+    tb.max_padded = ws.max_padded;
+    tb.tiles_b = reinterpret_cast<TileDesc*>(p + ws.tiles);
+    tb.status = reinterpret_cast<DevStatus*>(p + ws.status);
+    HIP_TRY(launch_build_tiles(tb, st), "tile builder launch");
+  }
   F8GemmArgs g = weight_args(w13, kF8GateUp, cus);
   rows_of(g);
   g.aq = q.q;
   g.as = q.s;
   g.a_rows = T;
-  g.out = p + ws.h;
   g.ld = I;
-  HIP_TRY(launch_f8_gemm(g, st), "gate_up launch");
-
-  F8QuantArgs hq{};
-  hq.x = p + ws.h;
-  hq.is_f32 = 1;
-  hq.T = ws.max_padded;
-  hq.rows = ntpp;
-  hq.ld = I;
-  hq.K = I;
-  hq.q = p + ws.hq;
-  hq.s = reinterpret_cast<float*>(p + ws.hs);
-  HIP_TRY(launch_f8_quantize(hq, st), "quantize launch");
+  g.tiles = reinterpret_cast<const TileDesc*>(p + ws.tiles);
+  g.status = reinterpret_cast<const DevStatus*>(p + ws.status);
+  uint8_t* hq = p + ws.hq;
+  float* hs = reinterpret_cast<float*>(p + ws.hs);
+  if (tiled) {
+    g.out = hq;
+    g.hs = hs;
+    HIP_TRY(launch_f8_tile(g, st), "gate_up launch");
+  } else {
+    g.out = p + ws.h;
+    HIP_TRY(launch_f8_gemm(g, st), "gate_up launch");
+    F8QuantArgs qh{};
+    qh.x = p + ws.h;
+    qh.is_f32 = 1;
+    qh.T = ws.max_padded;
+    qh.rows = ntpp;
+    qh.ld = I;
+    qh.K = I;
+    qh.q = hq;
+    qh.s = hs;
+    HIP_TRY(launch_f8_quantize(qh, st), "quantize launch");
+  }
 
   F8GemmArgs d = weight_args(w2, kF8Down, cus);
   rows_of(d);
-  d.aq = hq.q;
-  d.as = hq.s;
+  d.aq = hq;
+  d.as = hs;
   d.a_rows = ws.max_padded;
+  d.tiles = g.tiles;
+  d.status = g.status;
   d.out = p + ws.y;
   d.ld = H;
-  HIP_TRY(launch_f8_gemm(d, st), "down launch");
+  HIP_TRY(tiled ? launch_f8_tile(d, st) : launch_f8_gemm(d, st), "down launch");
 
   F8CombineArgs c{};
   c.y = reinterpret_cast<const float*>(p + ws.y);
@@ -343,7 +383,7 @@ chord_status chord_f8_moe(const chord_bf16* x, int T, int H, int I, const chord_
   c.num_experts = E_l;
   c.out = reinterpret_cast<uint16_t*>(out);
   HIP_TRY(launch_f8_combine(c, st), "combine launch");
-  set_last_plan("f8 moe: streaming GEMMs");
+  set_last_plan(tiled ? "f8 moe: tiled GEMMs" : "f8 moe: streaming GEMMs");
   return CHORD_OK;
 }
 

@@ -279,6 +279,7 @@ struct F8QuantArgs {
 };
 
 // Arguments of one 8-bit GEMM launch.
+constexpr int kF8TileRows = 256;  // tokens per workgroup of the tiled kernel
 enum F8Kind : int { kF8Plain = 0, kF8GateUp = 1, kF8Down = 2 };
 struct F8GemmArgs {
   int kind;
@@ -299,10 +300,15 @@ struct F8GemmArgs {
   int num_experts;
   int topk;
   int64_t n_flat;
-  // output: bf16 [*, ld] by row (plain), fp32 h [rows, ld] by aligned row
-  // (gate_up), fp32 y [slots, ld] by flat slot (down)
+  // tiled kernel: tiles of at most kF8TileRows rows
+  const TileDesc* tiles;
+  const DevStatus* status;
+  // output: bf16 [*, ld] by row (plain); h by aligned row (gate_up: fp32
+  // [rows, ld], or from the tiled kernel codes [rows, ld] and scales hs
+  // [rows, ld / 128]); fp32 y [slots, ld] by flat slot (down)
   void* out;
   int64_t ld;
+  float* hs;
 };
 
 struct F8CombineArgs {
@@ -344,6 +350,7 @@ hipError_t launch_f8_pack(const uint8_t* q, const float* s, int E, int N, int K,
                           uint8_t* dst, hipStream_t stream);
 hipError_t launch_f8_quantize(const F8QuantArgs& a, hipStream_t stream);
 hipError_t launch_f8_gemm(const F8GemmArgs& a, hipStream_t stream);
+hipError_t launch_f8_tile(const F8GemmArgs& a, hipStream_t stream);
 hipError_t launch_f8_combine(const F8CombineArgs& a, hipStream_t stream);
 
 constexpr int kAlignSingle = 8192;      // align in one workgroup up to this many entries
