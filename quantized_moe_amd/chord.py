@@ -8,7 +8,6 @@ library is missing this module raises on import -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from typing import Optional
 
@@ -398,58 +397,68 @@ def chord_moe_combine(rows, flat_to_row, topk_weights, out=None, stream=None):
 # These wrappers check types, shapes, layouts and devices (the C ABI sees only
 # addresses), run on the device of their first tensor whichever is current, and
 # take scratch memory and outputs from torch's allocator on the stream they run
-# on, call by call: two calls, streams or captured graphs share no memory.
+# on, call by call: two calls, streams or captured graphs share no memory.  The
+# smallest calls are bound by this code, so the checks are plain comparisons and
+# a message is only made where one fails.
 # ---------------------------------------------------------------------------
 
-def _require(ok: bool, what: str):
-    if not ok:
-        raise ChordError(1, what)
-
-
-def _tensor(t, name: str, dtype, shape, device, contiguous: bool = True):
-    _require(isinstance(t, torch.Tensor), f"{name} must be a tensor")
-    _require(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
-    _require(tuple(t.shape) == tuple(shape), f"{name} must be {list(shape)}, not {list(t.shape)}")
-    _require(t.device == device, f"{name} is on {t.device}, expected {device}")
-    _require(not contiguous or t.is_contiguous(), f"{name} must be contiguous")
-
-
-def _rows(t, name: str, dtypes):
-    """A device matrix whose rows are contiguous; returns its row stride."""
-    _require(isinstance(t, torch.Tensor) and t.is_cuda, f"{name} must be a tensor on the GPU")
-    _require(t.dtype in dtypes, f"{name} has type {t.dtype}")
-    _require(t.dim() == 2, f"{name} must have two dimensions")
-    T, K = t.shape
-    _require(K >= 1, f"{name} has no columns")
-    _require(K == 1 or T == 0 or t.stride(1) == 1, f"{name} must have contiguous rows")
-    ld = t.stride(0) if T > 1 else K
-    _require(ld >= K, f"{name} has overlapping rows")
-    return ld
-
-
-def _on_device(fn):
-    """Runs fn(first, ..., stream) on the device of its first tensor and on
-    `stream`: a raw handle is passed on, and what fn allocates belongs to it."""
-    @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
-        _require(isinstance(first, torch.Tensor) and first.is_cuda, "the first tensor must be on the GPU")
-        dev = first.device
-        if stream is not None:
-            _require(stream.device == dev, f"the stream is on {stream.device}, the tensors on {dev}")
-            with torch.cuda.stream(stream):
-                return fn(first, *args, stream=stream.cuda_stream, **kw)
-        if dev.index != torch.cuda.current_device():
-            with torch.cuda.device(dev):
-                return fn(first, *args, stream=torch.cuda.current_stream().cuda_stream, **kw)
-        return fn(first, *args, stream=torch.cuda.current_stream().cuda_stream, **kw)
-    return call
-
-
+_raw_stream = torch._C._cuda_getCurrentRawStream  # (device index) -> hipStream_t
+_current_device = torch.cuda.current_device
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_F32, _BF16, _F8, _I32 = torch.float32, torch.bfloat16, torch.float8_e4m3fn, torch.int32
 F8_BLOCK = 128
 
 
-@_on_device
+def _refuse(what: str):
+    raise ChordError(1, what)
+
+
+def _elsewhere(fn, t, stream, **kw):
+    """fn(t, ...) on the device of t and on `stream` (None: its current one); what
+    fn allocates then belongs to that stream."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _refuse("the first tensor must be on the GPU")
+    if stream is None:
+        with torch.cuda.device(t.device):
+            return fn(t, **kw)
+    if stream.device != t.device:
+        _refuse(f"the stream is on {stream.device}, the tensors are on {t.device}")
+    with torch.cuda.stream(stream):
+        return fn(t, **kw)
+
+
+def _away(t, stream) -> bool:
+    if stream is not None or not isinstance(t, torch.Tensor) or not t.is_cuda:
+        return True
+    return t.get_device() != _current_device()
+
+
+def _tensor(t, name: str, dtype, shape, device: int, contiguous: bool = True):
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape
+            or t.get_device() != device or (contiguous and not t.is_contiguous())):
+        if not isinstance(t, torch.Tensor):
+            _refuse(f"{name} must be a tensor")
+        if t.get_device() != device:
+            _refuse(f"{name} is on {t.device}, expected GPU {device}")
+        _refuse(f"{name} must be {'contiguous ' if contiguous else ''}{dtype} {list(shape)}, not "
+                f"{t.dtype} {list(t.shape)} with strides {list(t.stride())}")
+
+
+def _row_stride(t, name: str) -> int:
+    """Row stride of a matrix whose rows are contiguous."""
+    if t.dim() != 2 or t.shape[1] < 1:
+        _refuse(f"{name} must be a matrix, not {list(t.shape)}")
+    T, K = t.shape
+    if t.is_contiguous():
+        return K
+    ld, one = t.stride()
+    if T <= 1:
+        ld = K
+    if (one != 1 and K > 1) or ld < K:
+        _refuse(f"{name} must have contiguous rows that do not overlap, not strides {list(t.stride())}")
+    return ld
+
+
 def chord_moe_route(logits, k: int, scoring: int = SCORE_SOFTMAX, bias=None, n_group: int = 1,
                     topk_group: int = 1, renormalize: bool = True, scaling: float = 1.0, out=None,
                     stream=None):
@@ -457,23 +466,33 @@ def chord_moe_route(logits, k: int, scoring: int = SCORE_SOFTMAX, bias=None, n_g
     be strided) and their weights: (topk_ids int32 [T, k], topk_weights fp32
     [T, k]).  Experts with a logit or bias of -inf or NaN are not available;
     slots without an expert get id -1 and weight 0."""
-    ld = _rows(logits, "logits", _DTYPES)
+    if _away(logits, stream):
+        return _elsewhere(chord_moe_route, logits, stream, k=k, scoring=scoring, bias=bias,
+                          n_group=n_group, topk_group=topk_group, renormalize=renormalize,
+                          scaling=scaling, out=out)
+    dtype = _DTYPES.get(logits.dtype)
+    if dtype is None:
+        _refuse(f"logits have type {logits.dtype}")
+    ld = _row_stride(logits, "logits")
     T, E = logits.shape
-    dev = logits.device
+    dev = logits.get_device()
     if bias is not None:
-        _tensor(bias, "bias", torch.float32, (E,), dev)
-    _require(1 <= k <= 32, f"k={k} (1..32)")
+        _tensor(bias, "bias", _F32, (E,), dev)
+    if not 1 <= k <= 32:
+        _refuse(f"k={k} (1..32)")
     if out is None:
-        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
-        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+        ids = torch.empty((T, k), dtype=_I32, device=dev)
+        weights = torch.empty((T, k), dtype=_F32, device=dev)
     else:
         ids, weights = out
-        _tensor(ids, "topk_ids", torch.int32, (T, k), dev)
-        _tensor(weights, "topk_weights", torch.float32, (T, k), dev)
-    _check(lib.chord_moe_route(logits.data_ptr(), _DTYPES[logits.dtype], ld, T, E,
-                               None if bias is None else bias.data_ptr(), k, scoring, n_group,
-                               topk_group, renormalize, scaling, ids.data_ptr(), weights.data_ptr(),
-                               stream))
+        _tensor(ids, "topk_ids", _I32, (T, k), dev)
+        _tensor(weights, "topk_weights", _F32, (T, k), dev)
+    st = lib.chord_moe_route(logits.data_ptr(), dtype, ld, T, E,
+                             None if bias is None else bias.data_ptr(), k, scoring, n_group,
+                             topk_group, renormalize, scaling, ids.data_ptr(), weights.data_ptr(),
+                             _raw_stream(dev))
+    if st:
+        _check(st)
     return ids, weights
 
 
@@ -484,10 +503,15 @@ class F8PackedWeight:
         self.handle = handle
         self.ref = ctypes.byref(handle)
         self.buf = buf
+        self.num_experts, self.n, self.k = handle.num_experts, handle.n, handle.k
+        self.device = buf.get_device()
 
-    @property
-    def num_experts(self):
-        return self.handle.num_experts
+
+def _weight(w, name: str, device: int):
+    if not isinstance(w, F8PackedWeight):
+        _refuse(f"{name} must be a packed 8-bit weight")
+    if w.device != device:
+        _refuse(f"{name} is on GPU {w.device}, expected {device}")
 
 
 def chord_f8_packed_bytes(role: int, E: int, N: int, K: int) -> int:
@@ -496,59 +520,68 @@ def chord_f8_packed_bytes(role: int, E: int, N: int, K: int) -> int:
 
 def chord_f8_pack(role: int, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> F8PackedWeight:
     """codes float8_e4m3fn [E, N, K], scales fp32 [E, ceil(N/128), ceil(K/128)]."""
-    return _f8_pack(codes, scales, role, stream=stream)
-
-
-@_on_device
-def _f8_pack(codes, scales, role, stream=None):
-    _require(codes.dim() == 3, "codes must be [E, N, K]")
+    if _away(codes, stream):
+        return _elsewhere(lambda t: chord_f8_pack(role, t, scales), codes, stream)
+    if codes.dim() != 3:
+        _refuse(f"codes must be [E, N, K], not {list(codes.shape)}")
     E, N, K = codes.shape
-    _tensor(codes, "codes", torch.float8_e4m3fn, (E, N, K), codes.device)
-    _tensor(scales, "scales", torch.float32, (E, -(-N // F8_BLOCK), -(-K // F8_BLOCK)), codes.device)
+    dev = codes.get_device()
+    _tensor(codes, "codes", _F8, (E, N, K), dev)
+    _tensor(scales, "scales", _F32, (E, -(-N // F8_BLOCK), -(-K // F8_BLOCK)), dev)
     nbytes = lib.chord_f8_packed_bytes(role, E, N, K)
-    buf = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=codes.device)
+    buf = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
     h = F8Weight()
     _check(lib.chord_f8_pack(role, codes.data_ptr(), scales.data_ptr(), E, N, K, F8_BLOCK,
-                             buf.data_ptr(), nbytes, ctypes.byref(h), stream))
+                             buf.data_ptr(), nbytes, ctypes.byref(h), _raw_stream(dev)))
     return F8PackedWeight(h, buf)
 
 
-@_on_device
 def chord_f8_quantize(x, out=None, stream=None):
     """Codes float8_e4m3fn [T, ceil(K/128)*128] and scales fp32 [T, ceil(K/128)] of
     the bf16 rows x [T, K] (rows may be strided)."""
-    ld = _rows(x, "x", (torch.bfloat16,))
+    if _away(x, stream):
+        return _elsewhere(chord_f8_quantize, x, stream, out=out)
+    if x.dtype is not _BF16:
+        _refuse(f"x has type {x.dtype}, expected bfloat16")
+    ld = _row_stride(x, "x")
     T, K = x.shape
     groups = -(-K // F8_BLOCK)
+    dev = x.get_device()
     if out is None:
-        q = torch.empty((T, groups * F8_BLOCK), dtype=torch.float8_e4m3fn, device=x.device)
-        s = torch.empty((T, groups), dtype=torch.float32, device=x.device)
+        q = torch.empty((T, groups * F8_BLOCK), dtype=_F8, device=dev)
+        s = torch.empty((T, groups), dtype=_F32, device=dev)
     else:
         q, s = out
-        _tensor(q, "codes", torch.float8_e4m3fn, (T, groups * F8_BLOCK), x.device)
-        _tensor(s, "scales", torch.float32, (T, groups), x.device)
-    _check(lib.chord_f8_quantize(x.data_ptr(), T, K, ld, q.data_ptr(), s.data_ptr(), stream))
+        _tensor(q, "codes", _F8, (T, groups * F8_BLOCK), dev)
+        _tensor(s, "scales", _F32, (T, groups), dev)
+    st = lib.chord_f8_quantize(x.data_ptr(), T, K, ld, q.data_ptr(), s.data_ptr(), _raw_stream(dev))
+    if st:
+        _check(st)
     return q, s
 
 
-@_on_device
 def chord_f8_gemm(codes, scales, w: F8PackedWeight, out=None, stream=None):
     """bf16 [M, N]: chord_f8_quantize's (codes, scales) times the packed weight
     [N, K].  `out` may have strided rows."""
-    _require(isinstance(w, F8PackedWeight), "w must be a packed 8-bit weight")
-    _require(codes.dim() == 2, "codes must have two dimensions")
-    M = codes.shape[0]
-    N, groups = w.handle.n, -(-w.handle.k // F8_BLOCK)
-    _tensor(codes, "codes", torch.float8_e4m3fn, (M, groups * F8_BLOCK), codes.device)
-    _tensor(scales, "scales", torch.float32, (M, groups), codes.device)
-    _require(w.buf.device == codes.device, f"w is on {w.buf.device}, codes on {codes.device}")
+    if _away(codes, stream):
+        return _elsewhere(chord_f8_gemm, codes, stream, scales=scales, w=w, out=out)
+    dev = codes.get_device()
+    _weight(w, "w", dev)
+    if codes.dim() != 2:
+        _refuse(f"codes must be a matrix, not {list(codes.shape)}")
+    M, N, groups = codes.shape[0], w.n, -(-w.k // F8_BLOCK)
+    _tensor(codes, "codes", _F8, (M, groups * F8_BLOCK), dev)
+    _tensor(scales, "scales", _F32, (M, groups), dev)
+    ld = N
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=codes.device)
-        ld = N
+        out = torch.empty((M, N), dtype=_BF16, device=dev)
     else:
-        ld = _rows(out, "out", (torch.bfloat16,))
-        _tensor(out, "out", torch.bfloat16, (M, N), codes.device, contiguous=False)
-    _check(lib.chord_f8_gemm(codes.data_ptr(), scales.data_ptr(), M, w.ref, out.data_ptr(), ld, stream))
+        _tensor(out, "out", _BF16, (M, N), dev, contiguous=False)
+        ld = _row_stride(out, "out")
+    st = lib.chord_f8_gemm(codes.data_ptr(), scales.data_ptr(), M, w.ref, out.data_ptr(), ld,
+                           _raw_stream(dev))
+    if st:
+        _check(st)
     return out
 
 
@@ -556,34 +589,36 @@ def chord_f8_moe_workspace_bytes(T: int, k: int, E_l: int, H: int, I: int) -> in
     return lib.chord_f8_moe_workspace_bytes(T, k, E_l, H, I)
 
 
-@_on_device
 def chord_f8_moe(x, w13: F8PackedWeight, w2: F8PackedWeight, topk_ids, topk_weights,
                  expert_begin: int = 0, num_global_experts: int = 0, out=None, workspace=None,
                  stream=None):
     """The W8A8 layer over this GPU's experts: bf16 [T, H]."""
-    _require(isinstance(w13, F8PackedWeight) and isinstance(w2, F8PackedWeight),
-             "w13 and w2 must be packed 8-bit weights")
-    dev = x.device
-    _require(x.dim() == 2, "x must have two dimensions")
-    T, H = x.shape
-    _tensor(x, "x", torch.bfloat16, (T, w13.handle.k), dev)
-    _require(topk_ids.dim() == 2, "topk_ids must have two dimensions")
-    k = topk_ids.shape[1]
-    _tensor(topk_ids, "topk_ids", torch.int32, (T, k), dev)
-    _tensor(topk_weights, "topk_weights", torch.float32, (T, k), dev)
-    _require(w13.buf.device == dev and w2.buf.device == dev, f"the weights must be on {dev}")
-    I = w2.handle.k
+    if _away(x, stream):
+        return _elsewhere(chord_f8_moe, x, stream, w13=w13, w2=w2, topk_ids=topk_ids,
+                          topk_weights=topk_weights, expert_begin=expert_begin,
+                          num_global_experts=num_global_experts, out=out, workspace=workspace)
+    dev = x.get_device()
+    _weight(w13, "w13", dev)
+    _weight(w2, "w2", dev)
+    if x.dim() != 2 or not isinstance(topk_ids, torch.Tensor) or topk_ids.dim() != 2:
+        _refuse("x and topk_ids must be matrices")
+    T, k = topk_ids.shape
+    H, I = w13.k, w2.k
+    _tensor(x, "x", _BF16, (T, H), dev)
+    _tensor(topk_ids, "topk_ids", _I32, (T, k), dev)
+    _tensor(topk_weights, "topk_weights", _F32, (T, k), dev)
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((T, H), dtype=_BF16, device=dev)
     else:
-        _tensor(out, "out", torch.bfloat16, (T, H), dev)
-    need = lib.chord_f8_moe_workspace_bytes(T, k, w13.handle.num_experts, H, I)
+        _tensor(out, "out", _BF16, (T, H), dev)
     if workspace is None:
+        need = lib.chord_f8_moe_workspace_bytes(T, k, w13.num_experts, H, I)
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
     else:
-        _require(workspace.dtype == torch.uint8 and workspace.is_contiguous() and workspace.device == dev,
-                 f"workspace must be contiguous bytes on {dev}")
-    _check(lib.chord_f8_moe(x.data_ptr(), T, H, I, w13.ref, w2.ref, topk_ids.data_ptr(),
-                            topk_weights.data_ptr(), k, expert_begin, num_global_experts,
-                            out.data_ptr(), workspace.data_ptr(), workspace.numel(), stream))
+        _tensor(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+    st = lib.chord_f8_moe(x.data_ptr(), T, H, I, w13.ref, w2.ref, topk_ids.data_ptr(),
+                          topk_weights.data_ptr(), k, expert_begin, num_global_experts,
+                          out.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(dev))
+    if st:
+        _check(st)
     return out
