@@ -80,13 +80,16 @@ __global__ __launch_bounds__(64 * WK) void f8_stream(F8GemmArgs a) {
         }
       }
     }
+    // NT divides 8, so the tiles of an item share their slice and their block(s)
+    // of scales.
     const uint8_t* wp[NT];
+    const int wstep = f8_slice_width(tile0, a.n_tiles) * kF8BlockBytes;  // chunk to chunk
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int t = min(tile0 + n, a.n_tiles - 1);
-      wp[n] = a.wq + ((int64_t)e * a.n_tiles + t) * nc * kF8BlockBytes + lane * 16;
+      wp[n] = a.wq + ((int64_t)e * a.n_tiles * nc + f8_block(t, 0, a.n_tiles, nc)) * kF8BlockBytes +
+              lane * 16;
     }
-    // NT divides 8, so the tiles of an item share their block(s) of scales.
     const float* s0;
     const float* s1;
     if (a.kind == kF8GateUp) {
@@ -114,8 +117,8 @@ __global__ __launch_bounds__(64 * WK) void f8_stream(F8GemmArgs a) {
       c = min(c, c_hi - 1);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        w[p][n][0] = load_stream(wp[n] + (int64_t)c * kF8BlockBytes);
-        w[p][n][1] = load_stream(wp[n] + (int64_t)c * kF8BlockBytes + 1024);
+        w[p][n][0] = load_stream(wp[n] + (int64_t)c * wstep);
+        w[p][n][1] = load_stream(wp[n] + (int64_t)c * wstep + 1024);
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m) {

@@ -83,11 +83,12 @@ __global__ __launch_bounds__(kThreads) void pack_codes(const uint8_t* __restrict
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n;
        i += (int64_t)gridDim.x * kThreads) {
     const int lane = (int)(i & 63), half = (int)(i >> 6) & 1;
-    const int64_t blk = i >> 7;
-    const int c = (int)(blk % chunks);
-    const int64_t et = blk / chunks;
-    const int t = (int)(et % tiles);
-    const int64_t e = et / tiles;
+    const int64_t blk = i >> 7, e = blk / (tiles * chunks);
+    const int in = (int)(blk - e * tiles * chunks);  // block inside the expert
+    const int slice = in / (int)(kF8SliceTiles * chunks);
+    const int width = f8_slice_width(slice * kF8SliceTiles, (int)tiles);
+    const int rest = in - slice * (int)(kF8SliceTiles * chunks);
+    const int c = rest / width, t = slice * kF8SliceTiles + rest % width;
     const int r = lane & 15;
     int row = t * kTileRows + r;
     if (gate_up) row = (r & 1) * (N / 2) + 8 * t + 2 * (r >> 2) + ((r >> 1) & 1);

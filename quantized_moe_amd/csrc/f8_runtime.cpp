@@ -91,7 +91,7 @@ F8Ws f8_ws(int T, int k, int E_l, int H, int I) {
   w.experts = take((w.max_padded + kF8BlockM - 1) / kF8BlockM * 4);
   w.ntpp = take(4);
   w.status = take(sizeof(DevStatus));
-  w.max_tiles = (int)(w.max_padded / kF8TileRows) + E_l + 1;
+  w.max_tiles = (int)(w.max_padded / kF8MoeTileRows) + E_l + 1;
   w.tiles = take(w.max_tiles * sizeof(TileDesc));
   w.xq = take((int64_t)T * H);
   w.xs = take((int64_t)T * f8_chunks(H) * 4);
@@ -321,7 +321,7 @@ chord_status chord_f8_moe(const chord_bf16* x, int T, int H, int I, const chord_
     tb.layout = kIndexed;
     tb.num_experts = E_l;
     tb.tile_tokens = kF8BlockM;
-    tb.big_tokens = kF8TileRows;
+    tb.big_tokens = kF8MoeTileRows;
     tb.max_tiles_b = ws.max_tiles;
     tb.max_ksplit = 2;
     tb.expert_ids = experts;

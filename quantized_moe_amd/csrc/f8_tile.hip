@@ -1,23 +1,31 @@
 // 8-bit GEMM with block scales, LDS-tiled form for many rows: a workgroup of 8
 // waves computes 256 weight rows x up to 256 tokens.
 //
-// Per 128-wide K chunk the workgroup stages 32 KB of packed weights, the
-// tokens' 128-byte row pieces and their scales in LDS, straight from memory
-// (buffer_load ... lds), double-buffered: chunk c + 1 lands while chunk c is
-// multiplied.  Waves form a 2 x 4 grid (token halves x row quarters); a wave
-// owns 64 rows x 16 MG tokens and holds its four weight operands for the whole
-// chunk, so LDS reads stay below the matrix time (24 KB per wave and chunk at
-// MG = 8, 94 of 128 bytes per clock).  A matrix instruction covers the chunk, its
-// result is scaled into the fp32 accumulators one token group later, so the
-// four multiply-adds run beside the next matrix instructions.
+// Wave w owns weight tiles 2 w and 2 w + 1 (16 rows each) and every token.  Its
+// weights go straight from memory into registers; the tokens' 128-byte row pieces
+// and their scales go straight from memory into LDS (buffer_load ... lds), three
+// chunks of 128 along K ahead, in four buffers.  (With weights in LDS too only
+// one chunk fits in flight, and the loads alone took as long as the products.)
 //
-// Token rows lie in LDS as eight 16-byte pieces, piece p of row r at p ^ (r / 2 %
-// 8): 128-bit reads go in halves of 8 bytes for 16 lanes (16 rows, one piece) at
-// a time, and this key puts them on 16 different bank pairs.
+// A matrix instruction covers the chunk; its result is scaled into the fp32
+// accumulators one token group later, so the multiply-adds run beside the next
+// matrix instructions.  Nothing drains at the end of a chunk: the one barrier of
+// chunk c stands in its middle.  Behind it every wave knows that chunk c + 1 has
+// landed, so the last group already reads the next chunk's first operand, and
+// that chunk c - 1 is read, so its buffer takes chunk c + 3.
+//
+// Token rows lie in LDS as eight 16-byte pieces, piece p of row r at p ^ key(r).
+// A 128-bit read takes 8 lanes at a time, four neighbours of one operand
+// quarter and four of the next (lanes 0-3 with 20-23, 4-7 with 16-19, ...), so
+// four rows' piece p and the next four's piece p + 2: the key (r % 8 with its two
+// low bits swapped) puts those, and also the 16 lanes of two such groups over
+// 64 banks, on different banks.
 //
 // gate_up: 256 interleaved rows are one block of 128 features of h, gate and up,
-// so the epilogue quantises that block (maximum over the four row quarters
-// through LDS) and stores codes: h never exists in memory in more bits.
+// so the epilogue quantises that block (maximum over the eight waves through
+// LDS) and stores codes: h never exists in memory in more bits.
+#include <type_traits>
+
 #include "f8_common.h"
 
 namespace chord {
@@ -29,28 +37,40 @@ constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kTiles = 16;                // weight tiles per workgroup
 constexpr int kRows = kF8TileRows;        // tokens per workgroup
-constexpr int kWBuf = kTiles * kF8BlockBytes;
 constexpr int kXBuf = kRows * kF8Block;
+constexpr int kStages = 4;                // chunks: one in use, three on their way
 constexpr int kXcds = 8;
+constexpr int kStreamAux = 2;             // non-temporal
 
 typedef const __attribute__((address_space(4))) float ConstFloat;
 
 struct Smem {
-  uint8_t w[2][kWBuf];
-  uint8_t x[2][kXBuf];
-  float s[2][kRows];
+  uint8_t x[kStages][kXBuf];
   uint32_t xoff[kRows];  // byte offset of the row's codes, or kNoRow
   uint32_t soff[kRows];  // byte offset of the row's scales, or kNoRow
   int32_t dst[kRows];    // output row, or -1
-  uint32_t amax[4][kRows];
+  uint32_t amax[kWaves][kRows];
 };
 
-__device__ __forceinline__ i32x8_t operand(const uint4& a, const uint4& b) {
-  return i32x8_t{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+__device__ __forceinline__ i32x8_t operand(u32x4_t a, u32x4_t b) {
+  return i32x8_t{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
 
-// Buffer resource (raw, out-of-range offsets read as zero) in four scalars.
+// Scales of four chunks, and of the next four: the buffer changes at run time,
+// so it is an object of its own, which no other load can be taken to touch.
+typedef float Scales[2][kRows][4];
+
+// Memory straight to LDS, lane l's 4 bytes to `lds` + 4 l.  Written out because
+// the compiler, which sees that such a load writes LDS but not which half of
+// the scales, would wait for it before reading the other half; the barrier's
+// count covers it.  Nothing is returned in registers.  (s_nop 4: m0, and
+// scalars that a vector instruction wrote, have to be old enough for a memory
+// instruction; the compiler does not look in here.)
 typedef __attribute__((ext_vector_type(4))) int Rsrc;
+__device__ __forceinline__ void load_lds4(uint32_t lds, uint32_t voff, Rsrc r, int soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, %3 offen lds"
+               :: "s"(lds), "v"(voff), "s"(r), "s"(soff) : "memory", "m0");
+}
 __device__ __forceinline__ Rsrc make_rsrc(const void* p, int64_t bytes) {
   const uint64_t b = reinterpret_cast<uint64_t>(p);
   return Rsrc{__builtin_amdgcn_readfirstlane((int)b),
@@ -58,185 +78,234 @@ __device__ __forceinline__ Rsrc make_rsrc(const void* p, int64_t bytes) {
               __builtin_amdgcn_readfirstlane((int)bytes), kRsrcWord3};
 }
 
-// Memory straight to LDS: lane l's 16 (4) bytes go to `lds` + 16 (4) l.  Written
-// out because the compiler, which sees that such a load writes LDS but not
-// which part of it, waits for all of them before the next LDS read; the waits
-// here are the explicit ones in run_item.  Nothing is returned in registers.
-// (s_nop 4: m0, and scalars that a vector instruction wrote, have to be old
-// enough for a memory instruction; the compiler does not look in here.)
-__device__ __forceinline__ void load_lds16(uint32_t lds, uint32_t voff, Rsrc r, int soff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-               :: "s"(lds), "v"(voff), "s"(r), "s"(soff) : "memory", "m0");
-}
-__device__ __forceinline__ void load_lds4(uint32_t lds, uint32_t voff, Rsrc r, int soff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, %3 offen lds"
-               :: "s"(lds), "v"(voff), "s"(r), "s"(soff) : "memory", "m0");
-}
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
-}
+__device__ __forceinline__ int swz(int r) { return (r & 4) | ((r & 1) << 1) | ((r >> 1) & 1); }
 
 struct Item {
   int expert, slice, nrows;
   int64_t row0;  // first row (plain: of the activations; else: aligned row)
 };
 
+// One item with G = 2 MG token groups of 16.
 template <int MG, int KIND>
-__device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem& sm, const Item& it,
-                                         Rsrc xres, Rsrc sres) {
+__device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem& sm, Scales& scales,
+                                         const Item& it, __amdgpu_buffer_rsrc_t xres, Rsrc sres) {
+  constexpr int G = 2 * MG;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, col = lane & 15;
-  const int wm = wave >> 2, wn = wave & 3;
   const int nc = a.n_chunks;
   const int64_t expert_bytes = (int64_t)a.n_tiles * nc * kF8BlockBytes;
-  const Rsrc wres = make_rsrc(a.wq + it.expert * expert_bytes, expert_bytes);
+  const __amdgpu_buffer_rsrc_t wres = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(a.wq + it.expert * expert_bytes), 0, (int)expert_bytes, kRsrcWord3);
 
   // Token loads: instruction j brings rows 8 j .. 8 j + 7, one row per 8 lanes.
-  // Surplus slots repeat the last rows (the same bytes to the same place).
-  constexpr int kDma = (4 * MG + kWaves - 1) / kWaves;
+  // Surplus slots repeat the last rows (the same bytes to the same place), so
+  // that every wave issues the same number of loads.
+  constexpr int kDma = (2 * G + kWaves - 1) / kWaves;
   uint32_t xo[kDma];
   int jx[kDma];
 #pragma unroll
   for (int i = 0; i < kDma; ++i) {
-    jx[i] = min(wave + kWaves * i, 4 * MG - 1);
+    jx[i] = min(wave + kWaves * i, 2 * G - 1);
     const int row = 8 * jx[i] + (lane >> 3);
-    xo[i] = sm.xoff[row] + (uint32_t)(((lane & 7) ^ ((row >> 1) & 7)) * 16);
+    xo[i] = sm.xoff[row] + (uint32_t)(((lane & 7) ^ swz(row)) * 16);
   }
-  const int js = min(wave, (32 * MG + 63) / 64 - 1);
-  const uint32_t so = sm.soff[js * 64 + lane];
-  // Weight loads: two tiles per wave, 1 KB per instruction.
+  // Scales come for four chunks at a time, 16 rows x 4 chunks per instruction:
+  // fetched chunk by chunk, every row's 4 bytes are a memory request of their own,
+  // more of them than the rows themselves take (gate_up of 8192 tokens on 48
+  // experts: 381 us, with this 340).
+  uint32_t so[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) so[i] = sm.soff[(8 * i + wave) * 16 + (lane >> 2)] + (lane & 3) * 4;
+  // Weights: tiles past the last one of a partial slice repeat it.
   const int t0 = min(it.slice * kTiles + 2 * wave, a.n_tiles - 1);
   const int t1 = min(it.slice * kTiles + 2 * wave + 1, a.n_tiles - 1);
-  const uint32_t lx = lds_address(sm.x[0]), lw = lds_address(sm.w[0] + 2 * wave * kF8BlockBytes);
-  const uint32_t ls = lds_address(sm.s[0] + js * 64);
-  auto fill = [&](int b, int c) {
-#pragma unroll
-    for (int i = 0; i < kDma; ++i)
-      load_lds16(lx + b * kXBuf + jx[i] * 1024, xo[i], xres, c * kF8Block);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      load_lds16(lw + b * kWBuf + i * 1024, lane * 16 + (i & 1) * 1024, wres,
-                 ((i < 2 ? t0 : t1) * nc + c) * kF8BlockBytes);
-    load_lds4(ls + b * (kRows * 4), so, sres, c * 4);
+  const int o0 = f8_block(t0, 0, a.n_tiles, nc) * kF8BlockBytes;
+  const int o1 = f8_block(t1, 0, a.n_tiles, nc) * kF8BlockBytes;
+  const int wstep = f8_slice_width(t0, a.n_tiles) * kF8BlockBytes;  // chunk to chunk
+  // Weight registers: as far ahead as the tokens where the accumulators leave
+  // room, else one chunk.
+  constexpr int WR = G <= 12 ? 4 : 2;
+  u32x4_t w[WR][2][2];
+  constexpr int kW = 4;  // loads of weights per chunk
+  auto load_x = [&](int j, int b, int c) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        xres, (__attribute__((address_space(3))) void*)(sm.x[b] + jx[j] * 1024), 16, xo[j],
+        c * kF8Block, 0, 0);
+  };
+  // Half i of the scales of chunks c0 .. c0 + 3.  (Past a row's end: other rows',
+  // never used, or zeros.)
+  const uint32_t ls = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) float*)&scales[0][wave * 16][0];
+  auto load_s = [&](int i, int half, int c0) {
+    load_lds4(ls + half * (kRows * 16) + i * (kRows * 8), so[i], sres, c0 * 4);
+  };
+  auto load_w = [&](int j, int b, int c) {
+    w[b][j >> 1][j & 1] = __builtin_amdgcn_raw_buffer_load_b128(
+        wres, lane * 16 + (j & 1) * 1024, (j >> 1 ? o1 : o0) + c * wstep, kStreamAux);
   };
 
-  // Weight scales of this wave's four tiles (a gate and an up block, or one).
+  // Weight scales of this wave's two tiles (a gate and an up block, or one).
   // (Constant address space: uniform scalar loads, although the kernel writes.)
-  const int blk = KIND == kF8GateUp ? it.slice : min(2 * it.slice + (wn >> 1), a.nb - 1);
+  const int blk = KIND == kF8GateUp ? it.slice : min(2 * it.slice + (wave >> 2), a.nb - 1);
   const ConstFloat* s0 = (const ConstFloat*)(a.ws + ((int64_t)it.expert * a.nb + blk) * nc);
   const ConstFloat* s1 = KIND == kF8GateUp ? s0 + (int64_t)(a.nb / 2) * nc : s0;
 
-  f32x4_t acc[4][MG];
+  f32x4_t acc[2][G];
 #pragma unroll
-  for (int n = 0; n < 4; ++n)
+  for (int n = 0; n < 2; ++n)
 #pragma unroll
-    for (int g = 0; g < MG; ++g) acc[n][g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int g = 0; g < G; ++g) acc[n][g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  const int xrow = (wm * MG * 16 + col) * kF8Block;
-  const int x0 = xrow + (((2 * q) ^ ((col >> 1) & 7)) * 16);
-  const int x1 = xrow + (((2 * q + 1) ^ ((col >> 1) & 7)) * 16);
-  const int w0 = 4 * wn * kF8BlockBytes + lane * 16;
+  const int x0 = col * kF8Block + (((2 * q) ^ swz(col)) * 16);
+  const int x1 = col * kF8Block + (((2 * q + 1) ^ swz(col)) * 16);
 
-  auto compute = [&](int b, float sw0, float sw1) {
-    const uint8_t* xb = sm.x[b];
-    const uint8_t* wb = sm.w[b] + w0;
-    const float* sb = sm.s[b] + wm * MG * 16 + col;
-    auto read_x = [&](int g) {
-      return operand(*reinterpret_cast<const uint4*>(xb + x0 + g * 16 * kF8Block),
-                     *reinterpret_cast<const uint4*>(xb + x1 + g * 16 * kF8Block));
-    };
-    i32x8_t wv[4];
-#pragma unroll
-    for (int n = 0; n < 4; ++n)
-      wv[n] = operand(*reinterpret_cast<const uint4*>(wb + n * kF8BlockBytes),
-                      *reinterpret_cast<const uint4*>(wb + n * kF8BlockBytes + 1024));
-    i32x8_t xv[2];
-    float sx[2];
-    xv[0] = read_x(0);
-    sx[0] = sb[0];
-    f32x4_t r[2][4];
-    auto scale_in = [&](int g, float s) {
-      const float f0 = s * sw0, f1 = KIND == kF8GateUp ? s * sw1 : f0;
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        acc[n][g][0] = __builtin_fmaf(r[g & 1][n][0], f0, acc[n][g][0]);
-        acc[n][g][1] = __builtin_fmaf(r[g & 1][n][1], f1, acc[n][g][1]);
-        acc[n][g][2] = __builtin_fmaf(r[g & 1][n][2], f0, acc[n][g][2]);
-        acc[n][g][3] = __builtin_fmaf(r[g & 1][n][3], f1, acc[n][g][3]);
-      }
-    };
-    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int g = 0; g < MG; ++g) {
-      const float sprev = sx[(g + 1) & 1];
-      if (g + 1 < MG) {
-        xv[(g + 1) & 1] = read_x(g + 1);
-      }
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-        r[g & 1][n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv[n], xv[g & 1], zero, 0, 0,
-                                                                      0, 0, 0, 0);
-      if (g > 0) scale_in(g - 1, sprev);
-      if (g + 1 < MG) sx[(g + 1) & 1] = sb[(g + 1) * 16];
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    scale_in(MG - 1, sx[(MG - 1) & 1]);
+  auto read_x = [&](int b, int g) {
+    const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(sm.x[b] + x0 + g * 16 * kF8Block);
+    const u32x4_t hi = *reinterpret_cast<const u32x4_t*>(sm.x[b] + x1 + g * 16 * kF8Block);
+    return operand(lo, hi);
   };
-
-  fill(0, 0);
-  float sw0 = s0[0], sw1 = s1[0];
-  for (int c = 0; c < nc; ++c) {
-    // Everything issued one chunk ago has landed, in every wave; and no wave
-    // reads the other buffer any more.
+  auto read_s = [&](int half, int ph, int g) { return scales[half][g * 16 + col][ph]; };
+  const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+  i32x8_t xv[2];
+  float sx[2];
+  f32x4_t r[2][2] = {{zero, zero}, {zero, zero}};
+  float f0 = 0.f, f1 = 0.f;  // factors of the results in r
+  auto scale_in = [&](int n, int g) {
+    acc[n][g][0] = __builtin_fmaf(r[g & 1][n][0], f0, acc[n][g][0]);
+    acc[n][g][1] = __builtin_fmaf(r[g & 1][n][1], f1, acc[n][g][1]);
+    acc[n][g][2] = __builtin_fmaf(r[g & 1][n][2], f0, acc[n][g][2]);
+    acc[n][g][3] = __builtin_fmaf(r[g & 1][n][3], f1, acc[n][g][3]);
+  };
+  auto barrier = [&](auto outstanding) {  // ... loads of this wave may be on their way
+    constexpr int vm = decltype(outstanding)::value;
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));  // vmcnt(0)
+    __builtin_amdgcn_s_waitcnt((vm & 15) | (7 << 4) | (15 << 8) | ((vm >> 4) << 14));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    const int cn = c + 1 < nc ? c + 1 : c;
-    if (c + 1 < nc) fill((c + 1) & 1, c + 1);
-    const float n0 = s0[cn], n1 = s1[cn];
-    compute(c & 1, sw0, sw1);
+  };
+  float sw0 = s0[0], sw1 = s1[0];
+
+  // Chunk c in buffer b (= c % 4; its group 0 and that group's scales are in
+  // registers; half: which of the scales are its own).
+  // Load indices past the end repeat the last chunk, so every chunk issues the
+  // same loads and the counts are exact.  At the barrier only these may be
+  // younger than the tokens of chunk c + 1: a chunk's weights, the tokens of
+  // chunk c + 2 with (in two chunks of four) half of the next scales in front
+  // of them, and this chunk's weights.
+  constexpr int kBehind = 2 * kW + kDma;
+  auto chunk = [&](int b, int c, int half) {
+    const int nb = (b + 1) % kStages, fb = (b + 3) % kStages;
+    const int c1 = min(c + 1, nc - 1), c3 = min(c + 3, nc - 1);
+    const float n0 = s0[c1], n1 = s1[c1];
+    const i32x8_t w0 = operand(w[b % WR][0][0], w[b % WR][0][1]);
+    const i32x8_t w1 = operand(w[b % WR][1][0], w[b % WR][1][1]);
+    // Fences after every matrix instruction keep this order: one matrix
+    // instruction, then the multiply-adds of the one two places before it (left
+    // alone, the compiler puts those right behind their own instruction, with
+    // waits for its result).
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      if (g == G / 2 && (b == 1 || b == 2)) barrier(std::integral_constant<int, kBehind + 1>{});
+      if (g == G / 2 && (b == 0 || b == 3)) barrier(std::integral_constant<int, kBehind>{});
+      r[g & 1][0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w0, xv[g & 1], zero, 0, 0, 0, 0, 0, 0);
+      xv[(g + 1) & 1] = g + 1 < G ? read_x(b, g + 1) : read_x(nb, 0);
+      scale_in(0, (g + G - 1) % G);
+      __builtin_amdgcn_sched_barrier(0);
+      r[g & 1][1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w1, xv[g & 1], zero, 0, 0, 0, 0, 0, 0);
+      scale_in(1, (g + G - 1) % G);
+      f0 = sx[g & 1] * sw0;
+      f1 = KIND == kF8GateUp ? sx[g & 1] * sw1 : f0;
+      sx[(g + 1) & 1] = g + 1 < G ? read_s(half, b, g + 1) : read_s(b == 3 ? 1 - half : half, nb, 0);
+#pragma unroll
+      for (int j = 0; j < kW; ++j)
+        if (g < G / 2 && j * (G / 2) / kW == g) load_w(j, (b + WR - 1) % WR, WR == 4 ? c3 : c1);
+      if (g == G / 2 && b < 2) load_s(b, 1 - half, c - b + 4);
+#pragma unroll
+      for (int j = 0; j < kDma; ++j)
+        if (g >= G / 2 && j * (G / 2) / kDma == g - G / 2) load_x(j, fb, c3);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     sw0 = n0;
     sw1 = n1;
+  };
+
+  auto load_all_x = [&](int c) {
+#pragma unroll
+    for (int j = 0; j < kDma; ++j) load_x(j, c, min(c, nc - 1));
+  };
+  auto load_all_w = [&](int c) {
+#pragma unroll
+    for (int j = 0; j < kW; ++j) load_w(j, c, min(c, nc - 1));
+  };
+  // (Weights stand between the tokens of chunks 1 and 2, as the count at the
+  // barrier has it.)
+  if (WR == 4) {
+    load_all_w(0);
+    load_all_w(1);
   }
+  load_s(0, 0, 0);
+  load_s(1, 0, 0);
+  load_all_x(0);
+  load_all_x(1);
+  load_all_w(WR == 4 ? 2 : 0);
+  load_all_x(2);
+  barrier(std::integral_constant<int, kW + 2 * kDma>{});
+  xv[0] = read_x(0, 0);
+  sx[0] = read_s(0, 0, 0);
+  int c = 0, half = 0;
+  for (; c + 3 < nc; c += 4) {
+    chunk(0, c, half);
+    chunk(1, c + 1, half);
+    chunk(2, c + 2, half);
+    chunk(3, c + 3, half);
+    half = 1 - half;
+  }
+  if (c < nc) chunk(0, c, half);
+  if (c + 1 < nc) chunk(1, c + 1, half);
+  if (c + 2 < nc) chunk(2, c + 2, half);
+  scale_in(0, G - 1);
+  scale_in(1, G - 1);
+  // The repeated loads at the end land before their buffers are used again.
+  __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));
 
   if (KIND == kF8GateUp) {
-    // h of this lane: features 8 (4 wn + n) + 2 q + {0, 1} of token col in group g.
-    uint32_t m[MG];
+    // h of this lane: features 8 (2 wave + n) + 2 q + {0, 1} of token col in group g.
 #pragma unroll
-    for (int g = 0; g < MG; ++g) {
-      m[g] = 0;
+    for (int g = 0; g < G; ++g) {
+      uint32_t m = 0;
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
+      for (int n = 0; n < 2; ++n) {
         acc[n][g][0] = silu_mul(acc[n][g][0], acc[n][g][1]);
         acc[n][g][1] = silu_mul(acc[n][g][2], acc[n][g][3]);
-        m[g] = max(m[g], __float_as_uint(acc[n][g][0]) & 0x7FFFFFFFu);
-        m[g] = max(m[g], __float_as_uint(acc[n][g][1]) & 0x7FFFFFFFu);
+        m = max(m, __float_as_uint(acc[n][g][0]) & 0x7FFFFFFFu);
+        m = max(m, __float_as_uint(acc[n][g][1]) & 0x7FFFFFFFu);
       }
-      m[g] = max(m[g], (uint32_t)__shfl_xor((int)m[g], 16, 64));
-      m[g] = max(m[g], (uint32_t)__shfl_xor((int)m[g], 32, 64));
-      if (q == 0) sm.amax[wn][(wm * MG + g) * 16 + col] = m[g];
+      m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+      m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+      if (q == 0) sm.amax[wave][g * 16 + col] = m;
     }
-    __syncthreads();  // also: every wave is done with the stage buffers
+    __syncthreads();  // also: every wave is done with the token buffers
     uint8_t* codes = sm.x[0];  // [tokens][128]
 #pragma unroll
-    for (int g = 0; g < MG; ++g) {
-      const int t = (wm * MG + g) * 16 + col;
-      const F8Group f = f8_group(max(max(sm.amax[0][t], sm.amax[1][t]), max(sm.amax[2][t], sm.amax[3][t])));
+    for (int g = 0; g < G; ++g) {
+      const int t = g * 16 + col;
+      uint32_t m = sm.amax[0][t];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
+      for (int u = 1; u < kWaves; ++u) m = max(m, sm.amax[u][t]);
+      const F8Group f = f8_group(m);
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
         const float v0 = f.inv != 0.f ? f8_value(f, acc[n][g][0]) : 0.f;
         const float v1 = f.inv != 0.f ? f8_value(f, acc[n][g][1]) : 0.f;
-        *reinterpret_cast<uint16_t*>(codes + t * kF8Block + 8 * (4 * wn + n) + 2 * q) =
+        *reinterpret_cast<uint16_t*>(codes + t * kF8Block + 8 * (2 * wave + n) + 2 * q) =
             (uint16_t)__builtin_amdgcn_cvt_pk_fp8_f32(v0, v1, 0, false);
       }
-      if (wn == 0 && q == 0 && sm.dst[t] >= 0)
+      if (wave == 0 && q == 0 && sm.dst[t] >= 0)
         a.hs[(int64_t)sm.dst[t] * (a.nb / 2) + it.slice] = f.scale;
     }
     __syncthreads();
     uint8_t* hq = static_cast<uint8_t*>(a.out);
-    for (int i = threadIdx.x; i < 32 * MG * 8; i += kThreads) {
+    for (int i = threadIdx.x; i < 16 * G * 8; i += kThreads) {
       const int t = i >> 3;
       if (sm.dst[t] >= 0)
         *reinterpret_cast<uint4*>(hq + (int64_t)sm.dst[t] * a.ld + it.slice * kF8Block + (i & 7) * 16) =
@@ -245,14 +314,14 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem& sm, const It
     return;
   }
 
-  const int n_base = (it.slice * kTiles + 4 * wn) * 16 + 4 * q;
+  const int n_base = (it.slice * kTiles + 2 * wave) * 16 + 4 * q;
   const bool wide = a.ld % 4 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 7) == 0;
 #pragma unroll
-  for (int g = 0; g < MG; ++g) {
-    const int64_t d = sm.dst[(wm * MG + g) * 16 + col];
+  for (int g = 0; g < G; ++g) {
+    const int64_t d = sm.dst[g * 16 + col];
     if (d < 0) continue;
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
+    for (int n = 0; n < 2; ++n) {
       const int f = n_base + 16 * n;
       if (KIND == kF8Down) {
         if (f < a.N) *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + d * a.ld + f) = acc[n][g];
@@ -272,7 +341,7 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem& sm, const It
 }
 
 template <int KIND>
-__device__ __forceinline__ void do_item(const F8GemmArgs& a, Smem& sm, const Item& it) {
+__device__ __forceinline__ void do_item(const F8GemmArgs& a, Smem& sm, Scales& scales, const Item& it) {
   const int64_t pitch = (int64_t)a.n_chunks * kF8Block, spitch = (int64_t)a.n_chunks * 4;
   __syncthreads();  // the last item's epilogue is done with the tables
   const uint8_t* xbase = a.aq;
@@ -303,16 +372,19 @@ __device__ __forceinline__ void do_item(const F8GemmArgs& a, Smem& sm, const Ite
     sm.dst[m] = (int32_t)dst;
   }
   __syncthreads();
-  const Rsrc xres = make_rsrc(xbase, xrows * pitch), sres = make_rsrc(sbase, xrows * spitch);
+  const __amdgpu_buffer_rsrc_t xres =
+      __builtin_amdgcn_make_buffer_rsrc((void*)xbase, 0, (int)(xrows * pitch), kRsrcWord3);
+  const Rsrc sres = make_rsrc(sbase, xrows * spitch);
   switch ((it.nrows + 31) / 32) {
-    case 1: run_item<1, KIND>(a, sm, it, xres, sres); break;
-    case 2: run_item<2, KIND>(a, sm, it, xres, sres); break;
-    case 3: run_item<3, KIND>(a, sm, it, xres, sres); break;
-    case 4: run_item<4, KIND>(a, sm, it, xres, sres); break;
-    case 5: run_item<5, KIND>(a, sm, it, xres, sres); break;
-    case 6: run_item<6, KIND>(a, sm, it, xres, sres); break;
-    case 7: run_item<7, KIND>(a, sm, it, xres, sres); break;
-    default: run_item<8, KIND>(a, sm, it, xres, sres); break;
+    case 1: run_item<1, KIND>(a, sm, scales, it, xres, sres); break;
+    case 2: run_item<2, KIND>(a, sm, scales, it, xres, sres); break;
+    case 3: run_item<3, KIND>(a, sm, scales, it, xres, sres); break;
+    case 4: run_item<4, KIND>(a, sm, scales, it, xres, sres); break;
+    case 5: run_item<5, KIND>(a, sm, scales, it, xres, sres); break;
+    case 6: run_item<6, KIND>(a, sm, scales, it, xres, sres); break;
+    case 7: run_item<7, KIND>(a, sm, scales, it, xres, sres); break;
+    default:
+      if constexpr (KIND == kF8Plain) run_item<8, KIND>(a, sm, scales, it, xres, sres);
   }
 }
 
@@ -321,6 +393,7 @@ template <int KIND>
 __global__ __launch_bounds__(kThreads, 2) void f8_tile(F8GemmArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   Smem& sm = *reinterpret_cast<Smem*>(smem);
+  __shared__ __attribute__((aligned(16))) Scales scales;
   const int slices = (a.n_tiles + kTiles - 1) / kTiles;
   const int xcd = blockIdx.x % kXcds, local = blockIdx.x / kXcds;
   const int per_xcd = (gridDim.x + kXcds - 1 - xcd) / kXcds;
@@ -340,7 +413,7 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tile(F8GemmArgs a) {
       it.slice = rest / wide;
       it.row0 = (block * 8 + rest % wide) * kRows;
       it.nrows = (int)min((int64_t)kRows, a.a_rows - it.row0);
-      do_item<KIND>(a, sm, it);
+      do_item<KIND>(a, sm, scales, it);
     }
   } else {
     // The tile list comes in 8 groups of balanced size, one per XCD; all slices
@@ -355,8 +428,8 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tile(F8GemmArgs a) {
         it.expert = td.expert;
         it.slice = j % slices;
         it.row0 = td.row_begin;
-        it.nrows = min(td.nrows, kRows);
-        do_item<KIND>(a, sm, it);
+        it.nrows = min(td.nrows, kF8MoeTileRows);
+        do_item<KIND>(a, sm, scales, it);
       }
     }
   }

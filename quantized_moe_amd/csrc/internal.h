@@ -228,13 +228,13 @@ struct DispatchArgs {
 // Packed 8-bit weight layout (gfx950).
 //
 // A weight [E, N, K] is cut into 16-row tiles and 128-wide K chunks (both
-// padded with zero codes).  Each (expert, tile, chunk) is one 2048-byte block,
-// tile-major, in the operand order of v_mfma_f32_16x16x128_f8f6f4: piece h
-// (1 KB), lane l, 16 bytes: tile row r = l % 16, k = chunk * 128 +
-// (l / 16) * 32 + 16 h + [0, 16).  A wave streaming a tile along K reads
-// contiguous memory, and a block copied to LDS as it is gives operand reads
-// without bank conflicts.  The block scales, fp32 [E, ceil(N / 128), chunks],
-// follow the codes.
+// padded with zero codes).  Each (expert, tile, chunk) is one 2048-byte block
+// in the operand order of v_mfma_f32_16x16x128_f8f6f4: piece h (1 KB), lane l,
+// 16 bytes: tile row r = l % 16, k = chunk * 128 + (l / 16) * 32 + 16 h +
+// [0, 16).  The blocks of 16 neighbouring tiles (256 rows; the last slice may
+// have fewer) stand together chunk by chunk: a workgroup that streams a slice
+// along K reads 32 KB runs of contiguous memory.  The block scales, fp32
+// [E, ceil(N / 128), chunks], follow the codes.
 //
 // Gate_up weights interleave gate and up rows as the 4-bit layout does: tile t,
 // row r = 4q + w holds feature f = 8t + 2q + (w >> 1); w even = gate row f,
@@ -251,6 +251,17 @@ __host__ __device__ inline size_t f8_code_bytes(int E, int N, int K) {
 inline size_t f8_packed_bytes(int E, int N, int K) {
   return f8_code_bytes(E, N, K) +
          (size_t)E * ((N + kF8Block - 1) / kF8Block) * f8_chunks(K) * sizeof(float);
+}
+
+constexpr int kF8SliceTiles = 16;
+// Place of the block of tile t, chunk c inside its expert, in blocks.
+__host__ __device__ inline int f8_slice_width(int t, int n_tiles) {
+  const int rest = n_tiles - t / kF8SliceTiles * kF8SliceTiles;
+  return rest < kF8SliceTiles ? rest : kF8SliceTiles;
+}
+__host__ __device__ inline int f8_block(int t, int c, int n_tiles, int n_chunks) {
+  return t / kF8SliceTiles * kF8SliceTiles * n_chunks + c * f8_slice_width(t, n_tiles) +
+         t % kF8SliceTiles;
 }
 
 struct RouteArgs {
@@ -279,7 +290,8 @@ struct F8QuantArgs {
 };
 
 // Arguments of one 8-bit GEMM launch.
-constexpr int kF8TileRows = 256;  // tokens per workgroup of the tiled kernel
+constexpr int kF8TileRows = 256;     // tokens per workgroup of the tiled kernel, and of its
+constexpr int kF8MoeTileRows = 224;  // layer forms (the largest variant of gate_up would spill)
 enum F8Kind : int { kF8Plain = 0, kF8GateUp = 1, kF8Down = 2 };
 struct F8GemmArgs {
   int kind;
@@ -300,7 +312,7 @@ struct F8GemmArgs {
   int num_experts;
   int topk;
   int64_t n_flat;
-  // tiled kernel: tiles of at most kF8TileRows rows
+  // tiled kernel: tiles of at most kF8MoeTileRows rows
   const TileDesc* tiles;
   const DevStatus* status;
   // output: bf16 [*, ld] by row (plain); h by aligned row (gate_up: fp32
