@@ -69,7 +69,7 @@ F8GemmArgs weight_args(const chord_f8_weight* w, int kind, int cus) {
 }
 
 // ---- layer workspace --------------------------------------------------------
-constexpr int kF8BlockM = 16;  // rows per alignment block
+constexpr int kF8MaxBlockM = kF8SmallRows;  // rows per alignment block at most
 
 struct F8Ws {
   size_t align, sorted, experts, ntpp, status, tiles, xq, xs, h, hq, hs, y, total;
@@ -79,16 +79,16 @@ struct F8Ws {
 
 F8Ws f8_ws(int T, int k, int E_l, int H, int I) {
   F8Ws w{};
-  w.max_padded = chord_moe_align_max_padded(T, k, E_l, kF8BlockM);
+  w.max_padded = chord_moe_align_max_padded(T, k, E_l, kF8MaxBlockM);
   size_t off = 0;
   auto take = [&](int64_t bytes) {
     const size_t o = off;
     off += ((size_t)bytes + 255) & ~(size_t)255;
     return o;
   };
-  w.align = take((int64_t)chord_moe_align_workspace_bytes(T, k, E_l, kF8BlockM));
+  w.align = take((int64_t)chord_moe_align_workspace_bytes(T, k, E_l, kF8MaxBlockM));
   w.sorted = take(w.max_padded * 4);
-  w.experts = take((w.max_padded + kF8BlockM - 1) / kF8BlockM * 4);
+  w.experts = take((w.max_padded + 15) / 16 * 4);
   w.ntpp = take(4);
   w.status = take(sizeof(DevStatus));
   w.max_tiles = (int)(w.max_padded / kF8MoeTileRows) + E_l + 1;
@@ -103,6 +103,32 @@ F8Ws f8_ws(int T, int k, int E_l, int H, int I) {
   return w;
 }
 
+// How a layer call runs, from its expected rows per expert.
+struct F8MoePlan {
+  int block_m;          // rows per alignment block
+  bool small;           // tiled GEMMs over the alignment blocks (else over built tiles)
+  bool stream_gate_up;  // small: gate_up by the weight-streaming kernel
+  int active;           // expected experts with rows
+  const char* text;
+};
+constexpr double kSmallRowsPerExpert = 24.0;
+F8MoePlan f8_moe_plan(int T, int k, int E_g, int E_l, int I, int cus) {
+  const int eg = E_g > E_l ? E_g : E_l;
+  const double tok_e = (double)T * k / eg;
+  F8MoePlan p{};
+  p.small = tok_e < kSmallRowsPerExpert;
+  p.block_m = p.small && tok_e > 8.0 ? 32 : 16;
+  // Expected gate_up items of the small form (active experts x slices of 256
+  // rows) against its workgroups.
+  const double active = E_l * (1.0 - pow(1.0 - 1.0 / eg, (double)T * k));
+  p.active = std::max(1, (int)(active + 0.5));
+  p.stream_gate_up = p.small && p.block_m == 16 && active * (2 * I / 256) < 4.0 * 2 * cus;
+  p.text = !p.small ? "f8 moe: tiles of up to 224 rows"
+           : p.stream_gate_up ? "f8 moe: blocks of 16 rows, streaming gate_up"
+           : p.block_m == 16 ? "f8 moe: blocks of 16 rows" : "f8 moe: blocks of 32 rows";
+  return p;
+}
+
 chord_status check_moe_sizes(int T, int k, int E_l, int H, int I) {
   if (T < 0 || k < 1 || E_l < 1 || H < 1 || I < 1)
     return fail(CHORD_ERR_INVALID_ARGUMENT, "T=%d k=%d E_l=%d H=%d I=%d", T, k, E_l, H, I);
@@ -112,7 +138,7 @@ chord_status check_moe_sizes(int T, int k, int E_l, int H, int I) {
   const int64_t slots = (int64_t)T * k;
   if (slots >= (int64_t)1 << 30 || slots * H * 2 > kMaxOperand)
     return fail(CHORD_ERR_UNSUPPORTED, "T*k*H exceeds 2^30");
-  const int64_t rows = chord_moe_align_max_padded(T, k, E_l, kF8BlockM);
+  const int64_t rows = chord_moe_align_max_padded(T, k, E_l, kF8MaxBlockM);
   if (rows * I > kMaxOperand) return fail(CHORD_ERR_UNSUPPORTED, "rows of h exceed 2 GiB");
   return CHORD_OK;
 }
@@ -247,7 +273,7 @@ chord_status chord_f8_gemm(const chord_f8* codes, const float* scales, int64_t M
   g.out = out;
   g.ld = ld;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  HIP_TRY(M >= kTileMinRows ? launch_f8_tile(g, st) : launch_f8_gemm(g, st), "8-bit GEMM launch");
+  HIP_TRY(M >= kTileMinRows ? launch_f8_tile(g, false, st) : launch_f8_gemm(g, st), "8-bit GEMM launch");
   return CHORD_OK;
 }
 
@@ -284,7 +310,6 @@ chord_status chord_f8_moe(const chord_bf16* x, int T, int H, int I, const chord_
     return fail(CHORD_ERR_WORKSPACE, "workspace %zu bytes, %zu needed", ws_bytes, ws.total);
   if (!aligned(workspace, 256))
     return fail(CHORD_ERR_WORKSPACE, "the workspace must be 256-byte aligned");
-  (void)num_global_experts;
   int cus = 0;
   CHORD_CHECK(check_device(&cus));
   hipStream_t st = static_cast<hipStream_t>(stream);
@@ -301,52 +326,49 @@ chord_status chord_f8_moe(const chord_bf16* x, int T, int H, int I, const chord_
   q.q = p + ws.xq;
   q.s = reinterpret_cast<float*>(p + ws.xs);
   HIP_TRY(launch_f8_quantize(q, st), "quantize launch");
-  CHORD_CHECK(chord_moe_align(topk_ids, T, k, expert_begin, E_l, kF8BlockM, sorted, experts, ntpp,
+  const F8MoePlan plan = f8_moe_plan(T, k, num_global_experts, E_l, I, cus);
+  CHORD_CHECK(chord_moe_align(topk_ids, T, k, expert_begin, E_l, plan.block_m, sorted, experts, ntpp,
                               ws.max_padded, p + ws.align,
-                              chord_moe_align_workspace_bytes(T, k, E_l, kF8BlockM), 0, st));
-  auto rows_of = [&](F8GemmArgs& g) {
-    g.sorted_ids = sorted;
-    g.expert_ids = experts;
-    g.ntpp = ntpp;
-    g.block_m = kF8BlockM;
-    g.max_padded = ws.max_padded;
-    g.topk = k;
-    g.n_flat = (int64_t)T * k;
-  };
-  // Expected rows per expert pick the kernel.
-  const int eg = num_global_experts > E_l ? num_global_experts : E_l;
-  const bool tiled = (double)T * k / eg >= kTileMinRows;
-  if (tiled) {
+                              chord_moe_align_workspace_bytes(T, k, E_l, plan.block_m), 0, st));
+  const TileDesc* tiles = reinterpret_cast<const TileDesc*>(p + ws.tiles);
+  const DevStatus* status = reinterpret_cast<const DevStatus*>(p + ws.status);
+  if (!plan.small) {
     TileBuildArgs tb{};
     tb.layout = kIndexed;
     tb.num_experts = E_l;
-    tb.tile_tokens = kF8BlockM;
+    tb.tile_tokens = plan.block_m;
     tb.big_tokens = kF8MoeTileRows;
     tb.max_tiles_b = ws.max_tiles;
     tb.max_ksplit = 2;
     tb.expert_ids = experts;
     tb.ntpp = ntpp;
-    tb.block_m = kF8BlockM;
+    tb.block_m = plan.block_m;
     tb.max_padded = ws.max_padded;
     tb.tiles_b = reinterpret_cast<TileDesc*>(p + ws.tiles);
     tb.status = reinterpret_cast<DevStatus*>(p + ws.status);
     HIP_TRY(launch_build_tiles(tb, st), "tile builder launch");
   }
+  auto rows_of = [&](F8GemmArgs& g) {
+    g.sorted_ids = sorted;
+    g.expert_ids = experts;
+    g.ntpp = ntpp;
+    g.block_m = plan.block_m;
+    g.max_padded = ws.max_padded;
+    g.topk = k;
+    g.n_flat = (int64_t)T * k;
+    g.est_blocks = plan.active;
+    g.tiles = tiles;
+    g.status = status;
+  };
+  uint8_t* hq = p + ws.hq;
+  float* hs = reinterpret_cast<float*>(p + ws.hs);
   F8GemmArgs g = weight_args(w13, kF8GateUp, cus);
   rows_of(g);
   g.aq = q.q;
   g.as = q.s;
   g.a_rows = T;
   g.ld = I;
-  g.tiles = reinterpret_cast<const TileDesc*>(p + ws.tiles);
-  g.status = reinterpret_cast<const DevStatus*>(p + ws.status);
-  uint8_t* hq = p + ws.hq;
-  float* hs = reinterpret_cast<float*>(p + ws.hs);
-  if (tiled) {
-    g.out = hq;
-    g.hs = hs;
-    HIP_TRY(launch_f8_tile(g, st), "gate_up launch");
-  } else {
+  if (plan.stream_gate_up) {
     g.out = p + ws.h;
     HIP_TRY(launch_f8_gemm(g, st), "gate_up launch");
     F8QuantArgs qh{};
@@ -359,6 +381,10 @@ chord_status chord_f8_moe(const chord_bf16* x, int T, int H, int I, const chord_
     qh.q = hq;
     qh.s = hs;
     HIP_TRY(launch_f8_quantize(qh, st), "quantize launch");
+  } else {
+    g.out = hq;
+    g.hs = hs;
+    HIP_TRY(launch_f8_tile(g, plan.small, st), "gate_up launch");
   }
 
   F8GemmArgs d = weight_args(w2, kF8Down, cus);
@@ -366,11 +392,10 @@ chord_status chord_f8_moe(const chord_bf16* x, int T, int H, int I, const chord_
   d.aq = hq;
   d.as = hs;
   d.a_rows = ws.max_padded;
-  d.tiles = g.tiles;
-  d.status = g.status;
   d.out = p + ws.y;
   d.ld = H;
-  HIP_TRY(tiled ? launch_f8_tile(d, st) : launch_f8_gemm(d, st), "down launch");
+  HIP_TRY(plan.small && d.n_chunks <= 2 ? launch_f8_short_down(d, st) : launch_f8_tile(d, plan.small, st),
+          "down launch");
 
   F8CombineArgs c{};
   c.y = reinterpret_cast<const float*>(p + ws.y);
@@ -383,7 +408,7 @@ chord_status chord_f8_moe(const chord_bf16* x, int T, int H, int I, const chord_
   c.num_experts = E_l;
   c.out = reinterpret_cast<uint16_t*>(out);
   HIP_TRY(launch_f8_combine(c, st), "combine launch");
-  set_last_plan(tiled ? "f8 moe: tiled GEMMs" : "f8 moe: streaming GEMMs");
+  set_last_plan(plan.text);
   return CHORD_OK;
 }
 

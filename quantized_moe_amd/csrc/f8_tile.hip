@@ -36,20 +36,20 @@ constexpr uint32_t kNoRow = 0xC0000000u;  // byte offset past any row buffer
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kTiles = 16;                // weight tiles per workgroup
-constexpr int kRows = kF8TileRows;        // tokens per workgroup
-constexpr int kXBuf = kRows * kF8Block;
 constexpr int kStages = 4;                // chunks: one in use, three on their way
 constexpr int kXcds = 8;
 constexpr int kStreamAux = 2;             // non-temporal
 
 typedef const __attribute__((address_space(4))) float ConstFloat;
 
+// ROWS: tokens per workgroup at most.
+template <int ROWS>
 struct Smem {
-  uint8_t x[kStages][kXBuf];
-  uint32_t xoff[kRows];  // byte offset of the row's codes, or kNoRow
-  uint32_t soff[kRows];  // byte offset of the row's scales, or kNoRow
-  int32_t dst[kRows];    // output row, or -1
-  uint32_t amax[kWaves][kRows];
+  uint8_t x[kStages][ROWS * kF8Block];
+  uint32_t xoff[ROWS];  // byte offset of the row's codes, or kNoRow
+  uint32_t soff[ROWS];  // byte offset of the row's scales, or kNoRow
+  int32_t dst[ROWS];    // output row, or -1
+  uint32_t amax[kWaves][ROWS];
 };
 
 __device__ __forceinline__ i32x8_t operand(u32x4_t a, u32x4_t b) {
@@ -58,7 +58,10 @@ __device__ __forceinline__ i32x8_t operand(u32x4_t a, u32x4_t b) {
 
 // Scales of four chunks, and of the next four: the buffer changes at run time,
 // so it is an object of its own, which no other load can be taken to touch.
-typedef float Scales[2][kRows][4];
+template <int ROWS>
+struct Scales {
+  float s[2][ROWS][4];
+};
 
 // Memory straight to LDS, lane l's 4 bytes to `lds` + 4 l.  Written out because
 // the compiler, which sees that such a load writes LDS but not which half of
@@ -86,8 +89,8 @@ struct Item {
 };
 
 // One item with G = 2 MG token groups of 16.
-template <int MG, int KIND>
-__device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem& sm, Scales& scales,
+template <int MG, int KIND, int ROWS>
+__device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Scales<ROWS>& scales,
                                          const Item& it, __amdgpu_buffer_rsrc_t xres, Rsrc sres) {
   constexpr int G = 2 * MG;
   const int lane = threadIdx.x & 63;
@@ -114,9 +117,15 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem& sm, Scales& 
   // fetched chunk by chunk, every row's 4 bytes are a memory request of their own,
   // more of them than the rows themselves take (gate_up of 8192 tokens on 48
   // experts: 381 us, with this 340).
+  // (Fewer than 256 rows: the surplus waves repeat rows, to the same places.)
   uint32_t so[2];
+  uint32_t ls[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) so[i] = sm.soff[(8 * i + wave) * 16 + (lane >> 2)] + (lane & 3) * 4;
+  for (int i = 0; i < 2; ++i) {
+    const int m = (8 * i + wave) % (ROWS / 16);
+    so[i] = sm.soff[m * 16 + (lane >> 2)] + (lane & 3) * 4;
+    ls[i] = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) float*)&scales.s[0][m * 16][0];
+  }
   // Weights: tiles past the last one of a partial slice repeat it.
   const int t0 = min(it.slice * kTiles + 2 * wave, a.n_tiles - 1);
   const int t1 = min(it.slice * kTiles + 2 * wave + 1, a.n_tiles - 1);
@@ -135,9 +144,8 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem& sm, Scales& 
   };
   // Half i of the scales of chunks c0 .. c0 + 3.  (Past a row's end: other rows',
   // never used, or zeros.)
-  const uint32_t ls = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) float*)&scales[0][wave * 16][0];
   auto load_s = [&](int i, int half, int c0) {
-    load_lds4(ls + half * (kRows * 16) + i * (kRows * 8), so[i], sres, c0 * 4);
+    load_lds4(ls[i] + half * (ROWS * 16), so[i], sres, c0 * 4);
   };
   auto load_w = [&](int j, int b, int c) {
     w[b][j >> 1][j & 1] = __builtin_amdgcn_raw_buffer_load_b128(
@@ -164,7 +172,7 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem& sm, Scales& 
     const u32x4_t hi = *reinterpret_cast<const u32x4_t*>(sm.x[b] + x1 + g * 16 * kF8Block);
     return operand(lo, hi);
   };
-  auto read_s = [&](int half, int ph, int g) { return scales[half][g * 16 + col][ph]; };
+  auto read_s = [&](int half, int ph, int g) { return scales.s[half][g * 16 + col][ph]; };
   const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
   i32x8_t xv[2];
   float sx[2];
@@ -340,8 +348,9 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem& sm, Scales& 
   }
 }
 
-template <int KIND>
-__device__ __forceinline__ void do_item(const F8GemmArgs& a, Smem& sm, Scales& scales, const Item& it) {
+template <int KIND, int ROWS>
+__device__ __forceinline__ void do_item(const F8GemmArgs& a, Smem<ROWS>& sm, Scales<ROWS>& scales,
+                                        const Item& it) {
   const int64_t pitch = (int64_t)a.n_chunks * kF8Block, spitch = (int64_t)a.n_chunks * 4;
   __syncthreads();  // the last item's epilogue is done with the tables
   const uint8_t* xbase = a.aq;
@@ -352,7 +361,7 @@ __device__ __forceinline__ void do_item(const F8GemmArgs& a, Smem& sm, Scales& s
     sbase += it.row0 * spitch;
     xrows = it.nrows;
   }
-  if (threadIdx.x < kRows) {
+  if (threadIdx.x < ROWS) {
     const int m = threadIdx.x;
     int64_t src = -1, dst = -1;
     if (m < it.nrows) {
@@ -375,35 +384,38 @@ __device__ __forceinline__ void do_item(const F8GemmArgs& a, Smem& sm, Scales& s
   const __amdgpu_buffer_rsrc_t xres =
       __builtin_amdgcn_make_buffer_rsrc((void*)xbase, 0, (int)(xrows * pitch), kRsrcWord3);
   const Rsrc sres = make_rsrc(sbase, xrows * spitch);
-  switch ((it.nrows + 31) / 32) {
-    case 1: run_item<1, KIND>(a, sm, scales, it, xres, sres); break;
-    case 2: run_item<2, KIND>(a, sm, scales, it, xres, sres); break;
-    case 3: run_item<3, KIND>(a, sm, scales, it, xres, sres); break;
-    case 4: run_item<4, KIND>(a, sm, scales, it, xres, sres); break;
-    case 5: run_item<5, KIND>(a, sm, scales, it, xres, sres); break;
-    case 6: run_item<6, KIND>(a, sm, scales, it, xres, sres); break;
-    case 7: run_item<7, KIND>(a, sm, scales, it, xres, sres); break;
-    default:
-      if constexpr (KIND == kF8Plain) run_item<8, KIND>(a, sm, scales, it, xres, sres);
+  if constexpr (ROWS == kF8SmallRows) {
+    run_item<1, KIND, ROWS>(a, sm, scales, it, xres, sres);
+  } else {
+    switch ((it.nrows + 31) / 32) {
+      case 1: run_item<1, KIND, ROWS>(a, sm, scales, it, xres, sres); break;
+      case 2: run_item<2, KIND, ROWS>(a, sm, scales, it, xres, sres); break;
+      case 3: run_item<3, KIND, ROWS>(a, sm, scales, it, xres, sres); break;
+      case 4: run_item<4, KIND, ROWS>(a, sm, scales, it, xres, sres); break;
+      case 5: run_item<5, KIND, ROWS>(a, sm, scales, it, xres, sres); break;
+      case 6: run_item<6, KIND, ROWS>(a, sm, scales, it, xres, sres); break;
+      case 7: run_item<7, KIND, ROWS>(a, sm, scales, it, xres, sres); break;
+      default:
+        if constexpr (KIND == kF8Plain) run_item<8, KIND, ROWS>(a, sm, scales, it, xres, sres);
+    }
   }
 }
 
-// Persistent workgroups.  Workgroup b runs on XCD b % 8.
-template <int KIND>
-__global__ __launch_bounds__(kThreads, 2) void f8_tile(F8GemmArgs a) {
+// Persistent workgroups.  Workgroup b runs on XCD b % 8.  OCC: waves per SIMD.
+template <int KIND, int ROWS, int OCC>
+__global__ __launch_bounds__(kThreads, OCC) void f8_tile(F8GemmArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  Smem& sm = *reinterpret_cast<Smem*>(smem);
-  __shared__ __attribute__((aligned(16))) Scales scales;
+  Smem<ROWS>& sm = *reinterpret_cast<Smem<ROWS>*>(smem);
+  __shared__ __attribute__((aligned(16))) Scales<ROWS> scales;
   const int slices = (a.n_tiles + kTiles - 1) / kTiles;
   const int xcd = blockIdx.x % kXcds, local = blockIdx.x / kXcds;
-  const int per_xcd = (gridDim.x + kXcds - 1 - xcd) / kXcds;
+  const int run = gridDim.x / kXcds;  // (the grid is a multiple of 8)
   if (KIND == kF8Plain) {
-    // Runs of `per_xcd` consecutive items go to one XCD at a time.  Items walk
+    // Runs of `run` consecutive items go to one XCD at a time.  Items walk
     // blocks of 8 token tiles slice by slice, so those that run together share
     // few token tiles and few slices through their L2.
-    const int64_t tiles = (a.a_rows + kRows - 1) / kRows;
+    const int64_t tiles = (a.a_rows + ROWS - 1) / ROWS;
     const int64_t total = tiles * slices;
-    const int run = gridDim.x / kXcds;  // (the grid is a multiple of 8)
     for (int64_t i = (int64_t)xcd * run + local; i < total; i += gridDim.x) {
       const int64_t block = i / (8 * slices);
       const int wide = (int)min((int64_t)8, tiles - block * 8);
@@ -411,46 +423,65 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tile(F8GemmArgs a) {
       Item it;
       it.expert = 0;
       it.slice = rest / wide;
-      it.row0 = (block * 8 + rest % wide) * kRows;
-      it.nrows = (int)min((int64_t)kRows, a.a_rows - it.row0);
-      do_item<KIND>(a, sm, scales, it);
+      it.row0 = (block * 8 + rest % wide) * ROWS;
+      it.nrows = (int)min((int64_t)ROWS, a.a_rows - it.row0);
+      do_item<KIND, ROWS>(a, sm, scales, it);
+    }
+  } else if (ROWS == kF8SmallRows) {
+    // Tiles are the alignment blocks (at most ROWS rows), block t and all its
+    // slices on XCD t % 8.
+    const int64_t used = max((int64_t)0, min((int64_t)*a.ntpp, a.max_padded));
+    const int blocks = (int)(used / a.block_m);
+    const int mine = xcd < blocks ? (blocks - xcd + kXcds - 1) / kXcds : 0;
+    for (int64_t j = local; j < (int64_t)mine * slices; j += run) {
+      const int t = (int)(j / slices) * kXcds + xcd;
+      Item it;
+      it.expert = a.expert_ids[t];
+      it.slice = (int)(j % slices);
+      it.row0 = (int64_t)t * a.block_m;
+      it.nrows = a.block_m;
+      if (it.expert < 0 || it.expert >= a.num_experts) continue;  // uniform
+      do_item<KIND, ROWS>(a, sm, scales, it);
     }
   } else {
     // The tile list comes in 8 groups of balanced size, one per XCD; all slices
     // of a tile stay on one XCD, which reads its token rows once.
-    const int G = gridDim.x < kXcds ? (int)gridDim.x : kXcds;
-    for (int g = xcd; g < kTileGroups; g += G) {
-      const int t0 = a.status->group_start[g];
-      const int n = (a.status->group_start[g + 1] - t0) * slices;
-      for (int j = local; j < n; j += per_xcd) {
-        const TileDesc td = a.tiles[t0 + j / slices];
-        Item it;
-        it.expert = td.expert;
-        it.slice = j % slices;
-        it.row0 = td.row_begin;
-        it.nrows = min(td.nrows, kF8MoeTileRows);
-        do_item<KIND>(a, sm, scales, it);
-      }
+    const int t0 = a.status->group_start[xcd];
+    const int n = (a.status->group_start[xcd + 1] - t0) * slices;
+    for (int j = local; j < n; j += run) {
+      const TileDesc td = a.tiles[t0 + j / slices];
+      Item it;
+      it.expert = td.expert;
+      it.slice = j % slices;
+      it.row0 = td.row_begin;
+      it.nrows = min(td.nrows, kF8MoeTileRows);
+      do_item<KIND, ROWS>(a, sm, scales, it);
     }
   }
 }
 
 }  // namespace
 
-hipError_t launch_f8_tile(const F8GemmArgs& a, hipStream_t stream) {
-  // One workgroup per CU (LDS); a multiple of 8 so that every XCD gets a share.
-  const int grid = a.num_cus >= 8 ? a.num_cus / 8 * 8 : 8;
-  const dim3 g((unsigned)grid), b(kThreads);
-  auto run = [&](auto kernel) {
+hipError_t launch_f8_tile(const F8GemmArgs& a, bool small, hipStream_t stream) {
+  // A multiple of 8 workgroups, so that every XCD gets the same share: one per
+  // CU, and two in the small form.
+  const int cus = a.num_cus >= 8 ? a.num_cus / 8 * 8 : 8;
+  auto run = [&](auto kernel, int per_cu, size_t lds) {
     const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)sizeof(Smem));
+                                             (int)lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, g, b, sizeof(Smem), stream, a);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(cus * per_cu)), dim3(kThreads), lds, stream, a);
     return hipGetLastError();
   };
-  if (a.kind == kF8Plain) return run(f8_tile<kF8Plain>);
-  if (a.kind == kF8GateUp) return run(f8_tile<kF8GateUp>);
-  return run(f8_tile<kF8Down>);
+  constexpr int R = kF8TileRows, S = kF8SmallRows;
+  if (small) {
+    if (a.kind == kF8Plain) return run(f8_tile<kF8Plain, S, 4>, 2, sizeof(Smem<S>));
+    if (a.kind == kF8GateUp) return run(f8_tile<kF8GateUp, S, 4>, 2, sizeof(Smem<S>));
+    return run(f8_tile<kF8Down, S, 4>, 2, sizeof(Smem<S>));
+  }
+  if (a.kind == kF8Plain) return run(f8_tile<kF8Plain, R, 2>, 1, sizeof(Smem<R>));
+  if (a.kind == kF8GateUp) return run(f8_tile<kF8GateUp, R, 2>, 1, sizeof(Smem<R>));
+  return run(f8_tile<kF8Down, R, 2>, 1, sizeof(Smem<R>));
 }
 
 }  // namespace chord

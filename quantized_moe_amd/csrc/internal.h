@@ -292,6 +292,7 @@ struct F8QuantArgs {
 // Arguments of one 8-bit GEMM launch.
 constexpr int kF8TileRows = 256;     // tokens per workgroup of the tiled kernel, and of its
 constexpr int kF8MoeTileRows = 224;  // layer forms (the largest variant of gate_up would spill)
+constexpr int kF8SmallRows = 32;     // ... and of its small form, two workgroups per CU
 enum F8Kind : int { kF8Plain = 0, kF8GateUp = 1, kF8Down = 2 };
 struct F8GemmArgs {
   int kind;
@@ -312,7 +313,9 @@ struct F8GemmArgs {
   int num_experts;
   int topk;
   int64_t n_flat;
-  // tiled kernel: tiles of at most kF8MoeTileRows rows
+  int est_blocks;      // expected alignment blocks with rows
+  // tiled kernel: tiles of at most kF8MoeTileRows rows (small form: the
+  // alignment blocks of at most kF8SmallRows rows)
   const TileDesc* tiles;
   const DevStatus* status;
   // output: bf16 [*, ld] by row (plain); h by aligned row (gate_up: fp32
@@ -362,7 +365,9 @@ hipError_t launch_f8_pack(const uint8_t* q, const float* s, int E, int N, int K,
                           uint8_t* dst, hipStream_t stream);
 hipError_t launch_f8_quantize(const F8QuantArgs& a, hipStream_t stream);
 hipError_t launch_f8_gemm(const F8GemmArgs& a, hipStream_t stream);
-hipError_t launch_f8_tile(const F8GemmArgs& a, hipStream_t stream);
+hipError_t launch_f8_tile(const F8GemmArgs& a, bool small, hipStream_t stream);
+// Down product of the small form with K <= 256 (block_m at most 32).
+hipError_t launch_f8_short_down(const F8GemmArgs& a, hipStream_t stream);
 hipError_t launch_f8_combine(const F8CombineArgs& a, hipStream_t stream);
 
 constexpr int kAlignSingle = 8192;      // align in one workgroup up to this many entries
