@@ -593,22 +593,30 @@ chord_status chord_f8_pack(int role, const chord_f8* codes, const float* scales,
 chord_status chord_f8_quantize(const chord_bf16* x, int64_t T, int K, int64_t ld, chord_f8* codes,
                                float* scales, void* stream);
 
+/* Workspace bytes of chord_f8_gemm (0: it needs none); 0 for bad arguments. */
+size_t chord_f8_gemm_workspace_bytes(int64_t M, int N, int K);
+
 /*
  * Matrix product of quantised activations with a packed weight:
  *
  *   out[m, n] = bf16( sum over blocks c of scale_a[m, c] * scale_w[n / 128, c] *
  *                     sum over k in c of a[m, k] * w[n, k] )
  *
- * accumulated in fp32, rounded once.
+ * accumulated in fp32, rounded once.  Products of few rows split K over
+ * workgroups whose fp32 sums are added in order; which do depends on the sizes
+ * alone, so equal calls give equal bits.
  *
  * codes, scales: chord_f8_quantize's outputs for rows of length K (codes
  *          16-byte aligned).
  * w:       handle packed with CHORD_ROLE_PLAIN, [N, K].
  * out:     device bf16 [M, ld], ld >= N; columns from N on are left as they are.
- * Enqueued on `stream`; needs no workspace.  M == 0 is a no-op.
+ * workspace: chord_f8_gemm_workspace_bytes(M, N, K) bytes, 16-byte aligned,
+ *          caller-owned (NULL where that is 0); calls that may overlap need one each.
+ * Enqueued on `stream`.  M == 0 is a no-op.
  */
 chord_status chord_f8_gemm(const chord_f8* codes, const float* scales, int64_t M,
-                           const chord_f8_weight* w, chord_bf16* out, int64_t ld, void* stream);
+                           const chord_f8_weight* w, chord_bf16* out, int64_t ld, void* workspace,
+                           size_t ws_bytes, void* stream);
 
 /* Workspace bytes of chord_f8_moe; 0 for bad arguments. */
 size_t chord_f8_moe_workspace_bytes(int T, int k, int E_l, int H, int I);

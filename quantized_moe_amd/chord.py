@@ -34,7 +34,7 @@ EXPORTED = [
     "chord_moe_dispatch_contiguous_rows", "chord_moe_dispatch_workspace_bytes",
     "chord_moe_dispatch_contiguous", "chord_moe_dispatch_masked", "chord_moe_combine",
     "chord_w4a16_moe_plan", "chord_moe_route", "chord_f8_packed_bytes", "chord_f8_pack",
-    "chord_f8_quantize", "chord_f8_gemm", "chord_f8_moe_workspace_bytes", "chord_f8_moe",
+    "chord_f8_quantize", "chord_f8_gemm_workspace_bytes", "chord_f8_gemm", "chord_f8_moe_workspace_bytes", "chord_f8_moe",
 ]
 
 
@@ -107,7 +107,8 @@ def _load():
         "chord_f8_packed_bytes": (SZ, [I, I, I, I]),
         "chord_f8_pack": (I, [I, P, P, I, I, I, I, P, SZ, FP, P]),
         "chord_f8_quantize": (I, [P, I64, I, I64, P, P, P]),
-        "chord_f8_gemm": (I, [P, P, I64, FP, P, I64, P]),
+        "chord_f8_gemm_workspace_bytes": (SZ, [I64, I, I]),
+        "chord_f8_gemm": (I, [P, P, I64, FP, P, I64, P, SZ, P]),
         "chord_f8_moe_workspace_bytes": (SZ, [I, I, I, I, I]),
         "chord_f8_moe": (I, [P, I, I, I, FP, FP, P, P, I, I, I, P, P, SZ, P]),
     }
@@ -560,11 +561,16 @@ def chord_f8_quantize(x, out=None, stream=None):
     return q, s
 
 
-def chord_f8_gemm(codes, scales, w: F8PackedWeight, out=None, stream=None):
+def chord_f8_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
+    return lib.chord_f8_gemm_workspace_bytes(M, N, K)
+
+
+def chord_f8_gemm(codes, scales, w: F8PackedWeight, out=None, workspace=None, stream=None):
     """bf16 [M, N]: chord_f8_quantize's (codes, scales) times the packed weight
     [N, K].  `out` may have strided rows."""
     if _away(codes, stream):
-        return _elsewhere(chord_f8_gemm, codes, stream, scales=scales, w=w, out=out)
+        return _elsewhere(chord_f8_gemm, codes, stream, scales=scales, w=w, out=out,
+                          workspace=workspace)
     dev = codes.get_device()
     _weight(w, "w", dev)
     if codes.dim() != 2:
@@ -578,8 +584,17 @@ def chord_f8_gemm(codes, scales, w: F8PackedWeight, out=None, stream=None):
     else:
         _tensor(out, "out", _BF16, (M, N), dev, contiguous=False)
         ld = _row_stride(out, "out")
-    st = lib.chord_f8_gemm(codes.data_ptr(), scales.data_ptr(), M, w.ref, out.data_ptr(), ld,
-                           _raw_stream(dev))
+    ws, nbytes = None, 0
+    if workspace is not None:
+        _tensor(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+        ws, nbytes = workspace.data_ptr(), workspace.numel()
+    else:
+        nbytes = lib.chord_f8_gemm_workspace_bytes(M, N, w.k)
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            ws = workspace.data_ptr()
+    st = lib.chord_f8_gemm(codes.data_ptr(), scales.data_ptr(), M, w.ref, out.data_ptr(), ld, ws,
+                           nbytes, _raw_stream(dev))
     if st:
         _check(st)
     return out

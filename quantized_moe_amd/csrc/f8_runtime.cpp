@@ -14,9 +14,51 @@ constexpr int kRouteMaxGroups = 64;
 // Codes of one expert are addressed with 32-bit offsets.
 constexpr int64_t kMaxOperand = ((int64_t)1 << 31) - 1;
 
-// Rows (of the product; of an expert on average) from which the LDS-tiled
-// kernel takes over from the streaming one.
-constexpr int kTileMinRows = 64;
+// How a dense product runs: the weight-streaming kernel (tiles of 16 tokens x 16
+// outputs, K over the waves of a workgroup), or the tiled kernel with tile_rows
+// tokens x 256 outputs and K in parts that a second launch adds.
+struct F8GemmPlan {
+  bool stream;
+  int tile_rows;
+  int parts;
+};
+
+// The cheapest by estimate, in us on an MI355X: a round of 256 workgroups takes
+// 4 and so much per chunk, adding parts 4.5 and its bytes.  Fitted to sweeps
+// over M = 1 .. 4096 with N = 512 .. 7168, K = 500 .. 7168; where both sides
+// were near (within 10 %) it may pick the slower.  Measured, stream / tiled:
+// M=8 N=4096 K=7168 9.8 / 15.4; M=32 22.8 / 15.8 (64 rows, 8 parts); M=100
+// N=576 12.0 / 14.4; M=100 N=2112 42.2 / 17.4; M=512 N=4096 rows x parts 64x2
+// 32.9, 128x4 34.3, 256x8 41.6; M=2048 128x1 60.4, 256x2 78.9, 64x1 89.5.
+F8GemmPlan f8_gemm_plan(int64_t M, int N, int K) {
+  constexpr int64_t kCus = 256;  // (of the model, so that the workspace depends on sizes alone)
+  const int nc = (int)f8_chunks(K);
+  const int64_t tiles = f8_tiles(N), slices = (tiles + 15) / 16;
+  F8GemmPlan best{true, 0, 1};
+  if (M <= 16) return best;
+  double cost = 3.0 + std::max(1.0, (double)((M + 15) / 16 * tiles) / kCus) * (3.5 + 0.09 * nc);
+  const struct {
+    int rows;
+    double chunk;
+  } shapes[] = {{64, 0.75}, {96, 0.85}, {128, 1.0}, {192, 1.42}, {256, 1.82}};
+  for (const auto& s : shapes) {
+    const int64_t items = (M + s.rows - 1) / s.rows * slices;
+    for (int parts : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      if (parts > nc || (parts > 1 && items * parts > 2 * kCus)) break;
+      const double rounds = (double)((items * parts + kCus - 1) / kCus);
+      double c = rounds * (4.0 + (nc + parts - 1) / parts * s.chunk);
+      if (parts > 1) c += 4.5 + parts * (double)M * tiles * 16 * 8 / 4e6;
+      if (c < cost) {
+        cost = c;
+        best = F8GemmPlan{false, s.rows, parts};
+      }
+    }
+  }
+  return best;
+}
+size_t f8_gemm_ws(const F8GemmPlan& p, int64_t M, int N) {
+  return p.parts > 1 ? (size_t)p.parts * M * f8_tiles(N) * 16 * sizeof(float) : 0;
+}
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
@@ -254,7 +296,8 @@ chord_status chord_f8_quantize(const chord_bf16* x, int64_t T, int K, int64_t ld
 }
 
 chord_status chord_f8_gemm(const chord_f8* codes, const float* scales, int64_t M,
-                           const chord_f8_weight* w, chord_bf16* out, int64_t ld, void* stream) {
+                           const chord_f8_weight* w, chord_bf16* out, int64_t ld, void* workspace,
+                           size_t ws_bytes, void* stream) {
   clear_last_error();
   CHORD_CHECK(check_f8_weight(w, "w", CHORD_ROLE_PLAIN));
   if (M < 0) return fail(CHORD_ERR_INVALID_ARGUMENT, "M=%lld", (long long)M);
@@ -264,17 +307,32 @@ chord_status chord_f8_gemm(const chord_f8* codes, const float* scales, int64_t M
   if (M >= (int64_t)1 << 31) return fail(CHORD_ERR_UNSUPPORTED, "M=%lld", (long long)M);
   if (!codes || !scales || !out) return fail(CHORD_ERR_INVALID_ARGUMENT, "null pointer argument");
   if (!aligned(codes, 16)) return fail(CHORD_ERR_INVALID_ARGUMENT, "codes must be 16-byte aligned");
+  const F8GemmPlan plan = f8_gemm_plan(M, w->n, w->k);
+  const size_t need = f8_gemm_ws(plan, M, w->n);
+  if (need > 0 && (!workspace || ws_bytes < need))
+    return fail(CHORD_ERR_WORKSPACE, "workspace %zu bytes, %zu needed", ws_bytes, need);
+  if (need > 0 && !aligned(workspace, 16))
+    return fail(CHORD_ERR_WORKSPACE, "the workspace must be 16-byte aligned");
   int cus = 0;
   CHORD_CHECK(check_device(&cus));
   F8GemmArgs g = weight_args(w, kF8Plain, cus);
+  g.tile_rows = plan.tile_rows;
+  g.parts = plan.parts;
+  g.partials = static_cast<float*>(workspace);
   g.aq = codes;
   g.as = scales;
   g.a_rows = M;
   g.out = out;
   g.ld = ld;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  HIP_TRY(M >= kTileMinRows ? launch_f8_tile(g, false, st) : launch_f8_gemm(g, st), "8-bit GEMM launch");
+  HIP_TRY(plan.stream ? launch_f8_gemm(g, st) : launch_f8_tile(g, false, st), "8-bit GEMM launch");
   return CHORD_OK;
+}
+
+size_t chord_f8_gemm_workspace_bytes(int64_t M, int N, int K) {
+  clear_last_error();
+  if (M < 0 || check_shape(CHORD_ROLE_PLAIN, 1, N, K) != CHORD_OK) return 0;
+  return f8_gemm_ws(f8_gemm_plan(M, N, K), M, N);
 }
 
 size_t chord_f8_moe_workspace_bytes(int T, int k, int E_l, int H, int I) {

@@ -86,6 +86,7 @@ __device__ __forceinline__ int swz(int r) { return (r & 4) | ((r & 1) << 1) | ((
 struct Item {
   int expert, slice, nrows;
   int64_t row0;  // first row (plain: of the activations; else: aligned row)
+  int part;      // plain: part of K (of a.parts)
 };
 
 // One item with G = 2 MG token groups of 16.
@@ -96,8 +97,10 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, col = lane & 15;
-  const int nc = a.n_chunks;
-  const int64_t expert_bytes = (int64_t)a.n_tiles * nc * kF8BlockBytes;
+  // Chunks c_lo .. c_lo + nc of the row's n_chunks.
+  const int c_lo = KIND == kF8Plain ? (int)((int64_t)a.n_chunks * it.part / a.parts) : 0;
+  const int nc = KIND == kF8Plain ? (int)((int64_t)a.n_chunks * (it.part + 1) / a.parts) - c_lo : a.n_chunks;
+  const int64_t expert_bytes = (int64_t)a.n_tiles * a.n_chunks * kF8BlockBytes;
   const __amdgpu_buffer_rsrc_t wres = __builtin_amdgcn_make_buffer_rsrc(
       (void*)(a.wq + it.expert * expert_bytes), 0, (int)expert_bytes, kRsrcWord3);
 
@@ -111,7 +114,7 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
   for (int i = 0; i < kDma; ++i) {
     jx[i] = min(wave + kWaves * i, 2 * G - 1);
     const int row = 8 * jx[i] + (lane >> 3);
-    xo[i] = sm.xoff[row] + (uint32_t)(((lane & 7) ^ swz(row)) * 16);
+    xo[i] = sm.xoff[row] + (uint32_t)(c_lo * kF8Block + ((lane & 7) ^ swz(row)) * 16);
   }
   // Scales come for four chunks at a time, 16 rows x 4 chunks per instruction:
   // fetched chunk by chunk, every row's 4 bytes are a memory request of their own,
@@ -123,14 +126,14 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int m = (8 * i + wave) % (ROWS / 16);
-    so[i] = sm.soff[m * 16 + (lane >> 2)] + (lane & 3) * 4;
+    so[i] = sm.soff[m * 16 + (lane >> 2)] + (c_lo + (lane & 3)) * 4;
     ls[i] = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) float*)&scales.s[0][m * 16][0];
   }
   // Weights: tiles past the last one of a partial slice repeat it.
   const int t0 = min(it.slice * kTiles + 2 * wave, a.n_tiles - 1);
   const int t1 = min(it.slice * kTiles + 2 * wave + 1, a.n_tiles - 1);
-  const int o0 = f8_block(t0, 0, a.n_tiles, nc) * kF8BlockBytes;
-  const int o1 = f8_block(t1, 0, a.n_tiles, nc) * kF8BlockBytes;
+  const int o0 = f8_block(t0, c_lo, a.n_tiles, a.n_chunks) * kF8BlockBytes;
+  const int o1 = f8_block(t1, c_lo, a.n_tiles, a.n_chunks) * kF8BlockBytes;
   const int wstep = f8_slice_width(t0, a.n_tiles) * kF8BlockBytes;  // chunk to chunk
   // Weight registers: as far ahead as the tokens where the accumulators leave
   // room, else one chunk.
@@ -155,8 +158,8 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
   // Weight scales of this wave's two tiles (a gate and an up block, or one).
   // (Constant address space: uniform scalar loads, although the kernel writes.)
   const int blk = KIND == kF8GateUp ? it.slice : min(2 * it.slice + (wave >> 2), a.nb - 1);
-  const ConstFloat* s0 = (const ConstFloat*)(a.ws + ((int64_t)it.expert * a.nb + blk) * nc);
-  const ConstFloat* s1 = KIND == kF8GateUp ? s0 + (int64_t)(a.nb / 2) * nc : s0;
+  const ConstFloat* s0 = (const ConstFloat*)(a.ws + ((int64_t)it.expert * a.nb + blk) * a.n_chunks + c_lo);
+  const ConstFloat* s1 = KIND == kF8GateUp ? s0 + (int64_t)(a.nb / 2) * a.n_chunks : s0;
 
   f32x4_t acc[2][G];
 #pragma unroll
@@ -331,7 +334,11 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       const int f = n_base + 16 * n;
-      if (KIND == kF8Down) {
+      if (KIND == kF8Plain && a.parts > 1) {
+        if (f < a.n_tiles * 16)
+          *reinterpret_cast<f32x4_t*>(a.partials + ((int64_t)it.part * a.a_rows + it.row0 + d) * (a.n_tiles * 16) +
+                                      f) = acc[n][g];
+      } else if (KIND == kF8Down) {
         if (f < a.N) *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + d * a.ld + f) = acc[n][g];
       } else {
         uint16_t* p = static_cast<uint16_t*>(a.out) + (it.row0 + d) * a.ld + f;
@@ -401,6 +408,29 @@ __device__ __forceinline__ void do_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sca
   }
 }
 
+// out[m, n] = bf16(sum of the K parts, ascending).
+__global__ __launch_bounds__(256) void f8_add_parts(F8GemmArgs a) {
+  const int pitch = a.n_tiles * 16, quads = pitch / 4;
+  const bool wide = a.ld % 4 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 7) == 0;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.a_rows * quads;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t m = i / quads;
+    const int n = (int)(i - m * quads) * 4;
+    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int p = 0; p < a.parts; ++p)
+      v += *reinterpret_cast<const f32x4_t*>(a.partials + ((int64_t)p * a.a_rows + m) * pitch + n);
+    uint16_t* o = static_cast<uint16_t*>(a.out) + m * a.ld + n;
+    if (wide && n + 4 <= a.N) {
+      *reinterpret_cast<uint2*>(o) = make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
+    } else {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (n + u < a.N) o[u] = to_bf16(v[u]);
+    }
+  }
+}
+
 // Persistent workgroups.  Workgroup b runs on XCD b % 8.  OCC: waves per SIMD.
 template <int KIND, int ROWS, int OCC>
 __global__ __launch_bounds__(kThreads, OCC) void f8_tile(F8GemmArgs a) {
@@ -414,17 +444,19 @@ __global__ __launch_bounds__(kThreads, OCC) void f8_tile(F8GemmArgs a) {
     // Runs of `run` consecutive items go to one XCD at a time.  Items walk
     // blocks of 8 token tiles slice by slice, so those that run together share
     // few token tiles and few slices through their L2.
-    const int64_t tiles = (a.a_rows + ROWS - 1) / ROWS;
-    const int64_t total = tiles * slices;
-    for (int64_t i = (int64_t)xcd * run + local; i < total; i += gridDim.x) {
-      const int64_t block = i / (8 * slices);
+    const int rows = a.tile_rows;
+    const int64_t tiles = (a.a_rows + rows - 1) / rows;
+    const int64_t whole = tiles * slices;
+    for (int64_t i = (int64_t)xcd * run + local; i < whole * a.parts; i += gridDim.x) {
+      const int64_t u = i % whole, block = u / (8 * slices);
       const int wide = (int)min((int64_t)8, tiles - block * 8);
-      const int rest = (int)(i - block * 8 * slices);
+      const int rest = (int)(u - block * 8 * slices);
       Item it;
       it.expert = 0;
+      it.part = (int)(i / whole);
       it.slice = rest / wide;
-      it.row0 = (block * 8 + rest % wide) * ROWS;
-      it.nrows = (int)min((int64_t)ROWS, a.a_rows - it.row0);
+      it.row0 = (block * 8 + rest % wide) * rows;
+      it.nrows = (int)min((int64_t)rows, a.a_rows - it.row0);
       do_item<KIND, ROWS>(a, sm, scales, it);
     }
   } else if (ROWS == kF8SmallRows) {
@@ -474,14 +506,18 @@ hipError_t launch_f8_tile(const F8GemmArgs& a, bool small, hipStream_t stream) {
     return hipGetLastError();
   };
   constexpr int R = kF8TileRows, S = kF8SmallRows;
-  if (small) {
-    if (a.kind == kF8Plain) return run(f8_tile<kF8Plain, S, 4>, 2, sizeof(Smem<S>));
-    if (a.kind == kF8GateUp) return run(f8_tile<kF8GateUp, S, 4>, 2, sizeof(Smem<S>));
-    return run(f8_tile<kF8Down, S, 4>, 2, sizeof(Smem<S>));
+  if (a.kind == kF8Plain) {
+    const hipError_t e = run(f8_tile<kF8Plain, R, 2>, 1, sizeof(Smem<R>));
+    if (e != hipSuccess || a.parts <= 1) return e;
+    const int64_t n = (a.a_rows * (a.n_tiles * 4) + 255) / 256, most = (int64_t)a.num_cus * 16;
+    hipLaunchKernelGGL(f8_add_parts, dim3((unsigned)(n < most ? n : most)), dim3(256), 0, stream, a);
+    return hipGetLastError();
   }
-  if (a.kind == kF8Plain) return run(f8_tile<kF8Plain, R, 2>, 1, sizeof(Smem<R>));
-  if (a.kind == kF8GateUp) return run(f8_tile<kF8GateUp, R, 2>, 1, sizeof(Smem<R>));
-  return run(f8_tile<kF8Down, R, 2>, 1, sizeof(Smem<R>));
+  if (a.kind == kF8GateUp)
+    return small ? run(f8_tile<kF8GateUp, S, 4>, 2, sizeof(Smem<S>))
+                 : run(f8_tile<kF8GateUp, R, 2>, 1, sizeof(Smem<R>));
+  return small ? run(f8_tile<kF8Down, S, 4>, 2, sizeof(Smem<S>))
+               : run(f8_tile<kF8Down, R, 2>, 1, sizeof(Smem<R>));
 }
 
 }  // namespace chord

@@ -318,6 +318,10 @@ struct F8GemmArgs {
   // alignment blocks of at most kF8SmallRows rows)
   const TileDesc* tiles;
   const DevStatus* status;
+  // tiled kernel, plain: rows per tile (a multiple of 32), and parts of K whose
+  // fp32 sums [parts, a_rows, n_tiles * 16] a second launch adds
+  int tile_rows, parts;
+  float* partials;
   // output: bf16 [*, ld] by row (plain); h by aligned row (gate_up: fp32
   // [rows, ld], or from the tiled kernel codes [rows, ld] and scales hs
   // [rows, ld / 128]); fp32 y [slots, ld] by flat slot (down)
@@ -365,6 +369,7 @@ hipError_t launch_f8_pack(const uint8_t* q, const float* s, int E, int N, int K,
                           uint8_t* dst, hipStream_t stream);
 hipError_t launch_f8_quantize(const F8QuantArgs& a, hipStream_t stream);
 hipError_t launch_f8_gemm(const F8GemmArgs& a, hipStream_t stream);
+// small: the form over alignment blocks of at most 32 rows (gate_up and down).
 hipError_t launch_f8_tile(const F8GemmArgs& a, bool small, hipStream_t stream);
 // Down product of the small form with K <= 256 (block_m at most 32).
 hipError_t launch_f8_short_down(const F8GemmArgs& a, hipStream_t stream);

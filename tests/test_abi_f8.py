@@ -80,7 +80,7 @@ def _handle(role, E=1, N=256, K=256):
 
 
 def _gemm(h, codes=FAKE, s=FAKE, M=4, out=FAKE, ld=256):
-    return C.lib.chord_f8_gemm(codes, s, M, None if h is None else ctypes.byref(h), out, ld, None)
+    return C.lib.chord_f8_gemm(codes, s, M, None if h is None else ctypes.byref(h), out, ld, FAKE, 1 << 30, None)
 
 
 def test_gemm_refusals():
