@@ -24,7 +24,7 @@ LIB = os.path.join(PKG, "libchord.so")
 SOURCES = ["runtime.cpp", "align.hip", "pack.hip", "moe_kernels.hip", "gemm_stream.hip",
            "gemm_tile.hip", "dispatch.hip", "f8_runtime.cpp", "route.hip", "f8_quantize.hip",
            "f8_gemm.hip", "f8_tile.hip",
-           "f8_short.hip"]
+           "f8_short.hip", "f8_small.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

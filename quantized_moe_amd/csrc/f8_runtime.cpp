@@ -372,6 +372,29 @@ chord_status chord_f8_moe(const chord_bf16* x, int T, int H, int I, const chord_
   CHORD_CHECK(check_device(&cus));
   hipStream_t st = static_cast<hipStream_t>(stream);
   uint8_t* p = static_cast<uint8_t*>(workspace);
+  if (f8_small_fits(T, k, H, I)) {
+    const F8GemmArgs w13a = weight_args(w13, kF8GateUp, cus), w2a = weight_args(w2, kF8Down, cus);
+    F8SmallArgs s{};
+    s.x = x;
+    s.T = T;
+    s.k = k;
+    s.H = H;
+    s.I = I;
+    s.topk_ids = topk_ids;
+    s.topk_weights = topk_weights;
+    s.expert_begin = expert_begin;
+    s.num_experts = E_l;
+    s.w13 = w13a.wq;
+    s.s13 = w13a.ws;
+    s.w2 = w2a.wq;
+    s.s2 = w2a.ws;
+    s.h = reinterpret_cast<float*>(p + ws.h);
+    s.out = out;
+    s.num_cus = cus;
+    HIP_TRY(launch_f8_small(s, st), "small layer launch");
+    set_last_plan("f8 moe: a handful of tokens, two launches");
+    return CHORD_OK;
+  }
   int32_t* sorted = reinterpret_cast<int32_t*>(p + ws.sorted);
   int32_t* experts = reinterpret_cast<int32_t*>(p + ws.experts);
   int32_t* ntpp = reinterpret_cast<int32_t*>(p + ws.ntpp);

@@ -330,6 +330,21 @@ struct F8GemmArgs {
   float* hs;
 };
 
+// The layer in two launches (f8_small_fits: T <= kFusedMaxTokens, T * k <=
+// kFusedMaxSlots, rows that fit LDS).
+struct F8SmallArgs {
+  const uint16_t* x;  // bf16 [T, H]
+  int T, k, H, I;
+  const int32_t* topk_ids;
+  const float* topk_weights;
+  int expert_begin, num_experts;
+  const uint8_t *w13, *w2;  // packed codes
+  const float *s13, *s2;    // block scales
+  float* h;                 // [T * k, I]
+  uint16_t* out;            // bf16 [T, H]
+  int num_cus;
+};
+
 struct F8CombineArgs {
   const float* y;           // [T * k, H], rows of local slots
   const int32_t* topk_ids;  // [T, k]
@@ -373,6 +388,8 @@ hipError_t launch_f8_gemm(const F8GemmArgs& a, hipStream_t stream);
 hipError_t launch_f8_tile(const F8GemmArgs& a, bool small, hipStream_t stream);
 // Down product of the small form with K <= 256 (block_m at most 32).
 hipError_t launch_f8_short_down(const F8GemmArgs& a, hipStream_t stream);
+bool f8_small_fits(int T, int k, int H, int I);
+hipError_t launch_f8_small(const F8SmallArgs& a, hipStream_t stream);
 hipError_t launch_f8_combine(const F8CombineArgs& a, hipStream_t stream);
 
 constexpr int kAlignSingle = 8192;      // align in one workgroup up to this many entries
