@@ -43,6 +43,14 @@ __device__ __forceinline__ uint32_t f8_pack4(float a, float b, float c, float d)
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
 }
 
+// Two fp32 -> packed fp16 pair, nearest even.
+__device__ __forceinline__ uint32_t pk_f16(float a, float b) {
+  half2_t r;
+  r[0] = (_Float16)a;
+  r[1] = (_Float16)b;
+  return __builtin_bit_cast(uint32_t, r);
+}
+
 // Unsigned maximum over the 16 lanes of a row, in every lane (register moves:
 // neighbours 1 and 2 away, then the mirrored half row and row).
 __device__ __forceinline__ uint32_t row_max16(uint32_t x) {

@@ -117,42 +117,87 @@ __global__ __launch_bounds__(kThreads) void copy_scales(const float* __restrict_
     dst[i] = s[i];
 }
 
-// out[t] = bf16(sum over local slots, ascending, of w * y), rounded once: y stays
-// in fp32 between the down product and this sum (rounding it to bf16 there
-// made the layer's error 1.6 times that of one rounding).  One thread per 4
-// outputs; a token's ids and weights are read by every thread of its row (the
-// caches serve them), all rows of up to 8 slots in flight together.
-__global__ __launch_bounds__(kThreads) void combine_f32(F8CombineArgs a) {
-  const int nvec = a.H / 4;
-  const int spans = (nvec + kThreads - 1) / kThreads;
-  const int t = blockIdx.x / spans;
-  const int v = (blockIdx.x % spans) * kThreads + threadIdx.x;
+// out[t] = bf16(sum over local slots, ascending, of w * y), rounded once: y comes
+// in fp32, or in fp16 with a unit for each 256 outputs (rounding it to bf16
+// there made the layer's error 1.6 times that of one rounding).  A wave owns 64
+// x kPieces 16-byte pieces of one token's row, so ids and weights are uniform:
+// scalar loads, and no load at all for a slot without a row; two slots of a batch
+// are on their way together (8192 tokens with one local slot each: batches of 2,
+// 4, 8 take 44.5, 50, 62 us, the registers of larger ones cost waves; one thread
+// per 16 bytes with its own ids 84).  Bound by memory.
+constexpr int kCombineWaves = 4;
+constexpr int kPieces = 2;
+
+template <bool F16>
+__global__ __launch_bounds__(64 * kCombineWaves) void combine_slots(F8CombineArgs a) {
+  constexpr int P = F16 ? 8 : 4, B = 2;  // outputs per piece, slots per batch
+  const int nvec = a.H / P, spans = (nvec + 64 * kPieces - 1) / (64 * kPieces);
+  const int64_t wid = (int64_t)blockIdx.x * kCombineWaves + (threadIdx.x >> 6);
+  const int t = __builtin_amdgcn_readfirstlane((int)(wid / spans));
+  if (t >= a.T) return;
+  const int v0 = __builtin_amdgcn_readfirstlane((int)(wid - (int64_t)t * spans)) * 64 * kPieces +
+                 (int)(threadIdx.x & 63);
   const int64_t s0 = (int64_t)t * a.k;
-  constexpr int B = 8;
-  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+  const int slices = (a.H + 255) / 256;
+  float acc[kPieces][P];
+#pragma unroll
+  for (int p = 0; p < kPieces; ++p)
+#pragma unroll
+    for (int i = 0; i < P; ++i) acc[p][i] = 0.f;
   for (int j0 = 0; j0 < a.k; j0 += B) {
-    f32x4_t y[B];
-    float w[B];
+    bool local[B];
 #pragma unroll
     for (int u = 0; u < B; ++u) {
-      y[u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      w[u] = 0.f;
-      const int e = j0 + u < a.k ? a.topk_ids[s0 + j0 + u] : INT32_MIN;
+      const int e = a.topk_ids[s0 + min(j0 + u, a.k - 1)];
       // (unsigned difference: no id, however far off, wraps into the range)
-      if (e >= a.expert_begin && (uint32_t)e - (uint32_t)a.expert_begin < (uint32_t)a.num_experts) {
-        w[u] = a.topk_weights[s0 + j0 + u];
-        if (v < nvec) y[u] = __builtin_nontemporal_load(
-            reinterpret_cast<const f32x4_t*>(a.y + (s0 + j0 + u) * a.H) + v);
+      local[u] = j0 + u < a.k && e >= a.expert_begin &&
+                 (uint32_t)e - (uint32_t)a.expert_begin < (uint32_t)a.num_experts;
+    }
+    u32x4_t y[B][kPieces];
+    float w[B], unit[B][kPieces];
+#pragma unroll
+    for (int u = 0; u < B; ++u) {
+      if (!local[u]) continue;
+      const int64_t f = s0 + j0 + u;
+      w[u] = a.topk_weights[f];
+      const uint8_t* row = reinterpret_cast<const uint8_t*>(a.y) + f * a.H * (F16 ? 2 : 4);
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p) {
+        const int v = min(v0 + 64 * p, nvec - 1);
+        y[u][p] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(row) + v);
+        unit[u][p] = F16 ? a.ys[f * slices + v / 32] : 1.f;
       }
     }
 #pragma unroll
-    for (int u = 0; u < B; ++u)
+    for (int u = 0; u < B; ++u) {
+      if (!local[u]) continue;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(w[u], y[u][i], acc[i]);
+      for (int p = 0; p < kPieces; ++p) {
+        const float wu = w[u] * unit[u][p];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (F16) {
+            const half2_t h = __builtin_bit_cast(half2_t, (uint32_t)y[u][p][i]);
+            acc[p][2 * i] = __builtin_fmaf(wu, (float)h[0], acc[p][2 * i]);
+            acc[p][2 * i + 1] = __builtin_fmaf(wu, (float)h[1], acc[p][2 * i + 1]);
+          } else {
+            acc[p][i] = __builtin_fmaf(wu, __uint_as_float(y[u][p][i]), acc[p][i]);
+          }
+        }
+      }
+    }
   }
-  if (v < nvec)
-    *reinterpret_cast<uint2*>(a.out + (int64_t)t * a.H + v * 4) =
-        make_uint2(pk_bf16(acc[0], acc[1]), pk_bf16(acc[2], acc[3]));
+#pragma unroll
+  for (int p = 0; p < kPieces; ++p) {
+    const int v = v0 + 64 * p;
+    if (v >= nvec) continue;
+    uint16_t* o = a.out + (int64_t)t * a.H + (int64_t)v * P;
+    if constexpr (F16)
+      *reinterpret_cast<uint4*>(o) = make_uint4(pk_bf16(acc[p][0], acc[p][1]), pk_bf16(acc[p][2], acc[p][3]),
+                                                pk_bf16(acc[p][4], acc[p][5]), pk_bf16(acc[p][6], acc[p][7]));
+    else
+      *reinterpret_cast<uint2*>(o) = make_uint2(pk_bf16(acc[p][0], acc[p][1]), pk_bf16(acc[p][2], acc[p][3]));
+  }
 }
 
 unsigned grid_for(int64_t n, int64_t per, int64_t most) {
@@ -175,8 +220,11 @@ hipError_t launch_f8_quantize(const F8QuantArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_f8_combine(const F8CombineArgs& a, hipStream_t stream) {
-  const int spans = (a.H / 4 + kThreads - 1) / kThreads;
-  hipLaunchKernelGGL(combine_f32, dim3((unsigned)(a.T * spans)), dim3(kThreads), 0, stream, a);
+  const int per = 64 * kPieces * (a.ys != nullptr ? 8 : 4);
+  const int64_t waves = (int64_t)a.T * ((a.H + per - 1) / per);
+  const dim3 grid((unsigned)((waves + kCombineWaves - 1) / kCombineWaves)), block(64 * kCombineWaves);
+  if (a.ys != nullptr) hipLaunchKernelGGL((combine_slots<true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((combine_slots<false>), grid, block, 0, stream, a);
   return hipGetLastError();
 }
 

@@ -1,4 +1,4 @@
-// The W8A8 layer for a handful of tokens (T <= 16, T * k <= 64) in two launches.
+// The W8A8 layer for a handful of tokens (T * k <= 32) in two launches.
 // With one token the weights of its experts take about ten microseconds, and each
 // further launch in front of or between the two products four to five, so here
 // every workgroup groups the slots by expert itself (one wave, one ballot per
@@ -231,8 +231,13 @@ __global__ __launch_bounds__(kThreads) void small_down(F8SmallArgs a) {
 constexpr int64_t kRowBytes = 68 << 10;
 int64_t row_bytes(int64_t rows, int K) { return rows * (K + K / kF8Block * 4); }
 
+// Every workgroup quantises all rows, so with more slots the other forms win:
+// T * k = 32 (48 experts of 2048 x 7168) 198 us here, 216 there; 63 (I = 256) 89
+// and 85; 64 (16 experts of 1024 x 2048) 52 and 43.
+constexpr int kSmallSlots = 32;
+
 bool f8_small_fits(int T, int k, int H, int I) {
-  return T <= kFusedMaxTokens && (int64_t)T * k <= kFusedMaxSlots && row_bytes(T, H) <= kRowBytes &&
+  return T <= kFusedMaxTokens && (int64_t)T * k <= kSmallSlots && row_bytes(T, H) <= kRowBytes &&
          row_bytes((int64_t)T * k, I) <= kRowBytes;
 }
 

@@ -324,14 +324,16 @@ struct F8GemmArgs {
   float* partials;
   // output: bf16 [*, ld] by row (plain); h by aligned row (gate_up: fp32
   // [rows, ld], or from the tiled kernel codes [rows, ld] and scales hs
-  // [rows, ld / 128]); fp32 y [slots, ld] by flat slot (down)
+  // [rows, ld / 128]); y by flat slot (down: fp32 [slots, ld], or from the
+  // tiled kernel's large form fp16 [slots, ld] in units of ys [slots, slices of
+  // 256 outputs])
   void* out;
   int64_t ld;
   float* hs;
+  float* ys;
 };
 
-// The layer in two launches (f8_small_fits: T <= kFusedMaxTokens, T * k <=
-// kFusedMaxSlots, rows that fit LDS).
+// The layer in two launches (where f8_small_fits).
 struct F8SmallArgs {
   const uint16_t* x;  // bf16 [T, H]
   int T, k, H, I;
@@ -347,6 +349,7 @@ struct F8SmallArgs {
 
 struct F8CombineArgs {
   const float* y;           // [T * k, H], rows of local slots
+  const float* ys;          // null, or y is fp16 in these units [T * k, ceil(H / 256)]
   const int32_t* topk_ids;  // [T, k]
   const float* topk_weights;
   int T, k, H;
