@@ -79,8 +79,8 @@ def _handle(role, E=1, N=256, K=256):
     return h
 
 
-def _gemm(h, codes=FAKE, s=FAKE, M=4, out=FAKE, ld=256):
-    return C.lib.chord_f8_gemm(codes, s, M, None if h is None else ctypes.byref(h), out, ld, FAKE, 1 << 30, None)
+def _gemm(h, codes=FAKE, s=FAKE, M=4, out=FAKE, ld=256, ws=FAKE, n=1 << 30):
+    return C.lib.chord_f8_gemm(codes, s, M, None if h is None else ctypes.byref(h), out, ld, ws, n, None)
 
 
 def test_gemm_refusals():
@@ -102,6 +102,20 @@ def test_gemm_refusals():
     bad = _handle(2)
     bad.block = 64
     assert _gemm(bad) == UNSUPPORTED
+
+
+def test_gemm_workspace():
+    """Only products with K in parts need one; it has to be there, whole and aligned."""
+    assert C.chord_f8_gemm_workspace_bytes(1, 4096, 7168) == 0
+    assert C.chord_f8_gemm_workspace_bytes(8192, 4096, 7168) == 0
+    need = C.chord_f8_gemm_workspace_bytes(200, 520, 4000)
+    assert need > 0 and need % (200 * 528 * 4) == 0
+    h = _handle(2, N=520, K=4000)
+    assert _gemm(h, M=200, ld=520, ws=None) == WORKSPACE
+    assert _gemm(h, M=200, ld=520, n=need - 1) == WORKSPACE
+    assert _gemm(h, M=200, ld=520, ws=ODD) == WORKSPACE
+    for bad in ((-1, 300, 4096), (150, 0, 4096), (150, 300, 0), (150, 1 << 16, 1 << 16), (1, 16, 1 << 23)):
+        assert C.chord_f8_gemm_workspace_bytes(*bad) == 0
 
 
 def _moe(w13=None, w2=None, x=FAKE, T=4, H=256, I=128, k=2, ids=FAKE, out=FAKE, ws=FAKE, n=1 << 30):

@@ -124,17 +124,19 @@ def test_gemm_rows(C, M, N, K):
 @pytest.mark.parametrize("M,N,K", [
     (1, 1, 1), (3, 7, 128), (20, 17, 129), (1, 16, 1), (40, 128, 4096), (9, 2112, 1536), (130, 130, 130),
     (70, 513, 1290), (300, 1000, 384), (515, 776, 640), (1, 4096, 7168), (2000, 96, 256),
+    # K in 8, 4 and 6 parts, uneven ones, a ragged last chunk; long rows without
+    (200, 520, 4000), (333, 1025, 2500), (120, 2100, 3000), (70, 300, 7168), (700, 2000, 1800),
 ])
 def test_gemm_odd_sizes(C, M, N, K):
     banner(f"gemm M={M} N={N} K={K}")
     check_gemm(C, M, N, K, seed=M + N)
 
 
-@pytest.mark.parametrize("M", [5, 300])
-def test_gemm_strided_output_leaves_the_rest(C, M):
-    for off, ld, N in ((0, 512, 300), (3, 333, 300), (4, 512, 256)):
+@pytest.mark.parametrize("M,K", [(5, 384), (300, 384), (300, 4096)])
+def test_gemm_strided_output_leaves_the_rest(C, M, K):
+    for off, ld, N in ((0, 1024, 600), (3, 633, 600), (4, 1024, 512)):
         buf = torch.full((M + 2, ld), 7.0, dtype=torch.bfloat16, device="cuda")
-        check_gemm(C, M, N, 384, out=buf[1:M + 1, off:off + N])
+        check_gemm(C, M, N, K, out=buf[1:M + 1, off:off + N])
         b = f64(buf)
         assert np.all(b[0] == 7) and np.all(b[M + 1] == 7)
         assert np.all(b[:, :off] == 7) and np.all(b[:, off + N:] == 7)
@@ -151,6 +153,50 @@ def test_gemm_nan_rows_stay_rows(C):
         bad = np.isnan(got)
         assert bad[3].all() and bad[M - 1].all()
         assert not np.delete(bad, [3, M - 1], axis=0).any()
+
+
+def test_gemm_random_sizes(C):
+    rng = np.random.default_rng(11)
+    for _ in range(25):
+        M, N, K = (int(np.exp(rng.uniform(np.log(lo), np.log(hi)))) for lo, hi in ((1, 1500), (1, 1500), (1, 3000)))
+        banner(f"gemm random M={M} N={N} K={K}")
+        check_gemm(C, M, N, K, seed=M)
+
+
+def test_gemm_workspace_and_graphs(C):
+    """A product with K in parts: its workspace is checked, two streams at once and
+    graphs that replay in turn equal the eager call."""
+    M, N, K = 200, 520, 4000
+    codes, scales, _ = weights(1, N, K, 6)
+    w = C.chord_f8_pack(C.ROLE_PLAIN, codes.cuda(), scales.cuda())
+    sets = [C.chord_f8_quantize(activations(M, K, s).cuda()) for s in (1, 2)]
+    need = C.chord_f8_gemm_workspace_bytes(M, N, K)
+    assert need > 0
+    with pytest.raises(C.ChordError):
+        C.chord_f8_gemm(*sets[0], w, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+    want = [C.chord_f8_gemm(*a, w, workspace=torch.empty(need, dtype=torch.uint8, device="cuda")) for a in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = [C.chord_f8_gemm(*a, w, stream=s) for a, s in zip(sets, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graphs, outs = [], []
+    for a in sets:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(C.chord_f8_gemm(*a, w))
+        graphs.append(gr)
+    for rep in range(3):
+        for i in (0, 1):
+            for dst, src in zip(sets[i], C.chord_f8_quantize(activations(M, K, 30 + 2 * rep + i).cuda())):
+                dst.copy_(src)
+        graphs[0].replay()
+        graphs[1].replay()
+        torch.cuda.synchronize()
+        again = [C.chord_f8_gemm(*a, w) for a in sets]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, again))
 
 
 def test_linear_module_and_empty(C):
@@ -207,6 +253,13 @@ MOE_CASES = [
     (700, 256, 256, 8, 8, 3, 0, 0),
     (50, 256, 128, 300, 300, 5, 0, 0),     # mostly one row an expert
     (40, 256, 128, 16, 4, 2, 100, 0),      # no local expert
+    (3, 256, 128, 16, 4, 2, 100, 0),       # no local expert, two-launch form
+    (16, 256, 128, 2, 2, 2, 0, 0),         # two-launch form, a full tile and a second one
+    (4, 2048, 640, 40, 20, 8, 10, 0),      # two-launch form, 32 slots
+    (40, 256, 256, 100, 100, 2, 0, 0),     # blocks of 16 rows, K = 256 down
+    (70, 256, 128, 8, 8, 2, 0, 0),         # blocks of 32 rows, K = 128 down
+    (60, 384, 1152, 5, 5, 1, 0, 0),        # blocks of 32 rows, partial slices
+    (200, 128, 2048, 130, 130, 4, 0, 0),   # many blocks of 16 rows
 ]
 
 
@@ -261,7 +314,7 @@ def test_route_and_layers_together(C, T):
     assert np.array_equal(np.sort(s[s < T * 4]), local)
 
 
-@pytest.mark.parametrize("T", [5, 120])
+@pytest.mark.parametrize("T", [5, 40, 120])
 def test_moe_streams_and_graphs(C, T):
     """One layer on two streams at once, and captured in two graphs that replay
     in turn with eager calls between: all equal to the eager call."""
@@ -294,6 +347,38 @@ def test_moe_streams_and_graphs(C, T):
         again = [layer.indexed(*a, 0, 8) for a in sets]
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, again))
+
+
+@pytest.mark.parametrize("T,E", [(3, 4), (30, 40), (60, 8), (200, 4)])
+def test_moe_nan_tokens_stay_tokens(C, T, E):
+    layer, _, _ = make_layer(E, 512, 384, 13)
+    x = activations(T, 512, 2)
+    ids, w = routing(T, E, 2, 3)
+    args = torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda(), 0, E
+    want = f64(layer.indexed(x.cuda(), *args))
+    x[1, 100], x[T - 1, 511] = float("nan"), float("-inf")
+    got = f64(layer.indexed(x.cuda(), *args))
+    assert np.isnan(got[1]).all() and np.isnan(got[T - 1]).all()
+    keep = np.delete(np.arange(T), [1, T - 1])
+    assert np.array_equal(got[keep], want[keep])
+
+
+def test_moe_extreme_values(C):
+    """Tokens of zeros, and weights so small or large that h and y leave bf16's and
+    fp16's comfortable range: zero stays zero, magnitudes are kept."""
+    from quantized_moe_amd.moe import W8A8MoE
+    for T, E in ((4, 4), (100, 2)):
+        for size in (1e-8, 1e8):
+            c13, s13, _ = weights(E, 256, 256, 4)
+            c2, s2, _ = weights(E, 256, 128, 5)
+            layer = W8A8MoE(c13.cuda(), s13.cuda(), c2.cuda(), (s2 * size).cuda())
+            d13 = np.stack([f8.dequantize_weight(f64(c13[e].float()), f64(s13[e])) for e in range(E)])
+            d2 = np.stack([f8.dequantize_weight(f64(c2[e].float()), f64((s2 * size)[e])) for e in range(E)])
+            ids, w = routing(T, E, 2, 6)
+            x = activations(T, 256, 7)
+            x[2] = 0
+            got = check_moe(layer, d13, d2, x, ids, w, 0, E)
+            assert not f64(got)[2].any()
 
 
 def test_moe_refused_tensors(C):
