@@ -198,13 +198,20 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
 
   // Chunk c in buffer b (= c % 4; its group 0 and that group's scales are in
   // registers; half: which of the scales are its own).
-  // Load indices past the end repeat the last chunk, so every chunk issues the
-  // same loads and the counts are exact.  At the barrier only these may be
-  // younger than the tokens of chunk c + 1: a chunk's weights, the tokens of
-  // chunk c + 2 with (in two chunks of four) half of the next scales in front
+  // In the loop, load indices past the end repeat the last chunk, so every chunk
+  // issues the same loads and the counts are exact.  At the barrier only these
+  // may be younger than the tokens of chunk c + 1: a chunk's weights, the tokens
+  // of chunk c + 2 with (in two chunks of four) half of the next scales in front
   // of them, and this chunk's weights.
+  // Behind the loop (last) nothing is loaded any more, but for the next chunk's
+  // weights where they are only one chunk ahead; the counts there take no weights
+  // for granted, since the compiler drops loads whose registers nobody reads.
+  // (With one chunk ahead the chunk's own weights, already waited for, are
+  // younger than the tokens of chunk c + 1.)
   constexpr int kBehind = 2 * kW + kDma;
-  auto chunk = [&](int b, int c, int half) {
+  constexpr int kBehindLast = WR == 4 ? 0 : kW;
+  auto chunk = [&](int b, int c, int half, auto is_last) {
+    constexpr bool last = decltype(is_last)::value;
     const int nb = (b + 1) % kStages, fb = (b + 3) % kStages;
     const int c1 = min(c + 1, nc - 1), c3 = min(c + 3, nc - 1);
     const float n0 = s0[c1], n1 = s1[c1];
@@ -216,8 +223,10 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
     // waits for its result).
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      if (g == G / 2 && (b == 1 || b == 2)) barrier(std::integral_constant<int, kBehind + 1>{});
-      if (g == G / 2 && (b == 0 || b == 3)) barrier(std::integral_constant<int, kBehind>{});
+      if (g == G / 2 && !last && (b == 1 || b == 2)) barrier(std::integral_constant<int, kBehind + 1>{});
+      if (g == G / 2 && !last && (b == 0 || b == 3)) barrier(std::integral_constant<int, kBehind>{});
+      if (g == G / 2 && last && b == 0) barrier(std::integral_constant<int, kBehindLast + kDma>{});
+      if (g == G / 2 && last && b == 1) barrier(std::integral_constant<int, kBehindLast>{});
       r[g & 1][0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w0, xv[g & 1], zero, 0, 0, 0, 0, 0, 0);
       xv[(g + 1) & 1] = g + 1 < G ? read_x(b, g + 1) : read_x(nb, 0);
       scale_in(0, (g + G - 1) % G);
@@ -229,11 +238,11 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
       sx[(g + 1) & 1] = g + 1 < G ? read_s(half, b, g + 1) : read_s(b == 3 ? 1 - half : half, nb, 0);
 #pragma unroll
       for (int j = 0; j < kW; ++j)
-        if (g < G / 2 && j * (G / 2) / kW == g) load_w(j, (b + WR - 1) % WR, WR == 4 ? c3 : c1);
-      if (g == G / 2 && b < 2) load_s(b, 1 - half, c - b + 4);
+        if ((!last || WR == 2) && g < G / 2 && j * (G / 2) / kW == g) load_w(j, (b + WR - 1) % WR, WR == 4 ? c3 : c1);
+      if (!last && g == G / 2 && b < 2) load_s(b, 1 - half, c - b + 4);
 #pragma unroll
       for (int j = 0; j < kDma; ++j)
-        if (g >= G / 2 && j * (G / 2) / kDma == g - G / 2) load_x(j, fb, c3);
+        if (!last && g >= G / 2 && j * (G / 2) / kDma == g - G / 2) load_x(j, fb, c3);
       __builtin_amdgcn_sched_barrier(0);
     }
     sw0 = n0;
@@ -257,23 +266,28 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
   load_s(0, 0, 0);
   load_s(1, 0, 0);
   load_all_x(0);
+  __builtin_amdgcn_sched_barrier(0);
   load_all_x(1);
+  __builtin_amdgcn_sched_barrier(0);
   load_all_w(WR == 4 ? 2 : 0);
+  __builtin_amdgcn_sched_barrier(0);
   load_all_x(2);
   barrier(std::integral_constant<int, kW + 2 * kDma>{});
   xv[0] = read_x(0, 0);
   sx[0] = read_s(0, 0, 0);
   int c = 0, half = 0;
+  const std::false_type in_loop;
+  const std::true_type behind_loop;
   for (; c + 3 < nc; c += 4) {
-    chunk(0, c, half);
-    chunk(1, c + 1, half);
-    chunk(2, c + 2, half);
-    chunk(3, c + 3, half);
+    chunk(0, c, half, in_loop);
+    chunk(1, c + 1, half, in_loop);
+    chunk(2, c + 2, half, in_loop);
+    chunk(3, c + 3, half, in_loop);
     half = 1 - half;
   }
-  if (c < nc) chunk(0, c, half);
-  if (c + 1 < nc) chunk(1, c + 1, half);
-  if (c + 2 < nc) chunk(2, c + 2, half);
+  if (c < nc) chunk(0, c, half, behind_loop);
+  if (c + 1 < nc) chunk(1, c + 1, half, behind_loop);
+  if (c + 2 < nc) chunk(2, c + 2, half, behind_loop);
   scale_in(0, G - 1);
   scale_in(1, G - 1);
   // The repeated loads at the end land before their buffers are used again.

@@ -393,3 +393,48 @@ def test_moe_refused_tensors(C):
         a.update(bad)
         with pytest.raises(C.ChordError):
             layer.indexed(a.pop("x"), a.pop("ids"), a.pop("w"), **a)
+
+
+# -- chunks behind the tile kernel's loop of four --------------------------------
+
+def cold_calls(run, n=6):
+    """Results of n calls, each after its inputs were pushed out of the caches by
+    0.5 GB of other work that is still running when the call is queued."""
+    junk = torch.empty(1 << 27, device="cuda")
+    outs = []
+    for i in range(n):
+        junk.fill_(i)
+        outs.append(run())
+    torch.cuda.synchronize()
+    return outs
+
+
+@pytest.mark.parametrize("M", [40, 64, 100, 160, 200, 256])
+@pytest.mark.parametrize("K", [7168, 6656, 1664, 1152, 384, 640])
+def test_gemm_chunks_behind_the_loop(C, M, K):
+    """1, 2 and 3 chunks behind the loop, of every part of K and tile height: the
+    tokens' copies into shared memory are waited for there too."""
+    N = 1056
+    codes, scales, deq = weights(1, N, K, M + K)
+    w = C.chord_f8_pack(C.ROLE_PLAIN, codes.cuda(), scales.cuda())
+    q, s = C.chord_f8_quantize(activations(M, K, M).cuda())
+    a = f8.dequantize(f8.decode(host(q.view(torch.uint8))), f64(s))[:, :K]
+    ref, bound = f8.gemm(a, deq[0])
+    bound = bound + f8.HALF_BF16 * (np.abs(ref) + bound)
+    for got in cold_calls(lambda: C.chord_f8_gemm(q, s, w)):
+        assert np.all(np.abs(f64(got) - ref) <= bound)
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [
+    (70, 16, 2, 640, 384), (70, 16, 2, 768, 640), (60, 40, 4, 896, 768), (300, 4, 2, 640, 896),
+    (300, 4, 2, 1792, 640), (400, 4, 1, 768, 768), (150, 2, 2, 384, 1152),
+])
+def test_moe_chunks_behind_the_loop(C, T, E, k, H, I):
+    layer, d13, d2 = make_layer(E, H, I, T + H)
+    ids, w = routing(T, E, k, I)
+    x = activations(T, H, 3)
+    ref, bound, norm = f8.moe(f64(x), ids, w, d13, d2, 0)
+    xg, ig, wg = x.cuda(), torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda()
+    for got in cold_calls(lambda: layer.indexed(xg, ig, wg, 0, E)):
+        err = np.abs(f64(got) - ref)
+        assert np.all(err <= bound) and np.linalg.norm(err) <= norm
