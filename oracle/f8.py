@@ -144,6 +144,9 @@ def moe(x, topk_ids, topk_weights, w13, w2, expert_begin):
         hd = dequantize(val, s)
         y, dy = gemm(hd, w2[e])
         dy = dy + (flip + np.abs(hd) * wide(rel)) @ np.abs(w2[e]).T
+        # y is kept in fp16 with a power of two per 32 outputs: half a step
+        top = np.abs(y).reshape(n, -1, 32).max(axis=2)
+        dy = dy + 2.0 ** -11 * (np.abs(y) + dy) + 2.0 ** -25 * np.repeat(top, 32, axis=1)
         c = topk_weights[t, j].astype(np.float64)[:, None]
         np.add.at(out, t, c * y)
         np.add.at(bound, t, np.abs(c) * (dy + (k + 2) * U32 * (np.abs(y) + dy)))

@@ -51,6 +51,41 @@ __device__ __forceinline__ uint32_t pk_f16(float a, float b) {
   return __builtin_bit_cast(uint32_t, r);
 }
 
+// y of a layer's slot between the down product and the sum over slots: fp16 in
+// units of a power of two per 32 outputs, the exponent of the largest of them
+// (biased, one byte).  Scaling by it is exact, so a value is off by half a step of
+// fp16, 2^-11 of itself, and by 2^-25 units where it is far below the largest: an
+// eighth of the rounding to bf16 that follows the sum, for half the bytes of fp32.
+constexpr int kF8YBlock = 32;
+// Exponent for a largest magnitude with these bits (1 .. 253, so that the unit
+// and its inverse are normal; infinities and NaN stay what they are in fp16).
+__device__ __forceinline__ uint32_t f8_y_exponent(uint32_t abs_bits) {
+  return min(max(abs_bits >> 23, 1u), 253u);
+}
+// A matrix instruction's results for 32 outputs of a token, a of the first 16
+// and b of the next, four in each lane of a quarter wave q: their exponent, and
+// as 16 bytes of fp16 the 8 outputs at 16 (q & 1) + 8 (q >> 1).
+__device__ __forceinline__ uint32_t f8_y_pack(f32x4_t a, f32x4_t b, u32x4_t& out) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    m = max(m, max(__float_as_uint(a[i]) & 0x7FFFFFFFu, __float_as_uint(b[i]) & 0x7FFFFFFFu));
+  // Swaps of odd quarters with even ones, and of halves: the maximum over q.
+  auto s = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+  m = max((uint32_t)s[0], (uint32_t)s[1]);
+  s = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+  m = max((uint32_t)s[0], (uint32_t)s[1]);
+  const uint32_t e = f8_y_exponent(m);
+  const float inv = __uint_as_float((254u - e) << 23);
+  // The same swap brings a's neighbours together in even quarters, b's in odd.
+  const auto lo = __builtin_amdgcn_permlane16_swap(pk_f16(a[0] * inv, a[1] * inv),
+                                                   pk_f16(b[0] * inv, b[1] * inv), false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap(pk_f16(a[2] * inv, a[3] * inv),
+                                                   pk_f16(b[2] * inv, b[3] * inv), false, false);
+  out = u32x4_t{(uint32_t)lo[0], (uint32_t)hi[0], (uint32_t)lo[1], (uint32_t)hi[1]};
+  return e;
+}
+
 // Unsigned maximum over the 16 lanes of a row, in every lane (register moves:
 // neighbours 1 and 2 away, then the mirrored half row and row).
 __device__ __forceinline__ uint32_t row_max16(uint32_t x) {

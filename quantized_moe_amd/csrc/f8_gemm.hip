@@ -180,9 +180,6 @@ __global__ __launch_bounds__(64 * WK) void f8_stream(F8GemmArgs a) {
         if (a.kind == kF8GateUp) {
           float* h = static_cast<float*>(a.out) + dst[m] * a.ld + (tile0 + n) * 8 + 2 * q;
           *reinterpret_cast<float2*>(h) = make_float2(silu_mul(v[0], v[1]), silu_mul(v[2], v[3]));
-        } else if (a.kind == kF8Down) {
-          float* y = static_cast<float*>(a.out) + dst[m] * a.ld + (tile0 + n) * 16 + 4 * q;
-          *reinterpret_cast<f32x4_t*>(y) = v;
         } else {
           store4(static_cast<uint16_t*>(a.out), dst[m], a.ld, (tile0 + n) * 16 + 4 * q, a.N, v, wide);
         }

@@ -117,33 +117,31 @@ __global__ __launch_bounds__(kThreads) void copy_scales(const float* __restrict_
     dst[i] = s[i];
 }
 
-// out[t] = bf16(sum over local slots, ascending, of w * y), rounded once: y comes
-// in fp32, or in fp16 with a unit for each 256 outputs (rounding it to bf16
-// there made the layer's error 1.6 times that of one rounding).  A wave owns 64
-// x kPieces 16-byte pieces of one token's row, so ids and weights are uniform:
-// scalar loads, and no load at all for a slot without a row; two slots of a batch
-// are on their way together (8192 tokens with one local slot each: batches of 2,
-// 4, 8 take 44.5, 50, 62 us, the registers of larger ones cost waves; one thread
-// per 16 bytes with its own ids 84).  Bound by memory.
+// out[t] = bf16(sum over local slots, ascending, of w * y), rounded once.  A wave
+// owns 64 x kPieces 16-byte pieces of one token's row, so ids and weights are
+// uniform: scalar loads, and no load at all for a slot without a row; two slots
+// of a batch are on their way together (8192 tokens with one local slot each:
+// batches of 2, 4, 8 take 44.5, 50, 62 us, the registers of larger ones cost
+// waves; one thread per 16 bytes with its own ids 84).  Bound by memory.
 constexpr int kCombineWaves = 4;
 constexpr int kPieces = 2;
+constexpr int kPiece = 8;  // outputs per piece
 
-template <bool F16>
 __global__ __launch_bounds__(64 * kCombineWaves) void combine_slots(F8CombineArgs a) {
-  constexpr int P = F16 ? 8 : 4, B = 2;  // outputs per piece, slots per batch
-  const int nvec = a.H / P, spans = (nvec + 64 * kPieces - 1) / (64 * kPieces);
+  constexpr int B = 2;  // slots per batch
+  const int nvec = a.H / kPiece, spans = (nvec + 64 * kPieces - 1) / (64 * kPieces);
   const int64_t wid = (int64_t)blockIdx.x * kCombineWaves + (threadIdx.x >> 6);
   const int t = __builtin_amdgcn_readfirstlane((int)(wid / spans));
   if (t >= a.T) return;
   const int v0 = __builtin_amdgcn_readfirstlane((int)(wid - (int64_t)t * spans)) * 64 * kPieces +
                  (int)(threadIdx.x & 63);
   const int64_t s0 = (int64_t)t * a.k;
-  const int slices = (a.H + 255) / 256;
-  float acc[kPieces][P];
+  const int blocks = a.H / kF8YBlock;
+  float acc[kPieces][kPiece];
 #pragma unroll
   for (int p = 0; p < kPieces; ++p)
 #pragma unroll
-    for (int i = 0; i < P; ++i) acc[p][i] = 0.f;
+    for (int i = 0; i < kPiece; ++i) acc[p][i] = 0.f;
   for (int j0 = 0; j0 < a.k; j0 += B) {
     bool local[B];
 #pragma unroll
@@ -154,18 +152,18 @@ __global__ __launch_bounds__(64 * kCombineWaves) void combine_slots(F8CombineArg
                  (uint32_t)e - (uint32_t)a.expert_begin < (uint32_t)a.num_experts;
     }
     u32x4_t y[B][kPieces];
-    float w[B], unit[B][kPieces];
+    uint32_t exponent[B][kPieces];
+    float w[B];
 #pragma unroll
     for (int u = 0; u < B; ++u) {
       if (!local[u]) continue;
       const int64_t f = s0 + j0 + u;
       w[u] = a.topk_weights[f];
-      const uint8_t* row = reinterpret_cast<const uint8_t*>(a.y) + f * a.H * (F16 ? 2 : 4);
 #pragma unroll
       for (int p = 0; p < kPieces; ++p) {
         const int v = min(v0 + 64 * p, nvec - 1);
-        y[u][p] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(row) + v);
-        unit[u][p] = F16 ? a.ys[f * slices + v / 32] : 1.f;
+        y[u][p] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(a.y + f * a.H) + v);
+        exponent[u][p] = a.yu[f * blocks + v / (kF8YBlock / kPiece)];
       }
     }
 #pragma unroll
@@ -173,16 +171,12 @@ __global__ __launch_bounds__(64 * kCombineWaves) void combine_slots(F8CombineArg
       if (!local[u]) continue;
 #pragma unroll
       for (int p = 0; p < kPieces; ++p) {
-        const float wu = w[u] * unit[u][p];
+        const float unit = __uint_as_float(exponent[u][p] << 23);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if constexpr (F16) {
-            const half2_t h = __builtin_bit_cast(half2_t, (uint32_t)y[u][p][i]);
-            acc[p][2 * i] = __builtin_fmaf(wu, (float)h[0], acc[p][2 * i]);
-            acc[p][2 * i + 1] = __builtin_fmaf(wu, (float)h[1], acc[p][2 * i + 1]);
-          } else {
-            acc[p][i] = __builtin_fmaf(wu, __uint_as_float(y[u][p][i]), acc[p][i]);
-          }
+          const half2_t h = __builtin_bit_cast(half2_t, (uint32_t)y[u][p][i]);
+          acc[p][2 * i] = __builtin_fmaf(w[u], unit * (float)h[0], acc[p][2 * i]);
+          acc[p][2 * i + 1] = __builtin_fmaf(w[u], unit * (float)h[1], acc[p][2 * i + 1]);
         }
       }
     }
@@ -191,12 +185,9 @@ __global__ __launch_bounds__(64 * kCombineWaves) void combine_slots(F8CombineArg
   for (int p = 0; p < kPieces; ++p) {
     const int v = v0 + 64 * p;
     if (v >= nvec) continue;
-    uint16_t* o = a.out + (int64_t)t * a.H + (int64_t)v * P;
-    if constexpr (F16)
-      *reinterpret_cast<uint4*>(o) = make_uint4(pk_bf16(acc[p][0], acc[p][1]), pk_bf16(acc[p][2], acc[p][3]),
-                                                pk_bf16(acc[p][4], acc[p][5]), pk_bf16(acc[p][6], acc[p][7]));
-    else
-      *reinterpret_cast<uint2*>(o) = make_uint2(pk_bf16(acc[p][0], acc[p][1]), pk_bf16(acc[p][2], acc[p][3]));
+    *reinterpret_cast<uint4*>(a.out + (int64_t)t * a.H + (int64_t)v * kPiece) =
+        make_uint4(pk_bf16(acc[p][0], acc[p][1]), pk_bf16(acc[p][2], acc[p][3]),
+                   pk_bf16(acc[p][4], acc[p][5]), pk_bf16(acc[p][6], acc[p][7]));
   }
 }
 
@@ -212,19 +203,19 @@ hipError_t launch_f8_quantize(const F8QuantArgs& a, hipStream_t stream) {
   const dim3 grid(grid_for(groups, kGroupsPerPass, 1 << 20)), block(kThreads);
   const int size = a.is_f32 ? 4 : 2;
   const bool wide = a.K % 8 == 0 && a.ld * size % 16 == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0;
-  if (a.is_f32 && wide) hipLaunchKernelGGL((quantize_kernel<true, true>), grid, block, 0, stream, a);
-  else if (a.is_f32) hipLaunchKernelGGL((quantize_kernel<true, false>), grid, block, 0, stream, a);
+  // (fp32 rows are a layer's h, whose rows are wide.)
+  if (a.is_f32 && !wide) return hipErrorInvalidValue;
+  if (a.is_f32) hipLaunchKernelGGL((quantize_kernel<true, true>), grid, block, 0, stream, a);
   else if (wide) hipLaunchKernelGGL((quantize_kernel<false, true>), grid, block, 0, stream, a);
   else hipLaunchKernelGGL((quantize_kernel<false, false>), grid, block, 0, stream, a);
   return hipGetLastError();
 }
 
 hipError_t launch_f8_combine(const F8CombineArgs& a, hipStream_t stream) {
-  const int per = 64 * kPieces * (a.ys != nullptr ? 8 : 4);
+  const int per = 64 * kPieces * kPiece;
   const int64_t waves = (int64_t)a.T * ((a.H + per - 1) / per);
   const dim3 grid((unsigned)((waves + kCombineWaves - 1) / kCombineWaves)), block(64 * kCombineWaves);
-  if (a.ys != nullptr) hipLaunchKernelGGL((combine_slots<true>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((combine_slots<false>), grid, block, 0, stream, a);
+  hipLaunchKernelGGL(combine_slots, grid, block, 0, stream, a);
   return hipGetLastError();
 }
 

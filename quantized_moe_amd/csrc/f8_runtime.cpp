@@ -114,7 +114,7 @@ F8GemmArgs weight_args(const chord_f8_weight* w, int kind, int cus) {
 constexpr int kF8MaxBlockM = kF8SmallRows;  // rows per alignment block at most
 
 struct F8Ws {
-  size_t align, sorted, experts, ntpp, status, tiles, xq, xs, h, hq, hs, y, ys, total;
+  size_t align, sorted, experts, ntpp, status, tiles, xq, xs, h, hq, hs, y, yu, total;
   int64_t max_padded;
   int max_tiles;
 };
@@ -140,8 +140,8 @@ F8Ws f8_ws(int T, int k, int E_l, int H, int I) {
   w.h = take(w.max_padded * I * 4);
   w.hq = take(w.max_padded * I);
   w.hs = take(w.max_padded * f8_chunks(I) * 4);
-  w.y = take((int64_t)T * k * H * 4);
-  w.ys = take((int64_t)T * k * ((H + 255) / 256) * 4);
+  w.y = take((int64_t)T * k * H * 2);
+  w.yu = take((int64_t)T * k * H / 32);
   w.total = off;
   return w;
 }
@@ -475,14 +475,14 @@ chord_status chord_f8_moe(const chord_bf16* x, int T, int H, int I, const chord_
   d.as = hs;
   d.a_rows = ws.max_padded;
   d.out = p + ws.y;
-  d.ys = reinterpret_cast<float*>(p + ws.ys);
+  d.yu = p + ws.yu;
   d.ld = H;
   HIP_TRY(plan.small && d.n_chunks <= 2 ? launch_f8_short_down(d, st) : launch_f8_tile(d, plan.small, st),
           "down launch");
 
   F8CombineArgs c{};
-  c.y = reinterpret_cast<const float*>(p + ws.y);
-  c.ys = plan.small ? nullptr : reinterpret_cast<const float*>(p + ws.ys);
+  c.y = reinterpret_cast<const uint16_t*>(p + ws.y);
+  c.yu = p + ws.yu;
   c.topk_ids = topk_ids;
   c.topk_weights = topk_weights;
   c.T = T;

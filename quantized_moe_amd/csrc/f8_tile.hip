@@ -339,54 +339,24 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
     return;
   }
 
-  if constexpr (KIND == kF8Down && ROWS > kF8SmallRows) {
-    // y as fp16 in units of the largest of a token's 256 outputs here: 2^-12 of
-    // that largest at worst, a sixteenth of the rounding to bf16 that follows the
-    // sum over slots, for half the bytes of fp32 (prefill of 8192 tokens on 48
-    // experts: down 231 -> 212, combine 108 -> 84 us).  A block below 2^-100 is 0.
+  if constexpr (KIND == kF8Down) {
+    // A wave's two tiles are one block of y: no wave waits for another.
+    if ((it.slice * kTiles + 2 * wave) * 16 >= a.N) return;  // (N is a multiple of 128)
+    const int block = it.slice * (kTiles / 2) + wave, blocks = a.N / kF8YBlock;
+    uint16_t* y = static_cast<uint16_t*>(a.out) + block * kF8YBlock + 16 * (q & 1) + 8 * (q >> 1);
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      uint32_t m = 0;
+    for (int g0 = 0; g0 < G; g0 += 4) {
+      uint32_t e = 0;  // lane quarter q: exponent of group g0 + q
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const bool there = (it.slice * kTiles + 2 * wave + n) * 16 < a.N;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          m = max(m, there ? __float_as_uint(acc[n][g][i]) & 0x7FFFFFFFu : 0u);
+      for (int g = g0; g < g0 + 4 && g < G; ++g) {
+        u32x4_t v;
+        const uint32_t eg = f8_y_pack(acc[0][g], acc[1][g], v);
+        const int64_t d = sm.dst[g * 16 + col];
+        if (d >= 0) *reinterpret_cast<u32x4_t*>(y + d * a.ld) = v;
+        e = q == g - g0 ? eg : e;
       }
-      m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
-      m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
-      if (q == 0) sm.amax[wave][g * 16 + col] = m;
-    }
-    __syncthreads();  // also: every wave is done with the token buffers
-    // Staged by token, 16-byte piece p of token t at p ^ (t % 32), for whole lines.
-    uint8_t* stage = sm.x[0];
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const int t = g * 16 + col;
-      uint32_t m = sm.amax[0][t];
-#pragma unroll
-      for (int u = 1; u < kWaves; ++u) m = max(m, sm.amax[u][t]);
-      const float A = __uint_as_float(m);
-      const bool zero_block = A < kF8Tiny;
-      const float inv = zero_block ? 0.f : __builtin_amdgcn_rcpf(A);
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const uint32_t lo = pk_f16(acc[n][g][0] * inv, acc[n][g][1] * inv);
-        const uint32_t hi = pk_f16(acc[n][g][2] * inv, acc[n][g][3] * inv);
-        const int piece = (2 * wave + n) * 2 + (q >> 1);
-        *reinterpret_cast<uint2*>(stage + t * 512 + ((piece ^ (t & 31)) * 16) + (q & 1) * 8) = make_uint2(lo, hi);
-      }
-      if (wave == 0 && q == 0 && sm.dst[t] >= 0)
-        a.ys[(int64_t)sm.dst[t] * ((a.N + 255) / 256) + it.slice] = zero_block ? 0.f : A;
-    }
-    __syncthreads();
-    uint16_t* y = static_cast<uint16_t*>(a.out);
-    for (int i = threadIdx.x; i < 16 * G * 32; i += kThreads) {
-      const int t = i >> 5, piece = i & 31, n = it.slice * 256 + piece * 8;
-      if (sm.dst[t] >= 0 && n < a.N)
-        *reinterpret_cast<uint4*>(y + (int64_t)sm.dst[t] * a.ld + n) =
-            *reinterpret_cast<const uint4*>(stage + t * 512 + ((piece ^ (t & 31)) * 16));
+      const int64_t d = g0 + q < G ? sm.dst[(g0 + q) * 16 + col] : -1;
+      if (d >= 0) a.yu[d * blocks + block] = (uint8_t)e;
     }
     return;
   }
@@ -404,8 +374,6 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
         if (f < a.n_tiles * 16)
           *reinterpret_cast<f32x4_t*>(a.partials + ((int64_t)it.part * a.a_rows + it.row0 + d) * (a.n_tiles * 16) +
                                       f) = acc[n][g];
-      } else if (KIND == kF8Down) {
-        if (f < a.N) *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + d * a.ld + f) = acc[n][g];
       } else {
         uint16_t* p = static_cast<uint16_t*>(a.out) + (it.row0 + d) * a.ld + f;
         if (wide && f + 4 <= a.N) {

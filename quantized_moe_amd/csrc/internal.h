@@ -324,13 +324,12 @@ struct F8GemmArgs {
   float* partials;
   // output: bf16 [*, ld] by row (plain); h by aligned row (gate_up: fp32
   // [rows, ld], or from the tiled kernel codes [rows, ld] and scales hs
-  // [rows, ld / 128]); y by flat slot (down: fp32 [slots, ld], or from the
-  // tiled kernel's large form fp16 [slots, ld] in units of ys [slots, slices of
-  // 256 outputs])
+  // [rows, ld / 128]); y by flat slot (down: fp16 [slots, ld] with exponents yu
+  // [slots, ld / 32])
   void* out;
   int64_t ld;
   float* hs;
-  float* ys;
+  uint8_t* yu;
 };
 
 // The layer in two launches (where f8_small_fits).
@@ -348,8 +347,8 @@ struct F8SmallArgs {
 };
 
 struct F8CombineArgs {
-  const float* y;           // [T * k, H], rows of local slots
-  const float* ys;          // null, or y is fp16 in these units [T * k, ceil(H / 256)]
+  const uint16_t* y;        // fp16 [T * k, H], rows of local slots
+  const uint8_t* yu;        // their exponents [T * k, H / 32]
   const int32_t* topk_ids;  // [T, k]
   const float* topk_weights;
   int T, k, H;
