@@ -511,16 +511,28 @@ __global__ __launch_bounds__(kThreads, OCC) void f8_tile(F8GemmArgs a) {
     }
   } else {
     // The tile list comes in 8 groups of balanced size, one per XCD; all slices
-    // of a tile stay on one XCD, which reads its token rows once.
+    // of a tile stay on one XCD, which reads its token rows once.  Items that
+    // fill no whole round of the XCD's workgroups are cut by rows into as many
+    // pieces as fill one.
     const int t0 = a.status->group_start[xcd];
     const int n = (a.status->group_start[xcd + 1] - t0) * slices;
-    for (int j = local; j < n; j += run) {
-      const TileDesc td = a.tiles[t0 + j / slices];
+    const int whole = n / run * run, rest = n - whole;
+    const int pieces = rest > 0 ? run / rest : 1;
+    for (int j = local; j < whole + rest * pieces; j += run) {
+      const int u = j - whole, i = u < 0 ? j : whole + u / pieces;
+      const TileDesc td = a.tiles[t0 + i / slices];
       Item it;
       it.expert = td.expert;
-      it.slice = j % slices;
+      it.slice = i % slices;
       it.row0 = td.row_begin;
       it.nrows = min(td.nrows, kF8MoeTileRows);
+      if (u >= 0) {
+        const int rows = ((it.nrows + pieces - 1) / pieces + 31) / 32 * 32;
+        const int begin = u % pieces * rows;
+        if (begin >= it.nrows) continue;  // uniform
+        it.row0 += begin;
+        it.nrows = min(rows, it.nrows - begin);
+      }
       do_item<KIND, ROWS>(a, sm, scales, it);
     }
   }
