@@ -151,21 +151,36 @@ struct F8MoePlan {
   int block_m;          // rows per alignment block
   bool small;           // tiled GEMMs over the alignment blocks (else over built tiles)
   bool stream_gate_up;  // small: gate_up by the weight-streaming kernel
-  int active;           // expected experts with rows
+  int blocks;           // expected alignment blocks with rows
   const char* text;
 };
-constexpr double kSmallRowsPerExpert = 24.0;
+// Measured over layers of H = 1024 .. 7168, I = 256 .. 2048 with 4 .. 384 experts,
+// in us for a call:
+// - gate_up by the streaming kernel, whose many small workgroups start at once,
+//   as long as they are few (w < 3 a CU), else by tiles, which read a block's
+//   tokens once (streaming / tiled): 4 experts of 7168 x 256 with 20 rows each
+//   (w = 112) 33 / 54, with 120 (w = 272) 49 / 67; of 4096 x 1024 with 25 (w = 538)
+//   45 / 50, with 100 (w = 947) 60 / 54; 16 of 2048 x 768 with 12 (w = 921) 42 / 38;
+//   110 of 2048 x 768 with 2 (w = 5280) 139 / 111.
+// - Tiles over alignment blocks, two workgroups a CU, below 24 rows an expert,
+//   else tiles over up to 224 rows of an expert (blocks / large): 16 rows 395 /
+//   415 and 429 / 462, 24 rows 460 / 423 and 502 / 480 (48 experts of 7168 x 2048,
+//   384 of 7168 x 256); and also above where the blocks' tiles leave a CU one
+//   workgroup: 4 experts of 4096 x 1024 with 100 rows 54 / 58, 8 of 1024 x 512 with
+//   50 33 / 39, but 16 of 2048 x 768 with 100 81 / 56.
+// - Blocks of 32 rows above 8 an expert (16 / 32 rows): 10.7 rows 450 / 406 and 406 /
+//   382, 4 rows 412 / 414.
 F8MoePlan f8_moe_plan(int T, int k, int E_g, int E_l, int I, int cus) {
   const int eg = E_g > E_l ? E_g : E_l;
   const double tok_e = (double)T * k / eg;
+  const double active = std::max(1.0, E_l * (1.0 - pow(1.0 - 1.0 / eg, (double)T * k)));
+  const double rows = tok_e * E_l / active;  // of an expert with rows
+  auto blocks = [&](int m) { return active * std::max(1.0, rows / m + 0.5); };
   F8MoePlan p{};
-  p.small = tok_e < kSmallRowsPerExpert;
-  p.block_m = p.small && tok_e > 8.0 ? 32 : 16;
-  // Expected gate_up items of the small form (active experts x slices of 256
-  // rows) against its workgroups.
-  const double active = E_l * (1.0 - pow(1.0 - 1.0 / eg, (double)T * k));
-  p.active = std::max(1, (int)(active + 0.5));
-  p.stream_gate_up = p.small && p.block_m == 16 && active * (2 * I / 256) < 4.0 * 2 * cus;
+  p.stream_gate_up = blocks(16) * (2 * I / 32) < 3.0 * cus;
+  p.small = p.stream_gate_up || tok_e < 24.0 || blocks(32) * (2 * I / 256) < cus;
+  p.block_m = p.small && !p.stream_gate_up && tok_e > 8.0 ? 32 : 16;
+  p.blocks = (int)std::min(blocks(p.block_m), 1e9);
   p.text = !p.small ? "f8 moe: tiles of up to 224 rows"
            : p.stream_gate_up ? "f8 moe: blocks of 16 rows, streaming gate_up"
            : p.block_m == 16 ? "f8 moe: blocks of 16 rows" : "f8 moe: blocks of 32 rows";
@@ -438,7 +453,7 @@ chord_status chord_f8_moe(const chord_bf16* x, int T, int H, int I, const chord_
     g.max_padded = ws.max_padded;
     g.topk = k;
     g.n_flat = (int64_t)T * k;
-    g.est_blocks = plan.active;
+    g.est_blocks = plan.blocks;
     g.tiles = tiles;
     g.status = status;
   };

@@ -438,3 +438,56 @@ def test_moe_chunks_behind_the_loop(C, T, E, k, H, I):
     for got in cold_calls(lambda: layer.indexed(xg, ig, wg, 0, E)):
         err = np.abs(f64(got) - ref)
         assert np.all(err <= bound) and np.linalg.norm(err) <= norm
+
+
+TILED_CASES = [
+    # T, H, I, E, k, hot, plan; chunks 1 .. 7 of both products, partial slices,
+    # experts from one row to several tiles
+    (120, 640, 384, 90, 4, 0, "blocks of 16 rows"),
+    (150, 768, 896, 60, 3, 0, "blocks of 16 rows"),
+    (90, 896, 256, 100, 4, 0, "blocks of 16 rows"),
+    (300, 384, 256, 50, 2, 0, "blocks of 32 rows"),
+    (330, 640, 128, 50, 3, 0, "blocks of 16 rows, streaming gate_up"),
+    (450, 640, 128, 70, 3, 0, "blocks of 32 rows"),
+    (120, 896, 1152, 10, 1, 0, "blocks of 32 rows"),
+    (230, 768, 640, 24, 2, 0, "blocks of 32 rows"),
+    (420, 640, 768, 16, 2, 0, "blocks of 32 rows"),
+    (800, 384, 768, 16, 2, 0, "tiles of up to 224 rows"),
+    (1000, 640, 640, 18, 2, 2, "tiles of up to 224 rows"),
+    (1500, 768, 384, 30, 2, 0, "tiles of up to 224 rows"),
+    (1400, 896, 896, 12, 1, 1, "tiles of up to 224 rows"),
+    (1900, 512, 640, 10, 2, 0, "tiles of up to 224 rows"),
+    (900, 128, 1152, 20, 1, 1, "tiles of up to 224 rows"),
+]
+
+
+@pytest.mark.parametrize("T,H,I,E,k,hot,plan", TILED_CASES)
+def test_moe_tiled_forms(C, T, H, I, E, k, hot, plan):
+    """The forms of larger layers, inputs cold, results repeatable bit for bit."""
+    banner(f"f8 moe T={T} H={H} I={I} E={E} k={k} hot={hot}")
+    layer, d13, d2 = make_layer(E, H, I, T + E)
+    ids, w = routing(T, E, k, I + T, hot)
+    x = activations(T, H, 3)
+    ref, bound, norm = f8.moe(f64(x), ids, w, d13, d2, 0)
+    xg, ig, wg = x.cuda(), torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda()
+    outs = cold_calls(lambda: layer.indexed(xg, ig, wg, 0, E), 4)
+    assert C.last_plan() == "f8 moe: " + plan
+    err = np.abs(f64(outs[0]) - ref)
+    assert np.all(err <= bound) and np.linalg.norm(err) <= norm
+    assert all(torch.equal(o, outs[0]) for o in outs)
+
+
+def test_moe_tiled_forms_with_nan_and_foreign_rows(C):
+    """Tokens of NaN, of foreign experts only and with an expert twice, in layers
+    whose tiles hold them beside ordinary ones."""
+    for T, E, k, I in ((150, 60, 3, 896), (420, 16, 2, 768), (800, 16, 2, 768)):
+        layer, d13, d2 = make_layer(E, 384, I, T)
+        ids, w = routing(T, E, k, T)
+        ids[5], ids[6] = E + 3, ids[6][0]
+        x = activations(T, 384, 3)
+        ref, bound, _ = f8.moe(f64(x), ids, w, d13, d2, 0)
+        x[7, 11] = np.nan
+        got = f64(layer.indexed(x.cuda(), torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda(), 0, E))
+        assert np.isnan(got[7]).all() and not got[5].any()
+        rest = np.arange(T) != 7
+        assert np.all(np.abs(got - ref)[rest] <= bound[rest])
