@@ -6,7 +6,8 @@
 // their way while one is multiplied.
 //
 // Against the tiled kernel, whose workgroups drain and refill their pipeline for
-// every 256 features: 384 experts, 512 tokens, 7168 x 256 weights, 180 -> 160 us.
+// every 256 features: 384 experts, 512 tokens, 7168 x 256 weights, 180 -> 160 us
+// with y in fp32, and 150 with y in fp16 (0.83 GB of weights and y, 5.5 TB/s).
 #include "f8_common.h"
 
 namespace chord {

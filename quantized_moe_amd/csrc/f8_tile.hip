@@ -6,6 +6,9 @@
 // and their scales go straight from memory into LDS (buffer_load ... lds), three
 // chunks of 128 along K ahead, in four buffers.  (With weights in LDS too only
 // one chunk fits in flight, and the loads alone took as long as the products.)
+// 8192 x 4096 x 7168 takes 203 us, 2.37 PFLOP/s, matrix units busy for 59 % of
+// 1.83 GHz, to which the clock falls under them; weights of 48 experts of 4096 x 7168
+// with 170 rows each 330 us, 4.5 TB/s of them.
 //
 // A matrix instruction covers the chunk; its result is scaled into the fp32
 // accumulators one token group later, so the multiply-adds run beside the next
@@ -119,7 +122,7 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
   // Scales come for four chunks at a time, 16 rows x 4 chunks per instruction:
   // fetched chunk by chunk, every row's 4 bytes are a memory request of their own,
   // more of them than the rows themselves take (gate_up of 8192 tokens on 48
-  // experts: 381 us, with this 340).
+  // experts: 381 us so, 340 without a request a row).
   // (Fewer than 256 rows: the surplus waves repeat rows, to the same places.)
   uint32_t so[2];
   uint32_t ls[2];
@@ -340,7 +343,10 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
   }
 
   if constexpr (KIND == kF8Down) {
-    // A wave's two tiles are one block of y: no wave waits for another.
+    // A wave's two tiles are one block of y: no wave waits for another.  (8192
+    // tokens on 48 experts, 117 MB of y: 205 us; 218 staged through LDS in units
+    // per 256 outputs, 231 in fp32.  About 35 us of it are the stores, which all
+    // workgroups issue at the same time and the next item's loads queue behind.)
     if ((it.slice * kTiles + 2 * wave) * 16 >= a.N) return;  // (N is a multiple of 128)
     const int block = it.slice * (kTiles / 2) + wave, blocks = a.N / kF8YBlock;
     uint16_t* y = static_cast<uint16_t*>(a.out) + block * kF8YBlock + 16 * (q & 1) + 8 * (q >> 1);
