@@ -628,7 +628,10 @@ size_t chord_f8_moe_workspace_bytes(int T, int k, int E_l, int H, int I);
  *   y_tj = W2_e h~,  h = silu(W1_e x~_t) * (W3_e x~_t), both in fp32,
  *
  * x~ and h~ being x and h quantised as chord_f8_quantize does.  The call
- * quantises x and aligns the routing itself.
+ * quantises x and aligns the routing itself.  Between the down product and the
+ * sum over slots y is fp16 in units of a power of two per 32 outputs (2^-11 of a
+ * value; fp32 where a handful of slots make up the call); the sum is fp32 and
+ * rounded once.
  *
  * x:        device bf16 [T, H], 16-byte aligned.
  * w13, w2:  handles packed with roles GATE_UP (N = 2I, K = H) and DOWN (N = H,
