@@ -80,8 +80,8 @@ __global__ __launch_bounds__(64 * WK) void f8_stream(F8GemmArgs a) {
       } else if (m * 16 + col < a.block_m) {
         const int64_t f = a.sorted_ids[r];
         if (f >= 0 && f < a.n_flat) {
-          src[m] = a.kind == kF8GateUp ? f / a.topk : r;
-          dst[m] = a.kind == kF8GateUp ? r : f;
+          src[m] = f / a.topk;
+          dst[m] = r;
         }
       }
     }

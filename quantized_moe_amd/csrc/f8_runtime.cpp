@@ -137,12 +137,16 @@ F8Ws f8_ws(int T, int k, int E_l, int H, int I) {
   w.tiles = take(w.max_tiles * sizeof(TileDesc));
   w.xq = take((int64_t)T * H);
   w.xs = take((int64_t)T * f8_chunks(H) * 4);
-  w.h = take(w.max_padded * I * 4);
   w.hq = take(w.max_padded * I);
   w.hs = take(w.max_padded * f8_chunks(I) * 4);
+  // (h in fp32 is quantised, or used up, before y is written.)
+  const size_t both = off;
+  w.h = take(w.max_padded * I * 4);
+  const size_t h_end = off;
+  off = both;
   w.y = take((int64_t)T * k * H * 2);
   w.yu = take((int64_t)T * k * H / 32);
-  w.total = off;
+  w.total = std::max(off, h_end);
   return w;
 }
 
