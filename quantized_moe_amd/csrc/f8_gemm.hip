@@ -39,7 +39,8 @@ __device__ __forceinline__ void store4(uint16_t* out, int64_t row, int64_t ld, i
     if (n + i < N) p[i] = to_bf16(v[i]);
 }
 
-template <int NT, int MT, int WK, int PF>
+// EXACT: f8_exact_product (gate_up).
+template <int NT, int MT, int WK, int PF, bool EXACT>
 __global__ __launch_bounds__(64 * WK) void f8_stream(F8GemmArgs a) {
   __shared__ f32x4_t red[WK > 1 ? WK : 1][NT * MT][64];
   const int lane = threadIdx.x & 63;
@@ -141,8 +142,9 @@ __global__ __launch_bounds__(64 * WK) void f8_stream(F8GemmArgs a) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-          const f32x4_t r = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              av, operand(x[p][m][0], x[p][m][1]), zero, 0, 0, 0, 0, 0, 0);
+          const i32x8_t bv = operand(x[p][m][0], x[p][m][1]);
+          const f32x4_t r = EXACT ? f8_exact_product(av, bv)
+                                  : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, zero, 0, 0, 0, 0, 0, 0);
           const float f0 = sx[p][m] * sw0[p], f1 = sx[p][m] * sw1[p];
           acc[n][m][0] = __builtin_fmaf(r[0], f0, acc[n][m][0]);
           acc[n][m][1] = __builtin_fmaf(r[1], f1, acc[n][m][1]);
@@ -205,8 +207,8 @@ hipError_t launch_f8_gemm(const F8GemmArgs& a, hipStream_t stream) {
   };
   // A product alone has few tiles: one per workgroup, K over 8 waves (M = 1, N =
   // 4096, K = 7168: 12.8 us with two tiles and 4 waves, 7.8 so).
-  if (a.kind == kF8Plain) return run(f8_stream<1, 1, 8, 4>, 1, 8, 2);
-  return run(f8_stream<2, 1, 4, 4>, 2, 4, 4);
+  if (a.kind == kF8Plain) return run(f8_stream<1, 1, 8, 4, false>, 1, 8, 2);
+  return run(f8_stream<2, 1, 4, 4, true>, 2, 4, 4);
 }
 
 }  // namespace chord

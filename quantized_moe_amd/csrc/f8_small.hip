@@ -136,9 +136,7 @@ __global__ __launch_bounds__(kThreads) void small_gate_up(F8SmallArgs a) {
         for (int p = 0; p < PF; ++p) {
           const int c = c0 + p;
           if (c >= c_hi) break;
-          const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-          const f32x4_t r = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              operand(w[p][0], w[p][1]), read_codes(xp + c * kF8Block), zero, 0, 0, 0, 0, 0, 0);
+          const f32x4_t r = f8_exact_product(operand(w[p][0], w[p][1]), read_codes(xp + c * kF8Block));
           if (c + PF < c_hi) load_w(w[p], wp + (int64_t)(c + PF) * wstep);
           const float f0 = sp[c] * s0[c], f1 = sp[c] * s1[c];
           acc[0] = __builtin_fmaf(r[0], f0, acc[0]);

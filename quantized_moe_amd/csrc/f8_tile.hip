@@ -93,7 +93,7 @@ struct Item {
 };
 
 // One item with G = 2 MG token groups of 16.
-template <int MG, int KIND, int ROWS>
+template <int MG, int KIND, int ROWS, bool EXACT>
 __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Scales<ROWS>& scales,
                                          const Item& it, __amdgpu_buffer_rsrc_t xres, Rsrc sres) {
   constexpr int G = 2 * MG;
@@ -180,6 +180,17 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
   };
   auto read_s = [&](int half, int ph, int g) { return scales.s[half][g * 16 + col][ph]; };
   const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+  // EXACT: blocks of at most 16 rows, whose second group is empty.  (Left alone,
+  // the widened weights of the next chunks would be kept, and spill.)
+  auto product = [&](i32x8_t wv, i32x8_t x, int g) {
+    if constexpr (EXACT) {
+      if (g > 0) return zero;
+      asm volatile("" : "+v"(wv), "+v"(x));
+      return f8_exact_product(wv, x);
+    } else {
+      return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, x, zero, 0, 0, 0, 0, 0, 0);
+    }
+  };
   i32x8_t xv[2];
   float sx[2];
   f32x4_t r[2][2] = {{zero, zero}, {zero, zero}};
@@ -230,11 +241,11 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
       if (g == G / 2 && !last && (b == 0 || b == 3)) barrier(std::integral_constant<int, kBehind>{});
       if (g == G / 2 && last && b == 0) barrier(std::integral_constant<int, kBehindLast + kDma>{});
       if (g == G / 2 && last && b == 1) barrier(std::integral_constant<int, kBehindLast>{});
-      r[g & 1][0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w0, xv[g & 1], zero, 0, 0, 0, 0, 0, 0);
+      r[g & 1][0] = product(w0, xv[g & 1], g);
       xv[(g + 1) & 1] = g + 1 < G ? read_x(b, g + 1) : read_x(nb, 0);
       scale_in(0, (g + G - 1) % G);
       __builtin_amdgcn_sched_barrier(0);
-      r[g & 1][1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w1, xv[g & 1], zero, 0, 0, 0, 0, 0, 0);
+      r[g & 1][1] = product(w1, xv[g & 1], g);
       scale_in(1, (g + G - 1) % G);
       f0 = sx[g & 1] * sw0;
       f1 = KIND == kF8GateUp ? sx[g & 1] * sw1 : f0;
@@ -395,7 +406,7 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
   }
 }
 
-template <int KIND, int ROWS>
+template <int KIND, int ROWS, bool EXACT>
 __device__ __forceinline__ void do_item(const F8GemmArgs& a, Smem<ROWS>& sm, Scales<ROWS>& scales,
                                         const Item& it) {
   const int64_t pitch = (int64_t)a.n_chunks * kF8Block, spitch = (int64_t)a.n_chunks * 4;
@@ -432,18 +443,18 @@ __device__ __forceinline__ void do_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sca
       __builtin_amdgcn_make_buffer_rsrc((void*)xbase, 0, (int)(xrows * pitch), kRsrcWord3);
   const Rsrc sres = make_rsrc(sbase, xrows * spitch);
   if constexpr (ROWS == kF8SmallRows) {
-    run_item<1, KIND, ROWS>(a, sm, scales, it, xres, sres);
+    run_item<1, KIND, ROWS, EXACT>(a, sm, scales, it, xres, sres);
   } else {
     switch ((it.nrows + 31) / 32) {
-      case 1: run_item<1, KIND, ROWS>(a, sm, scales, it, xres, sres); break;
-      case 2: run_item<2, KIND, ROWS>(a, sm, scales, it, xres, sres); break;
-      case 3: run_item<3, KIND, ROWS>(a, sm, scales, it, xres, sres); break;
-      case 4: run_item<4, KIND, ROWS>(a, sm, scales, it, xres, sres); break;
-      case 5: run_item<5, KIND, ROWS>(a, sm, scales, it, xres, sres); break;
-      case 6: run_item<6, KIND, ROWS>(a, sm, scales, it, xres, sres); break;
-      case 7: run_item<7, KIND, ROWS>(a, sm, scales, it, xres, sres); break;
+      case 1: run_item<1, KIND, ROWS, EXACT>(a, sm, scales, it, xres, sres); break;
+      case 2: run_item<2, KIND, ROWS, EXACT>(a, sm, scales, it, xres, sres); break;
+      case 3: run_item<3, KIND, ROWS, EXACT>(a, sm, scales, it, xres, sres); break;
+      case 4: run_item<4, KIND, ROWS, EXACT>(a, sm, scales, it, xres, sres); break;
+      case 5: run_item<5, KIND, ROWS, EXACT>(a, sm, scales, it, xres, sres); break;
+      case 6: run_item<6, KIND, ROWS, EXACT>(a, sm, scales, it, xres, sres); break;
+      case 7: run_item<7, KIND, ROWS, EXACT>(a, sm, scales, it, xres, sres); break;
       default:
-        if constexpr (KIND == kF8Plain) run_item<8, KIND, ROWS>(a, sm, scales, it, xres, sres);
+        if constexpr (KIND == kF8Plain) run_item<8, KIND, ROWS, EXACT>(a, sm, scales, it, xres, sres);
     }
   }
 }
@@ -472,7 +483,8 @@ __global__ __launch_bounds__(256) void f8_add_parts(F8GemmArgs a) {
 }
 
 // Persistent workgroups.  Workgroup b runs on XCD b % 8.  OCC: waves per SIMD.
-template <int KIND, int ROWS, int OCC>
+// EXACT: f8_exact_product (gate_up over alignment blocks of 16 rows).
+template <int KIND, int ROWS, int OCC, bool EXACT>
 __global__ __launch_bounds__(kThreads, OCC) void f8_tile(F8GemmArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   Smem<ROWS>& sm = *reinterpret_cast<Smem<ROWS>*>(smem);
@@ -497,7 +509,7 @@ __global__ __launch_bounds__(kThreads, OCC) void f8_tile(F8GemmArgs a) {
       it.slice = rest / wide;
       it.row0 = (block * 8 + rest % wide) * rows;
       it.nrows = (int)min((int64_t)rows, a.a_rows - it.row0);
-      do_item<KIND, ROWS>(a, sm, scales, it);
+      do_item<KIND, ROWS, EXACT>(a, sm, scales, it);
     }
   } else if (ROWS == kF8SmallRows) {
     // Tiles are the alignment blocks (at most ROWS rows), block t and all its
@@ -513,7 +525,7 @@ __global__ __launch_bounds__(kThreads, OCC) void f8_tile(F8GemmArgs a) {
       it.row0 = (int64_t)t * a.block_m;
       it.nrows = a.block_m;
       if (it.expert < 0 || it.expert >= a.num_experts) continue;  // uniform
-      do_item<KIND, ROWS>(a, sm, scales, it);
+      do_item<KIND, ROWS, EXACT>(a, sm, scales, it);
     }
   } else {
     // The tile list comes in 8 groups of balanced size, one per XCD; all slices
@@ -539,7 +551,7 @@ __global__ __launch_bounds__(kThreads, OCC) void f8_tile(F8GemmArgs a) {
         it.row0 += begin;
         it.nrows = min(rows, it.nrows - begin);
       }
-      do_item<KIND, ROWS>(a, sm, scales, it);
+      do_item<KIND, ROWS, EXACT>(a, sm, scales, it);
     }
   }
 }
@@ -559,17 +571,18 @@ hipError_t launch_f8_tile(const F8GemmArgs& a, bool small, hipStream_t stream) {
   };
   constexpr int R = kF8TileRows, S = kF8SmallRows;
   if (a.kind == kF8Plain) {
-    const hipError_t e = run(f8_tile<kF8Plain, R, 2>, 1, sizeof(Smem<R>));
+    const hipError_t e = run(f8_tile<kF8Plain, R, 2, false>, 1, sizeof(Smem<R>));
     if (e != hipSuccess || a.parts <= 1) return e;
     const int64_t n = (a.a_rows * (a.n_tiles * 4) + 255) / 256, most = (int64_t)a.num_cus * 16;
     hipLaunchKernelGGL(f8_add_parts, dim3((unsigned)(n < most ? n : most)), dim3(256), 0, stream, a);
     return hipGetLastError();
   }
   if (a.kind == kF8GateUp)
-    return small ? run(f8_tile<kF8GateUp, S, 4>, 2, sizeof(Smem<S>))
-                 : run(f8_tile<kF8GateUp, R, 2>, 1, sizeof(Smem<R>));
-  return small ? run(f8_tile<kF8Down, S, 4>, 2, sizeof(Smem<S>))
-               : run(f8_tile<kF8Down, R, 2>, 1, sizeof(Smem<R>));
+    return !small             ? run(f8_tile<kF8GateUp, R, 2, false>, 1, sizeof(Smem<R>))
+           : a.block_m <= 16 ? run(f8_tile<kF8GateUp, S, 4, true>, 2, sizeof(Smem<S>))
+                             : run(f8_tile<kF8GateUp, S, 4, false>, 2, sizeof(Smem<S>));
+  return small ? run(f8_tile<kF8Down, S, 4, false>, 2, sizeof(Smem<S>))
+               : run(f8_tile<kF8Down, R, 2, false>, 1, sizeof(Smem<R>));
 }
 
 }  // namespace chord
