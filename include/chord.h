@@ -630,7 +630,8 @@ size_t chord_f8_moe_workspace_bytes(int T, int k, int E_l, int H, int I);
  * x~ and h~ being x and h quantised as chord_f8_quantize does.  The call
  * quantises x and aligns the routing itself.  Between the down product and the
  * sum over slots y is fp16 in units of a power of two per 32 outputs (2^-11 of a
- * value; fp32 where a handful of slots make up the call); the sum is fp32 and
+ * value; fp32 where a handful of slots make up the call); a y that is infinite or
+ * NaN stays so and leaves the outputs beside it as they are.  The sum is fp32 and
  * rounded once.  Products of gate_up are summed in fp32 where rows per expert are
  * few (blocks of 16), else, like all others, as the 8-bit matrix instruction
  * does: eights of products on a grid of 2^-13 of the largest.

@@ -84,10 +84,21 @@ __device__ __forceinline__ uint32_t pk_f16(float a, float b) {
 // fp16, 2^-11 of itself, and by 2^-25 units where it is far below the largest: an
 // eighth of the rounding to bf16 that follows the sum, for half the bytes of fp32.
 constexpr int kF8YBlock = 32;
-// Exponent for a largest magnitude with these bits (1 .. 253, so that the unit
-// and its inverse are normal; infinities and NaN stay what they are in fp16).
+// Exponent for a largest finite magnitude with these bits (1 .. 253, so that the
+// unit and its inverse are normal).  Infinities and NaN have no part in it: scaled
+// by any unit they are in fp16 what they were, and a unit as large as theirs would
+// leave zeros of the finite outputs beside them.
+constexpr uint32_t kF8NotFinite = 0x7F800000u;  // magnitudes from these bits on
 __device__ __forceinline__ uint32_t f8_y_exponent(uint32_t abs_bits) {
   return min(max(abs_bits >> 23, 1u), 253u);
+}
+// Maximum over the quarter waves (swaps of odd quarters with even ones, and of
+// halves).
+__device__ __forceinline__ uint32_t f8_quarter_max(uint32_t m) {
+  auto s = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+  m = max((uint32_t)s[0], (uint32_t)s[1]);
+  s = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+  return max((uint32_t)s[0], (uint32_t)s[1]);
 }
 // A matrix instruction's results for 32 outputs of a token, a of the first 16
 // and b of the next, four in each lane of a quarter wave q: their exponent, and
@@ -97,11 +108,16 @@ __device__ __forceinline__ uint32_t f8_y_pack(f32x4_t a, f32x4_t b, u32x4_t& out
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     m = max(m, max(__float_as_uint(a[i]) & 0x7FFFFFFFu, __float_as_uint(b[i]) & 0x7FFFFFFFu));
-  // Swaps of odd quarters with even ones, and of halves: the maximum over q.
-  auto s = __builtin_amdgcn_permlane16_swap(m, m, false, false);
-  m = max((uint32_t)s[0], (uint32_t)s[1]);
-  s = __builtin_amdgcn_permlane32_swap(m, m, false, false);
-  m = max((uint32_t)s[0], (uint32_t)s[1]);
+  m = f8_quarter_max(m);
+  if (__builtin_amdgcn_ballot_w64(m >= kF8NotFinite) != 0) {  // (by the whole wave, for the swaps)
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x = __float_as_uint(a[i]) & 0x7FFFFFFFu, y = __float_as_uint(b[i]) & 0x7FFFFFFFu;
+      m = max(m, max(x < kF8NotFinite ? x : 0u, y < kF8NotFinite ? y : 0u));
+    }
+    m = f8_quarter_max(m);
+  }
   const uint32_t e = f8_y_exponent(m);
   const float inv = __uint_as_float((254u - e) << 23);
   // The same swap brings a's neighbours together in even quarters, b's in odd.
