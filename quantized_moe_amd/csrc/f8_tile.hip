@@ -299,9 +299,19 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
     chunk(3, c + 3, half, in_loop);
     half = 1 - half;
   }
+  // Where a chunk behind the loop is missing its weights (repeats of the last
+  // chunk's) are read all the same: a load without a reader on some path could be
+  // dropped or moved there, and the counts in the loop rely on every one.
+  auto used = [&](int b) {
+#pragma unroll
+    for (int j = 0; j < kW; ++j) asm volatile("" ::"v"(w[b % WR][j >> 1][j & 1]));
+  };
   if (c < nc) chunk(0, c, half, behind_loop);
+  else used(0);
   if (c + 1 < nc) chunk(1, c + 1, half, behind_loop);
+  else used(1);
   if (c + 2 < nc) chunk(2, c + 2, half, behind_loop);
+  else used(2);
   scale_in(0, G - 1);
   scale_in(1, G - 1);
   // The repeated loads at the end land before their buffers are used again.
