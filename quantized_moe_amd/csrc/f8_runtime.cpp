@@ -2,6 +2,7 @@
 // checks (before any HIP call), workspace layout and launch sequences.
 #include <algorithm>
 #include <cmath>
+#include <cstdio>
 
 #include "host.h"
 
@@ -346,6 +347,13 @@ chord_status chord_f8_gemm(const chord_f8* codes, const float* scales, int64_t M
   g.ld = ld;
   hipStream_t st = static_cast<hipStream_t>(stream);
   HIP_TRY(plan.stream ? launch_f8_gemm(g, st) : launch_f8_tile(g, false, st), "8-bit GEMM launch");
+  if (plan.stream) {
+    set_last_plan("f8 gemm: streaming");
+  } else {
+    char text[64];
+    snprintf(text, sizeof(text), "f8 gemm: tiles of %d rows, K in %d", plan.tile_rows, plan.parts);
+    set_last_plan(text);
+  }
   return CHORD_OK;
 }
 

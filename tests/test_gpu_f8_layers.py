@@ -6,8 +6,8 @@ import pytest
 import torch
 
 from oracle import f8
-from tests.gpu_util import banner
-from tests.test_gpu_f8 import C, activations, f64, routing, weights  # noqa: F401  (C: a fixture)
+from tests.gpu_util import banner, host
+from tests.test_gpu_f8 import C, activations, cold_calls, f64, routing, weights  # noqa: F401  (C: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +61,70 @@ def test_moe_one_output_that_is_not_finite(C, T, H, I, E, k, plan):  # noqa: F81
     assert np.abs(ref[keep]).max() < big / 8            # what is compared is finite
     err = np.abs(got - ref)
     assert np.all(err[keep] <= bound[keep]), np.argwhere(keep & ~(err <= bound))[:5]
+
+
+GEMM_FORMS = [
+    # M, N, K, plan: the last tile has 1, 33, .. rows, so every count of token
+    # groups up to the tallest; 0 to 3 chunks behind the loop of four; ragged N
+    (12, 300, 900, "streaming"),
+    (200, 520, 4000, "tiles of 64 rows, K in 8"),
+    (5473, 553, 1024, "tiles of 96 rows, K in 1"),
+    (5601, 516, 640, "tiles of 96 rows, K in 1"),
+    (5663, 515, 768, "tiles of 96 rows, K in 1"),
+    (5728, 542, 832, "tiles of 96 rows, K in 1"),
+    (5249, 1043, 576, "tiles of 128 rows, K in 1"),
+    (6177, 833, 728, "tiles of 128 rows, K in 1"),
+    (6271, 781, 832, "tiles of 128 rows, K in 1"),
+    (6400, 779, 984, "tiles of 128 rows, K in 1"),
+    (10977, 523, 600, "tiles of 192 rows, K in 1"),
+    (11094, 516, 767, "tiles of 192 rows, K in 1"),
+    (11711, 514, 856, "tiles of 192 rows, K in 1"),
+    (10945, 564, 1024, "tiles of 192 rows, K in 1"),
+    (12289, 819, 960, "tiles of 256 rows, K in 1"),
+    (13345, 802, 576, "tiles of 256 rows, K in 1"),
+    (12438, 856, 704, "tiles of 256 rows, K in 1"),
+    (12488, 771, 896, "tiles of 256 rows, K in 1"),
+    (12799, 828, 576, "tiles of 256 rows, K in 1"),
+    (12800, 772, 704, "tiles of 256 rows, K in 1"),
+    (8160, 1365, 576, "tiles of 256 rows, K in 1"),
+    (8191, 4096, 7168, "tiles of 256 rows, K in 1"),
+    # K in parts that a second launch adds
+    (5471, 66, 2176, "tiles of 96 rows, K in 3"),
+    (2721, 40, 1368, "tiles of 96 rows, K in 6"),
+    (1633, 50, 4607, "tiles of 96 rows, K in 12"),
+    (4129, 260, 3712, "tiles of 128 rows, K in 3"),
+    (4223, 42, 2176, "tiles of 128 rows, K in 6"),
+    (2305, 40, 4480, "tiles of 128 rows, K in 12"),
+]
+
+
+@pytest.mark.parametrize("M,N,K,plan", GEMM_FORMS)
+def test_gemm_forms(C, M, N, K, plan):  # noqa: F811
+    """The streaming kernel and every height of tile, inputs cold, equal bits from
+    equal calls.  Value by value on a sample of rows (the first and last tiles and
+    200 of the rest) against the oracle's bound.  Row by row on all: half a step of
+    bf16 at every value, so of the row's norm; the sums' own errors are random and
+    far smaller (a row that is 1 % off, or another row, is not)."""
+    banner(f"gemm M={M} N={N} K={K} {plan}")
+    codes, scales, deq = weights(1, N, K, M)
+    w = C.chord_f8_pack(C.ROLE_PLAIN, codes.cuda(), scales.cuda())
+    q, s = C.chord_f8_quantize(activations(M, K, M + 1).cuda())
+    outs = cold_calls(lambda: C.chord_f8_gemm(q, s, w), 3)
+    assert C.last_plan() == "f8 gemm: " + plan
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    a = f8.dequantize(f8.decode(host(q.view(torch.uint8))), f64(s))[:, :K]
+    rng = np.random.default_rng(M)
+    ends = min(256, M)
+    rows = np.unique(np.concatenate([np.arange(ends), np.arange(M - ends, M), rng.integers(0, M, 200)]))
+    if K * N > 1 << 23:
+        rows = rows[::4]
+    got = f64(outs[0])
+    ref, bound = f8.gemm(a[rows], deq[0])
+    bound = bound + f8.HALF_BF16 * (np.abs(ref) + bound)
+    err = np.abs(got[rows] - ref)
+    assert np.all(err <= bound), (float((err / np.maximum(bound, 1e-300)).max()), rows[np.argwhere(err > bound)[:5, 0]])
+    whole = (torch.from_numpy(a).cuda() @ torch.from_numpy(deq[0].T.copy()).cuda()).cpu().numpy()
+    assert np.allclose(whole[rows], ref, rtol=0, atol=1e-9 * np.abs(ref).max())
+    off = np.linalg.norm(got - whole, axis=1) / np.linalg.norm(whole, axis=1)
+    assert np.all(off <= f8.HALF_BF16), (off.max(), np.argwhere(off > f8.HALF_BF16)[:5, 0])
+    banner(f"  worst row {off.max():.5f}")
