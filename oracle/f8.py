@@ -193,3 +193,9 @@ def route(logits, bias, k, sigmoid, n_group, topk_group, renorm, scaling):
             w = w / (w.sum() + 1e-20)
         weights[t, :len(order)] = w * scaling
     return ids, weights
+
+
+def rows_off(got, ref):
+    """Error of each row, over the row's norm (a row of zeros has to be zeros)."""
+    err, size = np.linalg.norm(got - ref, axis=1), np.linalg.norm(ref, axis=1)
+    return np.where(size > 0, err / np.where(size > 0, size, 1.0), np.where(err > 0, np.inf, 0.0))

@@ -93,7 +93,7 @@ struct Item {
 };
 
 // One item with G = 2 MG token groups of 16.
-template <int MG, int KIND, int ROWS, bool EXACT>
+template <int MG, int KIND, int ROWS, int EXACT>
 __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Scales<ROWS>& scales,
                                          const Item& it, __amdgpu_buffer_rsrc_t xres, Rsrc sres) {
   constexpr int G = 2 * MG;
@@ -180,11 +180,11 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
   };
   auto read_s = [&](int half, int ph, int g) { return scales.s[half][g * 16 + col][ph]; };
   const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-  // EXACT: blocks of at most 16 rows, whose second group is empty.  (Left alone,
-  // the widened weights of the next chunks would be kept, and spill.)
+  // EXACT: f8_exact_product for this many groups, the rest of a block being empty.
+  // (Left alone, the widened weights of the next chunks would be kept, and spill.)
   auto product = [&](i32x8_t wv, i32x8_t x, int g) {
-    if constexpr (EXACT) {
-      if (g > 0) return zero;
+    if constexpr (EXACT > 0) {
+      if (g >= EXACT) return zero;
       asm volatile("" : "+v"(wv), "+v"(x));
       return f8_exact_product(wv, x);
     } else {
@@ -416,7 +416,7 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
   }
 }
 
-template <int KIND, int ROWS, bool EXACT>
+template <int KIND, int ROWS, int EXACT>
 __device__ __forceinline__ void do_item(const F8GemmArgs& a, Smem<ROWS>& sm, Scales<ROWS>& scales,
                                         const Item& it) {
   const int64_t pitch = (int64_t)a.n_chunks * kF8Block, spitch = (int64_t)a.n_chunks * 4;
@@ -493,8 +493,8 @@ __global__ __launch_bounds__(256) void f8_add_parts(F8GemmArgs a) {
 }
 
 // Persistent workgroups.  Workgroup b runs on XCD b % 8.  OCC: waves per SIMD.
-// EXACT: f8_exact_product (gate_up over alignment blocks of 16 rows).
-template <int KIND, int ROWS, int OCC, bool EXACT>
+// EXACT: token groups by f8_exact_product (gate_up over alignment blocks: 1 or 2).
+template <int KIND, int ROWS, int OCC, int EXACT>
 __global__ __launch_bounds__(kThreads, OCC) void f8_tile(F8GemmArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   Smem<ROWS>& sm = *reinterpret_cast<Smem<ROWS>*>(smem);
@@ -581,18 +581,18 @@ hipError_t launch_f8_tile(const F8GemmArgs& a, bool small, hipStream_t stream) {
   };
   constexpr int R = kF8TileRows, S = kF8SmallRows;
   if (a.kind == kF8Plain) {
-    const hipError_t e = run(f8_tile<kF8Plain, R, 2, false>, 1, sizeof(Smem<R>));
+    const hipError_t e = run(f8_tile<kF8Plain, R, 2, 0>, 1, sizeof(Smem<R>));
     if (e != hipSuccess || a.parts <= 1) return e;
     const int64_t n = (a.a_rows * (a.n_tiles * 4) + 255) / 256, most = (int64_t)a.num_cus * 16;
     hipLaunchKernelGGL(f8_add_parts, dim3((unsigned)(n < most ? n : most)), dim3(256), 0, stream, a);
     return hipGetLastError();
   }
   if (a.kind == kF8GateUp)
-    return !small             ? run(f8_tile<kF8GateUp, R, 2, false>, 1, sizeof(Smem<R>))
-           : a.block_m <= 16 ? run(f8_tile<kF8GateUp, S, 4, true>, 2, sizeof(Smem<S>))
-                             : run(f8_tile<kF8GateUp, S, 4, false>, 2, sizeof(Smem<S>));
-  return small ? run(f8_tile<kF8Down, S, 4, false>, 2, sizeof(Smem<S>))
-               : run(f8_tile<kF8Down, R, 2, false>, 1, sizeof(Smem<R>));
+    return !small             ? run(f8_tile<kF8GateUp, R, 2, 0>, 1, sizeof(Smem<R>))
+           : a.block_m <= 16 ? run(f8_tile<kF8GateUp, S, 4, 1>, 2, sizeof(Smem<S>))
+                             : run(f8_tile<kF8GateUp, S, 4, 2>, 2, sizeof(Smem<S>));
+  return small ? run(f8_tile<kF8Down, S, 4, 0>, 2, sizeof(Smem<S>))
+               : run(f8_tile<kF8Down, R, 2, 0>, 1, sizeof(Smem<R>));
 }
 
 }  // namespace chord

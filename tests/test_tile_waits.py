@@ -150,7 +150,7 @@ def loop_of(assembly, kernel):
     raise AssertionError("no loop found")
 
 
-@pytest.mark.parametrize("kernel", ["f8_tileILi1ELi32ELi4ELb0", "f8_tileILi1ELi32ELi4ELb1"])
+@pytest.mark.parametrize("kernel", ["f8_tileILi1ELi32ELi4ELi1", "f8_tileILi1ELi32ELi4ELi2"])
 def test_a_lost_or_moved_load_is_noticed(assembly, kernel):
     """The same text with one load of weights taken out of the loop, with a larger
     count at a barrier, and with scales behind the rows.  (Weights three chunks ahead,
