@@ -188,3 +188,23 @@ def test_moe_every_row_of_many(C, T, H, I, E, k, hot, plan):  # noqa: F811
     assert off.max() <= 0.04
     if plan == "blocks of 32 rows":
         assert (off > f8.HALF_BF16).sum() <= max(1, T // 100), np.sort(off)[-T // 100 - 3:]
+
+
+def test_gemm_sums_inside_a_block_as_documented(C):  # noqa: F811
+    """A small term beside two that cancel: kept exactly where it stands in another
+    eight of the block, off by the grid of its own eight at most (7 products on
+    2^-13 of the largest's power of two) where it stands beside them."""
+    for where, exact in ((8, True), (120, True), (2, False), (7, False)):
+        x = torch.zeros((1, 128), dtype=torch.bfloat16)
+        codes = torch.zeros((1, 1, 128))
+        x[0, :2] = 1.0                      # code 448, scale 1 / 448
+        codes[0, 0, 0], codes[0, 0, 1] = 448.0, -448.0
+        x[0, where] = 2.0 ** -9             # code 0.875
+        codes[0, 0, where] = 1.0
+        w = C.chord_f8_pack(C.ROLE_PLAIN, codes.to(torch.float8_e4m3fn).cuda(), torch.ones((1, 1, 1), device="cuda"))
+        got = float(C.chord_f8_gemm(*C.chord_f8_quantize(x.cuda()), w))
+        want = 0.875 / 448
+        if exact:
+            assert abs(got - want) <= (f8.HALF_BF16 + 4 * f8.U32) * want
+        else:
+            assert abs(got - want) <= 7 * 2.0 ** -13 * 2.0 ** 17 / 448 * (1 + f8.HALF_BF16)
