@@ -39,10 +39,12 @@ __device__ __forceinline__ void store4(uint16_t* out, int64_t row, int64_t ld, i
     if (n + i < N) p[i] = to_bf16(v[i]);
 }
 
-// EXACT: f8_exact_product (gate_up).
-template <int NT, int MT, int WK, int PF, bool EXACT>
+// NT weight tiles x 16 tokens a workgroup, K over WK waves, PF chunks on their way.
+// GATE_UP: a layer's gate_up over alignment blocks (summed by f8_exact_product),
+// else the dense product.
+template <int NT, int WK, int PF, bool GATE_UP>
 __global__ __launch_bounds__(64 * WK) void f8_stream(F8GemmArgs a) {
-  __shared__ f32x4_t red[WK > 1 ? WK : 1][NT * MT][64];
+  __shared__ f32x4_t red[WK][NT][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, col = lane & 15;
@@ -52,39 +54,35 @@ __global__ __launch_bounds__(64 * WK) void f8_stream(F8GemmArgs a) {
   const int groups = (a.n_tiles + NT - 1) / NT;
   const int64_t pitch = (int64_t)nc * kF8Block;
   int64_t ntok;  // token tiles
-  if (a.kind == kF8Plain) {
-    ntok = (a.a_rows + MT * 16 - 1) / (MT * 16);
-  } else {
+  if (GATE_UP) {
     const int64_t used = max((int64_t)0, min((int64_t)*a.ntpp, a.max_padded));
     ntok = used / a.block_m;
+  } else {
+    ntok = (a.a_rows + 15) / 16;
   }
   for (int64_t item = blockIdx.x; item < ntok * groups; item += gridDim.x) {
     const int ti = (int)(item / groups);
     const int tile0 = (int)(item % groups) * NT;
     int e = 0;
-    int64_t row0 = (int64_t)ti * MT * 16;
-    if (a.kind != kF8Plain) {
+    if (GATE_UP) {
       e = a.expert_ids[ti];
-      row0 = (int64_t)ti * a.block_m;
       if (e < 0 || e >= a.num_experts) continue;  // uniform
     }
-    // Rows of this lane's tokens; lanes without one read row 0 and store
-    // nothing (their results touch no other token).
-    int64_t src[MT], dst[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int64_t r = row0 + m * 16 + col;
-      src[m] = 0;
-      dst[m] = -1;
-      if (a.kind == kF8Plain) {
-        if (r < a.a_rows) src[m] = dst[m] = r;
-      } else if (m * 16 + col < a.block_m) {
+    // Row of this lane's token; lanes without one read row 0 and store nothing
+    // (their results touch no other token).
+    int64_t src = 0, dst = -1;
+    if (GATE_UP) {
+      const int64_t r = (int64_t)ti * a.block_m + col;
+      if (col < a.block_m) {
         const int64_t f = a.sorted_ids[r];
         if (f >= 0 && f < a.n_flat) {
-          src[m] = f / a.topk;
-          dst[m] = r;
+          src = f / a.topk;
+          dst = r;
         }
       }
+    } else {
+      const int64_t r = (int64_t)ti * 16 + col;
+      if (r < a.a_rows) src = dst = r;
     }
     // NT divides 8, so the tiles of an item share their slice and their block(s)
     // of scales.
@@ -98,27 +96,20 @@ __global__ __launch_bounds__(64 * WK) void f8_stream(F8GemmArgs a) {
     }
     const float* s0;
     const float* s1;
-    if (a.kind == kF8GateUp) {
+    if (GATE_UP) {
       s0 = a.ws + ((int64_t)e * a.nb + tile0 / 16) * nc;
       s1 = s0 + (int64_t)(a.nb / 2) * nc;
     } else {
-      s0 = s1 = a.ws + ((int64_t)e * a.nb + tile0 / 8) * nc;
+      s0 = s1 = a.ws + (int64_t)(tile0 / 8) * nc;
     }
-    const uint8_t* xp[MT];
-    const float* sp[MT];
+    const uint8_t* xp = a.aq + src * pitch + q * 32;
+    const float* sp = a.as + src * nc;
+    f32x4_t acc[NT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      xp[m] = a.aq + src[m] * pitch + q * 32;
-      sp[m] = a.as + src[m] * nc;
-    }
-    f32x4_t acc[NT][MT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int m = 0; m < MT; ++m) acc[n][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int n = 0; n < NT; ++n) acc[n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-    uint4 w[PF][NT][2], x[PF][MT][2];
-    float sx[PF][MT], sw0[PF], sw1[PF];
+    uint4 w[PF][NT][2], x[PF][2];
+    float sx[PF], sw0[PF], sw1[PF];
     auto load = [&](int p, int c) {
       c = min(c, c_hi - 1);
 #pragma unroll
@@ -126,31 +117,24 @@ __global__ __launch_bounds__(64 * WK) void f8_stream(F8GemmArgs a) {
         w[p][n][0] = load_stream(wp[n] + (int64_t)c * wstep);
         w[p][n][1] = load_stream(wp[n] + (int64_t)c * wstep + 1024);
       }
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        x[p][m][0] = *reinterpret_cast<const uint4*>(xp[m] + c * kF8Block);
-        x[p][m][1] = *reinterpret_cast<const uint4*>(xp[m] + c * kF8Block + 16);
-        sx[p][m] = sp[m][c];
-      }
+      x[p][0] = *reinterpret_cast<const uint4*>(xp + c * kF8Block);
+      x[p][1] = *reinterpret_cast<const uint4*>(xp + c * kF8Block + 16);
+      sx[p] = sp[c];
       sw0[p] = s0[c];
       sw1[p] = s1[c];
     };
     auto compute = [&](int p) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const i32x8_t av = operand(w[p][n][0], w[p][n][1]);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-          const i32x8_t bv = operand(x[p][m][0], x[p][m][1]);
-          const f32x4_t r = EXACT ? f8_exact_product(av, bv)
+        const i32x8_t av = operand(w[p][n][0], w[p][n][1]), bv = operand(x[p][0], x[p][1]);
+        const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+        const f32x4_t r = GATE_UP ? f8_exact_product(av, bv)
                                   : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, zero, 0, 0, 0, 0, 0, 0);
-          const float f0 = sx[p][m] * sw0[p], f1 = sx[p][m] * sw1[p];
-          acc[n][m][0] = __builtin_fmaf(r[0], f0, acc[n][m][0]);
-          acc[n][m][1] = __builtin_fmaf(r[1], f1, acc[n][m][1]);
-          acc[n][m][2] = __builtin_fmaf(r[2], f0, acc[n][m][2]);
-          acc[n][m][3] = __builtin_fmaf(r[3], f1, acc[n][m][3]);
-        }
+        const float f0 = sx[p] * sw0[p], f1 = sx[p] * sw1[p];
+        acc[n][0] = __builtin_fmaf(r[0], f0, acc[n][0]);
+        acc[n][1] = __builtin_fmaf(r[1], f1, acc[n][1]);
+        acc[n][2] = __builtin_fmaf(r[2], f0, acc[n][2]);
+        acc[n][3] = __builtin_fmaf(r[3], f1, acc[n][3]);
       }
     };
     if (c_lo < c_hi) {
@@ -164,34 +148,24 @@ __global__ __launch_bounds__(64 * WK) void f8_stream(F8GemmArgs a) {
         }
       }
     }
-    if (WK > 1) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) red[wave][n][lane] = acc[n];
+    __syncthreads();
 #pragma unroll
-        for (int m = 0; m < MT; ++m) red[wave][n * MT + m][lane] = acc[n][m];
-      __syncthreads();
-    }
+    for (int n = 0; n < NT; ++n) {
+      if (n != wave) continue;  // (NT <= WK)
+      f32x4_t v = red[0][n][lane];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const int j = n * MT + m;
-        if (j % WK != wave) continue;
-        f32x4_t v = acc[n][m];
-        if (WK > 1) {
-          v = red[0][j][lane];
-#pragma unroll
-          for (int u = 1; u < WK; ++u) v += red[u][j][lane];
-        }
-        if (dst[m] < 0 || tile0 + n >= a.n_tiles) continue;
-        if (a.kind == kF8GateUp) {
-          float* h = static_cast<float*>(a.out) + dst[m] * a.ld + (tile0 + n) * 8 + 2 * q;
-          *reinterpret_cast<float2*>(h) = make_float2(silu_mul(v[0], v[1]), silu_mul(v[2], v[3]));
-        } else {
-          store4(static_cast<uint16_t*>(a.out), dst[m], a.ld, (tile0 + n) * 16 + 4 * q, a.N, v, wide);
-        }
+      for (int u = 1; u < WK; ++u) v += red[u][n][lane];
+      if (dst < 0 || tile0 + n >= a.n_tiles) continue;
+      if (GATE_UP) {
+        float* h = static_cast<float*>(a.out) + dst * a.ld + (tile0 + n) * 8 + 2 * q;
+        *reinterpret_cast<float2*>(h) = make_float2(silu_mul(v[0], v[1]), silu_mul(v[2], v[3]));
+      } else {
+        store4(static_cast<uint16_t*>(a.out), dst, a.ld, (tile0 + n) * 16 + 4 * q, a.N, v, wide);
       }
-    if (WK > 1) __syncthreads();
+    }
+    __syncthreads();
   }
 }
 
@@ -207,8 +181,8 @@ hipError_t launch_f8_gemm(const F8GemmArgs& a, hipStream_t stream) {
   };
   // A product alone has few tiles: one per workgroup, K over 8 waves (M = 1, N =
   // 4096, K = 7168: 12.8 us with two tiles and 4 waves, 7.8 so).
-  if (a.kind == kF8Plain) return run(f8_stream<1, 1, 8, 4, false>, 1, 8, 2);
-  return run(f8_stream<2, 1, 4, 4, true>, 2, 4, 4);
+  if (a.kind == kF8Plain) return run(f8_stream<1, 8, 4, false>, 1, 8, 2);
+  return run(f8_stream<2, 4, 4, true>, 2, 4, 4);
 }
 
 }  // namespace chord

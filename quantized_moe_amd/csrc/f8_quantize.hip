@@ -14,23 +14,20 @@ constexpr int kThreads = 256;
 constexpr int kGroupsPerPass = kThreads / 16;
 
 // Values j .. j+7 of a row as fp32, zeros from K on.  Wide: 16-byte aligned
-// rows with K % 8 == 0, so the 8 values are all there or none is.
+// rows with K % 8 == 0, so the 8 values are all there or none is.  (fp32 rows are a
+// layer's h, which are wide.)
 template <bool F32, bool WIDE>
 __device__ __forceinline__ void load8(const void* x, int64_t row, int j, int K, float (&v)[8]) {
+  static_assert(WIDE || !F32);
   if (F32) {
     const float* p = static_cast<const float*>(x) + row;
-    if (WIDE) {
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-      if (j < K) {
-        a = *reinterpret_cast<const float4*>(p + j);
-        b = *reinterpret_cast<const float4*>(p + j + 4);
-      }
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-      v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = j + i < K ? p[j + i] : 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    if (j < K) {
+      a = *reinterpret_cast<const float4*>(p + j);
+      b = *reinterpret_cast<const float4*>(p + j + 4);
     }
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     return;
   }
   const uint16_t* p = static_cast<const uint16_t*>(x) + row;
@@ -204,7 +201,6 @@ hipError_t launch_f8_quantize(const F8QuantArgs& a, hipStream_t stream) {
   const dim3 grid(grid_for(groups, kGroupsPerPass, 1 << 20)), block(kThreads);
   const int size = a.is_f32 ? 4 : 2;
   const bool wide = a.K % 8 == 0 && a.ld * size % 16 == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0;
-  // (fp32 rows are a layer's h, whose rows are wide.)
   if (a.is_f32 && !wide) return hipErrorInvalidValue;
   if (a.is_f32) hipLaunchKernelGGL((quantize_kernel<true, true>), grid, block, 0, stream, a);
   else if (wide) hipLaunchKernelGGL((quantize_kernel<false, true>), grid, block, 0, stream, a);

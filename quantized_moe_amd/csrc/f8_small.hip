@@ -8,8 +8,10 @@
 // with each wave quantising what it multiplies, 16 columns at a time whether
 // there are tokens for them or not; 18.5 so.)
 //
-// The values are those of the other forms: the same quantisation of the same
-// 128 columns, fp32 h and y, slots added in ascending order.
+// x and h are quantised as in the other forms, from the same 128 columns, and the
+// slots added in the same ascending order.  y never leaves the workgroup and stays
+// fp32 (fp16 with a shared exponent in the forms that write it to memory), and
+// gate_up is always summed in fp32.
 #include "f8_common.h"
 
 namespace chord {
