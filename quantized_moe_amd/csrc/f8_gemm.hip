@@ -9,10 +9,13 @@
 // operand (16 output features), tokens the B operand, so a lane's four results
 // belong to one token and share its scale.
 //
-// Bound by memory: weights of 4096 x 7168 for one token in 7.8 us with their
-// launch (3.8 TB/s; a launch of nothing is 3.5 us).  A weight tile is read again
-// for each 16 tokens, and a wave has few products beside its loads, so from
-// about a hundred tokens the tiled kernel is the faster one.
+// Bound by memory: weights of 4096 x 7168 for one token in 7.5 us with their
+// launch (a launch of nothing is 3.5 us).  Loads stop at the end of a wave's part of
+// K: with the last chunk loaded again in the place of those behind it the ring of
+// four took 8.5 us here, and 14.2 for 6.9 with two chunks a wave (16 tokens, 7168 x
+// 2048).  A weight tile is read again for each 16 tokens, and a wave has few products
+// beside its loads, so with long K and wide N the tiled kernel is the faster one
+// from about 30 tokens.
 #include "f8_common.h"
 
 namespace chord {
@@ -111,7 +114,6 @@ __global__ __launch_bounds__(64 * WK) void f8_stream(F8GemmArgs a) {
     uint4 w[PF][NT][2], x[PF][2];
     float sx[PF], sw0[PF], sw1[PF];
     auto load = [&](int p, int c) {
-      c = min(c, c_hi - 1);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         w[p][n][0] = load_stream(wp[n] + (int64_t)c * wstep);
@@ -139,12 +141,13 @@ __global__ __launch_bounds__(64 * WK) void f8_stream(F8GemmArgs a) {
     };
     if (c_lo < c_hi) {
 #pragma unroll
-      for (int p = 0; p < PF; ++p) load(p, c_lo + p);
+      for (int p = 0; p < PF; ++p)
+        if (c_lo + p < c_hi) load(p, c_lo + p);
       for (int c = c_lo; c < c_hi; c += PF) {
 #pragma unroll
         for (int p = 0; p < PF; ++p) {
           if (c + p < c_hi) compute(p);
-          load(p, c + p + PF);
+          if (c + p + PF < c_hi) load(p, c + p + PF);
         }
       }
     }

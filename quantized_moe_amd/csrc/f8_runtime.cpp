@@ -26,18 +26,27 @@ struct F8GemmPlan {
 
 // The cheapest by estimate, in us on an MI355X: a round of 256 workgroups takes
 // 4 and so much per chunk, adding parts 4.5 and its bytes.  Fitted to sweeps
-// over M = 1 .. 4096 with N = 512 .. 7168, K = 500 .. 7168; where both sides
+// over M = 1 .. 4096 with N = 128 .. 7168, K = 500 .. 7168; where both sides
 // were near (within 10 %) it may pick the slower.  Measured, stream / tiled:
-// M=8 N=4096 K=7168 9.8 / 15.4; M=32 22.8 / 15.8 (64 rows, 8 parts); M=100
-// N=576 12.0 / 14.4; M=100 N=2112 42.2 / 17.4; M=512 N=4096 rows x parts 64x2
-// 32.9, 128x4 34.3, 256x8 41.6; M=2048 128x1 60.4, 256x2 78.9, 64x1 89.5.
+// M=17 N=7168 K=2048 10.0 / 11.9; M=32 N=4096 K=512 3.8 / 8.8, K=7168 16.6 / 15.9;
+// M=100 N=576 K=7168 9.5 / 14.4, N=1024 K=1024 4.5 / 10.8, N=2112 K=7168 30.3 /
+// 17.4; M=128 N=1024 K=4096 9.6 / 14.3, N=4096 K=512 7.2 / 10.3, K=7168 58 / 23;
+// M=512 N=4096 rows x parts 64x2 32.9, 128x4 34.3, 256x8 41.6; M=2048 128x1 60.4,
+// 256x2 78.9, 64x1 89.5.  Up to 128 rows a round of the streaming kernel is given
+// what its chunks take and a launch of whole tiles 2.5 more; with more rows, where
+// a weight tile is read again more than eight times, a round 3.5 besides (M=200
+// N=4096 K=7168 89 / 25, N=2112 K=1024 9.5 / 11.7, N=1024 K=1024 5.8 / 11.0; M=400
+// N=2112 K=1024 14.8 / 12.6: short K would gain from the former there, too).
 F8GemmPlan f8_gemm_plan(int64_t M, int N, int K) {
   constexpr int64_t kCus = 256;  // (of the model, so that the workspace depends on sizes alone)
   const int nc = (int)f8_chunks(K);
   const int64_t tiles = f8_tiles(N), slices = (tiles + 15) / 16;
   F8GemmPlan best{true, 0, 1};
   if (M <= 16) return best;
-  double cost = 3.0 + std::max(1.0, (double)((M + 15) / 16 * tiles) / kCus) * (3.5 + 0.09 * nc);
+  const int64_t streams = (M + 15) / 16 * tiles;
+  double cost = 3.0 + std::max(1.0, (double)streams / kCus) * (3.5 + 0.09 * nc);
+  const bool few = M <= 128;
+  if (few) cost = std::min(cost, 3.0 + (double)((streams + kCus - 1) / kCus) * (0.1 + 0.113 * nc));
   const struct {
     int rows;
     double chunk;
@@ -49,6 +58,7 @@ F8GemmPlan f8_gemm_plan(int64_t M, int N, int K) {
       const double rounds = (double)((items * parts + kCus - 1) / kCus);
       double c = rounds * (4.0 + (nc + parts - 1) / parts * s.chunk);
       if (parts > 1) c += 4.5 + parts * (double)M * tiles * 16 * 8 / 4e6;
+      else if (few) c += 2.5;
       if (c < cost) {
         cost = c;
         best = F8GemmPlan{false, s.rows, parts};

@@ -68,7 +68,11 @@ GEMM_FORMS = [
     # M, N, K, plan: the last tile has 1, 33, .. rows, so every count of token
     # groups up to the tallest; 0 to 3 chunks behind the loop of four; ragged N
     (12, 300, 900, "streaming"),
+    (100, 1024, 1024, "streaming"),
     (200, 520, 4000, "tiles of 64 rows, K in 8"),
+    (161, 1300, 640, "tiles of 64 rows, K in 1"),
+    (225, 1300, 768, "tiles of 64 rows, K in 1"),
+    (255, 1300, 896, "tiles of 64 rows, K in 1"),
     (5473, 553, 1024, "tiles of 96 rows, K in 1"),
     (5601, 516, 640, "tiles of 96 rows, K in 1"),
     (5663, 515, 768, "tiles of 96 rows, K in 1"),
