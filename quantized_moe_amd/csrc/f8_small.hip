@@ -118,7 +118,10 @@ __global__ __launch_bounds__(kThreads) void small_gate_up(F8SmallArgs a) {
   const int nt = a.I / 8, nc = a.H / kF8Block, nb = 2 * a.I / kF8Block;
   const int c_lo = nc * wave / kWaves, c_hi = nc * (wave + 1) / kWaves;
   const int wstep = f8_slice_width(0, nt) * kF8BlockBytes;  // (2 I is a multiple of 256)
-  constexpr int PF = 7;
+  // Chunks on their way.  Deeper than needed costs registers, so waves (T = 1: 8
+  // experts of 7168 x 256, 4096 x 512 and 2048 x 768 with 4, 7, 8 and 10 chunks 18.8,
+  // 18.4, 18.6, 29.7; 19.4, 19.2, 19.4, 30.3; 18.9, 19.1, 19.2, 24.9 us for the layer).
+  constexpr int PF = 8;
   for (int item = blockIdx.x; item < rt.tiles * nt; item += gridDim.x) {
     const int ti = item / nt, t = item - ti * nt, e = rt.expert[ti];
     const bool live = col < rt.rows[ti];
@@ -132,7 +135,8 @@ __global__ __launch_bounds__(kThreads) void small_gate_up(F8SmallArgs a) {
     u32x4_t w[PF][2];
     if (c_lo < c_hi) {
 #pragma unroll
-      for (int p = 0; p < PF; ++p) load_w(w[p], wp + (int64_t)min(c_lo + p, c_hi - 1) * wstep);
+      for (int p = 0; p < PF; ++p)
+        if (c_lo + p < c_hi) load_w(w[p], wp + (int64_t)(c_lo + p) * wstep);
       for (int c0 = c_lo; c0 < c_hi; c0 += PF) {
 #pragma unroll
         for (int p = 0; p < PF; ++p) {
@@ -191,7 +195,8 @@ __global__ __launch_bounds__(kThreads) void small_down(F8SmallArgs a) {
       f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
       u32x4_t w[PF][2];
 #pragma unroll
-      for (int p = 0; p < PF; ++p) load_w(w[p], wp + (int64_t)min(p, nc - 1) * wstep);
+      for (int p = 0; p < PF; ++p)
+        if (p < nc) load_w(w[p], wp + (int64_t)p * wstep);
       for (int c0 = 0; c0 < nc; c0 += PF) {
 #pragma unroll
         for (int p = 0; p < PF; ++p) {
