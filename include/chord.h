@@ -656,7 +656,8 @@ size_t chord_f8_moe_workspace_bytes(int T, int k, int E_l, int H, int I);
  * out:      device bf16 [T, H], 16-byte aligned; every row is written.
  * workspace: chord_f8_moe_workspace_bytes(...) bytes, 256-byte aligned,
  *           caller-owned; calls that may overlap need one each.
- * T*k*H must stay below 2^30.  T == 0 is a no-op.
+ * T*k must stay below 2^30, and T*H and I times the aligned rows (at most T*k +
+ * 31 E_l) below 2^31.  T == 0 is a no-op.
  */
 chord_status chord_f8_moe(const chord_bf16* x, int T, int H, int I, const chord_f8_weight* w13,
                           const chord_f8_weight* w2, const int32_t* topk_ids,

@@ -211,10 +211,11 @@ chord_status check_moe_sizes(int T, int k, int E_l, int H, int I) {
     return fail(CHORD_ERR_UNSUPPORTED, "H=%d and I=%d must be multiples of 128", H, I);
   if (E_l > kMaxExperts) return fail(CHORD_ERR_UNSUPPORTED, "more than %d local experts", kMaxExperts);
   const int64_t slots = (int64_t)T * k;
-  if (slots >= (int64_t)1 << 30 || slots * H * 2 > kMaxOperand)
-    return fail(CHORD_ERR_UNSUPPORTED, "T*k*H exceeds 2^30");
+  if (slots >= (int64_t)1 << 30) return fail(CHORD_ERR_UNSUPPORTED, "T*k=%lld", (long long)slots);
+  // (Codes of x and h are loaded with 32-bit offsets; y is stored with 64-bit ones.)
+  if ((int64_t)T * H > kMaxOperand) return fail(CHORD_ERR_UNSUPPORTED, "codes of x exceed 2 GiB");
   const int64_t rows = chord_moe_align_max_padded(T, k, E_l, kF8MaxBlockM);
-  if (rows * I > kMaxOperand) return fail(CHORD_ERR_UNSUPPORTED, "rows of h exceed 2 GiB");
+  if (rows * I > kMaxOperand) return fail(CHORD_ERR_UNSUPPORTED, "codes of h exceed 2 GiB");
   return CHORD_OK;
 }
 

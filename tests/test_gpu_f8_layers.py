@@ -212,3 +212,28 @@ def test_gemm_sums_inside_a_block_as_documented(C):  # noqa: F811
             assert abs(got - want) <= (f8.HALF_BF16 + 4 * f8.U32) * want
         else:
             assert abs(got - want) <= 7 * 2.0 ** -13 * 2.0 ** 17 / 448 * (1 + f8.HALF_BF16)
+
+
+def test_moe_slots_past_32_bits(C):  # noqa: F811
+    """40000 tokens of 8 slots and 7168 outputs: y of the last slots lies past 4 GiB.
+    Tokens without a local expert are zeros, a sample of the others (first, last,
+    and between) is compared with the oracle."""
+    T, H, I, E, E_g, k = 40000, 7168, 128, 2, 64, 8
+    banner(f"f8 moe T={T} H={H} I={I} E={E} k={k}")
+    layer, d13, d2 = make_layer(E, H, I, 21)
+    rng = np.random.default_rng(22)
+    ids = np.argsort(rng.random((T, E_g)), axis=1)[:, :k].astype(np.int32)
+    w = rng.uniform(0.1, 1.0, (T, k)).astype(np.float32)
+    ids[-3:, -1] = [0, 1, 0]   # (the very last slot is local; an expert may stand twice)
+    g = torch.Generator(device="cuda").manual_seed(23)
+    x = torch.randn((T, H), generator=g, device="cuda").bfloat16()
+    got = layer.indexed(x, torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda(), 0, E_g)
+    local = (ids < E).any(axis=1)
+    rows = np.nonzero(local)[0]
+    rows = np.concatenate([rows[:20], rng.choice(rows, 60, replace=False), rows[-40:]])
+    assert not got[torch.from_numpy(~local).cuda()].any()
+    at = torch.from_numpy(rows).cuda()
+    ref, bound, _ = f8.moe(f64(x[at]), ids[rows], w[rows], d13, d2, 0)
+    part = f64(got[at])
+    assert np.all(np.abs(part - ref) <= bound)
+    assert f8.rows_off(part, ref).max() <= 0.04
