@@ -517,8 +517,8 @@ typedef enum { CHORD_SCORE_SOFTMAX = 0, CHORD_SCORE_SIGMOID = 1 } chord_scoring;
  * bias:         device fp32 [E], or NULL.
  * topk_ids:     device int32 [T, k] out; topk_weights: device fp32 [T, k] out.
  * 1 <= E <= 1024; 1 <= k <= min(32, topk_group * E / n_group); n_group divides
- * E, is at most 64, and 1 <= topk_group <= n_group (1, 1: no groups).  T == 0 is
- * a no-op.  Enqueued on `stream`; needs no workspace.
+ * E, is at most 64, and 1 <= topk_group <= n_group (1, 1: no groups).  T is at
+ * most 2^25; T == 0 is a no-op.  Enqueued on `stream`; needs no workspace.
  */
 chord_status chord_moe_route(const void* logits, int dtype, int64_t ld, int T, int E,
                              const float* bias, int k, int scoring, int n_group, int topk_group,

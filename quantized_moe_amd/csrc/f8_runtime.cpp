@@ -12,6 +12,8 @@ namespace {
 
 constexpr int kRouteMaxK = 32;
 constexpr int kRouteMaxGroups = 64;
+// One wave a token, and a launch has fewer than 2^32 threads.
+constexpr int kRouteMaxTokens = 1 << 25;
 // Codes of one expert are addressed with 32-bit offsets.
 constexpr int64_t kMaxOperand = ((int64_t)1 << 31) - 1;
 
@@ -246,6 +248,7 @@ chord_status chord_moe_route(const void* logits, int dtype, int64_t ld, int T, i
                 kRouteMaxK, topk_group * (E / n_group));
   if (!std::isfinite(scaling))
     return fail(CHORD_ERR_INVALID_ARGUMENT, "scaling is not finite");
+  if (T > kRouteMaxTokens) return fail(CHORD_ERR_UNSUPPORTED, "T=%d above %d", T, kRouteMaxTokens);
   if (T == 0) return CHORD_OK;
   if (!logits || !topk_ids || !topk_weights)
     return fail(CHORD_ERR_INVALID_ARGUMENT, "null pointer argument");
