@@ -236,9 +236,11 @@ __global__ __launch_bounds__(kThreads) void small_down(F8SmallArgs a) {
 constexpr int64_t kRowBytes = 68 << 10;
 int64_t row_bytes(int64_t rows, int K) { return rows * (K + K / kF8Block * 4); }
 
-// Every workgroup quantises all rows, so with more slots the other forms win:
-// T * k = 32 (48 experts of 2048 x 7168) 198 us here, 216 there; 63 (I = 256) 89
-// and 85; 64 (16 experts of 1024 x 2048) 52 and 43.
+// Every workgroup quantises all rows, so with more slots the other forms win, the
+// sooner the smaller the weights (here / there, in us): 24 slots, 64 experts of 7168
+// x 256 37 / 50, 32 slots 45 / 52, 56 slots 64 / 68; 32 slots, 48 experts of 7168 x
+// 2048 206 / 212, 16 of 1024 x 512 22 / 26, 64 of 2048 x 768 49 / 42; 64 slots 26 /
+// 27 and 69 / 60, 16 of 1024 x 2048 43 / 43.
 constexpr int kSmallSlots = 32;
 
 bool f8_small_fits(int T, int k, int H, int I) {
