@@ -50,23 +50,26 @@ __device__ __forceinline__ uint32_t f8_pack4(float a, float b, float c, float d)
 // neighbouring codes a large h gets, and 2 to 4 of a hundred tokens are then off by
 // up to 0.0185 of their norm, where this product leaves 0.0022 (bf16 alone: 0.0017
 // on average).  So gate_up takes it wherever the weights' bytes are the bound, in
-// every form over alignment blocks: 64 tokens on 48 experts 174 to 182 us either
-// way, 512 tokens of 384 experts 244 us for 224.  Over large tiles the widening
-// takes longer than the products (8192 tokens on 48 experts: 775 us for 330), so
+// every form over alignment blocks, at no cost in time there: 64 tokens on 48
+// experts 173 us for 176, 512 tokens of 384 experts 222 for 225.  Over large tiles
+// the widening takes longer than the products (8192 tokens on 48 experts: 775 us for
+// 330, with no register to keep widened weights in), so
 // there the 8-bit instruction stays; the error over all outputs is 0.0019 to 0.0024.
 typedef __attribute__((ext_vector_type(8))) _Float16 half8_t;
-__device__ __forceinline__ half8_t f8_widen(int lo, int hi) {
-  const half2_t a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, false);
-  const half2_t b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, true);
-  const half2_t c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, false);
-  const half2_t d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, true);
+// (`one` is 1, as the conversions' scale.)
+__device__ __forceinline__ half8_t f8_widen(int lo, int hi, float one) {
+  const half2_t a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, one, false);
+  const half2_t b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, one, true);
+  const half2_t c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, one, false);
+  const half2_t d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, one, true);
   return half8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
-__device__ __forceinline__ f32x4_t f8_exact_product(i32x8_t a, i32x8_t b) {
+__device__ __forceinline__ f32x4_t f8_exact_product(i32x8_t a, i32x8_t b, float one = 1.f) {
   f32x4_t r = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int j = 0; j < 8; j += 2)
-    r = __builtin_amdgcn_mfma_f32_16x16x32_f16(f8_widen(a[j], a[j + 1]), f8_widen(b[j], b[j + 1]), r, 0, 0, 0);
+    r = __builtin_amdgcn_mfma_f32_16x16x32_f16(f8_widen(a[j], a[j + 1], one), f8_widen(b[j], b[j + 1], one), r,
+                                               0, 0, 0);
   return r;
 }
 

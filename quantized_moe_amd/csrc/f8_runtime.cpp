@@ -176,19 +176,18 @@ struct F8MoePlan {
 // - gate_up by the streaming kernel, whose many small workgroups start at once,
 //   as long as they are few (w < 3 a CU), else by tiles, which read a block's
 //   tokens once (streaming / tiled): 4 experts of 7168 x 256 with 20 rows each
-//   (w = 112) 33 / 54, with 120 (w = 272) 49 / 67; of 4096 x 1024 with 25 (w = 538)
-//   45 / 50, with 100 (w = 947) 60 / 54; 16 of 2048 x 768 with 12 (w = 921) 42 / 38;
-//   110 of 2048 x 768 with 2 (w = 5280) 139 / 111.
+//   (w = 112) 34 / 54, with 120 (w = 272) 47 / 70; of 4096 x 1024 with 25 (w = 538)
+//   41 / 50, with 100 (w = 1728) 86 / 87; 16 of 2048 x 768 with 12 (w = 921) 40 / 38.
 // - Tiles over alignment blocks, two workgroups a CU and gate_up in fp32 sums, below
 //   24 rows an expert, else tiles over up to 224 rows of an expert (blocks /
-//   large): 16 rows 412 / 413 and 447 / 462, 24 rows 488 / 421 and 530 / 478 (48
+//   large): 16 rows 385 / 416 and 426 / 463, 24 rows 458 / 422 and 507 / 479 (48
 //   experts of 7168 x 2048, 384 of 7168 x 256).  Also above where the blocks' tiles
 //   leave a CU one workgroup, within 15 % either way and exact: 8 of 1024 x 512 with
-//   50 rows 34 / 38, 16 of 640 x 768 with 50 36 / 39, 4 of 4096 x 1024 with 50 58 /
-//   57 and with 100 69 / 60, 2 of 7168 x 1024 with 100 84 / 75; with more workgroups
-//   it does not pay: 16 of 2048 x 768 with 100 92 / 57.
-// - Blocks of 32 rows above 8 an expert (16 / 32 rows): 10.7 rows 395 / 401 and 441 /
-//   425, 16 rows 533 / 412 and 588 / 447, 4 rows 353 / 388 and 362 / 399.
+//   50 rows 32 / 37, 16 of 640 x 768 with 50 33 / 38, 4 of 4096 x 1024 with 50 57 /
+//   57 and with 100 67 / 60, 2 of 7168 x 1024 with 100 82 / 76; with more workgroups
+//   it does not pay: 16 of 2048 x 768 with 100 84 / 57.
+// - Blocks of 32 rows above 8 an expert (16 / 32 rows): 10.7 rows 392 / 372 and 441 /
+//   402, 16 rows 530 / 385 and 588 / 426, 4 rows 353 / 355 and 363 / 367.
 F8MoePlan f8_moe_plan(int T, int k, int E_g, int E_l, int I, int cus) {
   const int eg = E_g > E_l ? E_g : E_l;
   const double tok_e = (double)T * k / eg;

@@ -16,10 +16,10 @@ namespace {
 constexpr int kWavesPerBlock = 4;
 constexpr int kRing = 4;      // tiles in flight
 // Tiles per wave at most (about: they come in pairs).  Of little weight: with 16, 24,
-// 32 and 48 a layer of 512 tokens on 384 experts of 7168 x 256 takes 441, 427, 438,
-// 436 us, of 256 tokens on 160 of 5120 x 256 174, 175, 174, 173, on 256 of 2048 x 128
-// 67, 67, 68, 67.
-constexpr int kPart = 24;
+// 28, 32 and 48 a layer of 512 tokens on 384 experts of 7168 x 256 takes 441, 434, 428,
+// 438, 436 us, of 256 tokens on 160 of 5120 x 256 174, 175, 177, 174, 173, on 256 of
+// 2048 x 128 67, 67, 68, 68, 67.
+constexpr int kPart = 28;
 
 __device__ __forceinline__ i32x8_t operand(u32x4_t a, u32x4_t b) {
   return i32x8_t{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};

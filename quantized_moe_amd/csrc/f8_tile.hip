@@ -181,12 +181,14 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
   auto read_s = [&](int half, int ph, int g) { return scales.s[half][g * 16 + col][ph]; };
   const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
   // EXACT: f8_exact_product for this many groups, the rest of a block being empty.
-  // (Left alone, the widened weights of the next chunks would be kept, and spill.)
+  // (With a constant 1 the widened weights of the next products would be kept, and
+  // spill.)
   auto product = [&](i32x8_t wv, i32x8_t x, int g) {
     if constexpr (EXACT > 0) {
       if (g >= EXACT) return zero;
-      asm volatile("" : "+v"(wv), "+v"(x));
-      return f8_exact_product(wv, x);
+      float one = 1.f;
+      asm volatile("" : "+s"(one));
+      return f8_exact_product(wv, x, one);
     } else {
       return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, x, zero, 0, 0, 0, 0, 0, 0);
     }
@@ -196,6 +198,7 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
   f32x4_t r[2][2] = {{zero, zero}, {zero, zero}};
   float f0 = 0.f, f1 = 0.f;  // factors of the results in r
   auto scale_in = [&](int n, int g) {
+    if (EXACT > 0 && g >= EXACT) return;
     acc[n][g][0] = __builtin_fmaf(r[g & 1][n][0], f0, acc[n][g][0]);
     acc[n][g][1] = __builtin_fmaf(r[g & 1][n][1], f1, acc[n][g][1]);
     acc[n][g][2] = __builtin_fmaf(r[g & 1][n][2], f0, acc[n][g][2]);
@@ -231,6 +234,12 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
     const float n0 = s0[c1], n1 = s1[c1];
     const i32x8_t w0 = operand(w[b % WR][0][0], w[b % WR][0][1]);
     const i32x8_t w1 = operand(w[b % WR][1][0], w[b % WR][1][1]);
+    if constexpr (EXACT > 0) {
+      if (!last)
+#pragma unroll
+        for (int j = 0; j < kW; ++j) load_w(j, (b + WR - 1) % WR, c3);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     // Fences after every matrix instruction keep this order: one matrix
     // instruction, then the multiply-adds of the one two places before it (left
     // alone, the compiler puts those right behind their own instruction, with
@@ -241,18 +250,29 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
       if (g == G / 2 && !last && (b == 0 || b == 3)) barrier(std::integral_constant<int, kBehind>{});
       if (g == G / 2 && last && b == 0) barrier(std::integral_constant<int, kBehindLast + kDma>{});
       if (g == G / 2 && last && b == 1) barrier(std::integral_constant<int, kBehindLast>{});
-      r[g & 1][0] = product(w0, xv[g & 1], g);
-      xv[(g + 1) & 1] = g + 1 < G ? read_x(b, g + 1) : read_x(nb, 0);
-      scale_in(0, (g + G - 1) % G);
-      __builtin_amdgcn_sched_barrier(0);
-      r[g & 1][1] = product(w1, xv[g & 1], g);
-      scale_in(1, (g + G - 1) % G);
-      f0 = sx[g & 1] * sw0;
-      f1 = KIND == kF8GateUp ? sx[g & 1] * sw1 : f0;
+      if constexpr (EXACT > 0) {
+        // (Scaled at once: the registers that hold results over a group would spill.)
+        r[g & 1][0] = product(w0, xv[g & 1], g);
+        r[g & 1][1] = product(w1, xv[g & 1], g);
+        xv[(g + 1) & 1] = g + 1 < G ? read_x(b, g + 1) : read_x(nb, 0);
+        f0 = sx[g & 1] * sw0;
+        f1 = sx[g & 1] * sw1;
+        scale_in(0, g);
+        scale_in(1, g);
+      } else {
+        r[g & 1][0] = product(w0, xv[g & 1], g);
+        xv[(g + 1) & 1] = g + 1 < G ? read_x(b, g + 1) : read_x(nb, 0);
+        scale_in(0, (g + G - 1) % G);
+        __builtin_amdgcn_sched_barrier(0);
+        r[g & 1][1] = product(w1, xv[g & 1], g);
+        scale_in(1, (g + G - 1) % G);
+        f0 = sx[g & 1] * sw0;
+        f1 = KIND == kF8GateUp ? sx[g & 1] * sw1 : f0;
+      }
       sx[(g + 1) & 1] = g + 1 < G ? read_s(half, b, g + 1) : read_s(b == 3 ? 1 - half : half, nb, 0);
 #pragma unroll
       for (int j = 0; j < kW; ++j)
-        if ((!last || WR == 2) && g < G / 2 && j * (G / 2) / kW == g) load_w(j, (b + WR - 1) % WR, WR == 4 ? c3 : c1);
+        if (EXACT == 0 && (!last || WR == 2) && g < G / 2 && j * (G / 2) / kW == g) load_w(j, (b + WR - 1) % WR, WR == 4 ? c3 : c1);
       if (!last && g == G / 2 && b < 2) load_s(b, 1 - half, c - b + 4);
 #pragma unroll
       for (int j = 0; j < kDma; ++j)
@@ -312,8 +332,10 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
   else used(1);
   if (c + 2 < nc) chunk(2, c + 2, half, behind_loop);
   else used(2);
-  scale_in(0, G - 1);
-  scale_in(1, G - 1);
+  if (EXACT == 0) {
+    scale_in(0, G - 1);
+    scale_in(1, G - 1);
+  }
   // The repeated loads at the end land before their buffers are used again.
   __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));
 
