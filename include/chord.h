@@ -637,12 +637,13 @@ size_t chord_f8_moe_workspace_bytes(int T, int k, int E_l, int H, int I);
  * NaN stays so and leaves the outputs beside it as they are.  The sum is fp32 and
  * rounded once.
  *
- * Products of gate_up are summed in fp32 where rows per expert are few (below 24
- * on average, and up to a few hundred where the layer is small): a token is then
- * off by its rounding to bf16, 0.0017 of its norm, at most 0.0022 in the tests.
- * With more rows the 8-bit matrix instruction sums them (as chord_f8_gemm says),
- * which can give a value of h the neighbouring code: 2 to 4 of a hundred tokens are
- * off by more than half a step of bf16 (2^-8 of the norm), the worst by 0.0185.
+ * Products of gate_up are summed in fp32 below 64 rows an expert (on average over
+ * the global experts): a token is then off by its rounding to bf16, 0.0017 of its
+ * norm, at most 0.0026 in the tests.  With more rows, where fp32 sums would take up to
+ * a quarter more time, the 8-bit matrix instruction sums them (as chord_f8_gemm
+ * says), which can give a value of h the neighbouring code: 2 to 4 of a hundred tokens
+ * are off by more than half a step of bf16 (2^-8 of the norm), the worst by 0.0185.
+ * CHORD_F8_FP32_SUMS=1 in the environment (read once) takes fp32 sums at every size.
  * The down product is summed by that instruction in every form; nothing is
  * quantised behind it, and its error is small beside the rounding to bf16.
  *

@@ -48,14 +48,13 @@ __device__ __forceinline__ uint32_t f8_pack4(float a, float b, float c, float d)
 // those of fp32.  The 8-bit instruction sums eights of products on a grid of 2^-13
 // of the largest; behind gate_up the difference decides now and then which of two
 // neighbouring codes a large h gets, and 2 to 4 of a hundred tokens are then off by
-// up to 0.0185 of their norm, where this product leaves 0.0022 (bf16 alone: 0.0017
-// on average).  So gate_up takes it wherever the weights' bytes are the bound, in
-// every form over alignment blocks, at no cost in time there: 64 tokens on 48
-// experts 173 us for 176, 512 tokens of 384 experts 222 for 225.  Large tiles are
-// bound by the products, twice as many matrix cycles in fp16 (8192 tokens on 48
-// experts: 510 us for 330 with weights widened once a chunk, 520 with tokens brought
-// as fp16), so the 8-bit instruction stays there; the error over all outputs is 0.0019
-// to 0.0024.
+// up to 0.0185 of their norm, where this product leaves 0.0026 (bf16 alone: 0.0017
+// on average).  So gate_up takes it wherever the weights' bytes are the bound, at no
+// cost in time there: 64 tokens on 48 experts 173 us for 176, 512 tokens of 384
+// experts 222 for 225.  Large tiles of many rows are bound by the products, twice as
+// many matrix cycles in fp16 (8192 tokens on 48 experts: 510 us for 330 with weights
+// widened once a chunk, 520 with tokens brought as fp16), so from 64 rows an expert
+// on the 8-bit instruction stays; the error over all outputs is 0.0019 to 0.0024.
 typedef __attribute__((ext_vector_type(8))) _Float16 half8_t;
 // (`one` is 1, as the conversions' scale.)
 __device__ __forceinline__ half8_t f8_widen(int lo, int hi, float one) {

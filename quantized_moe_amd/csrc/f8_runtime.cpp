@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
+#include <cstdlib>
 
 #include "host.h"
 
@@ -168,6 +169,7 @@ struct F8MoePlan {
   int block_m;          // rows per alignment block
   bool small;           // tiled GEMMs over the alignment blocks (else over built tiles)
   bool stream_gate_up;  // small: gate_up by the weight-streaming kernel
+  bool exact;           // large: gate_up in fp32 sums (else they always are)
   int blocks;           // expected alignment blocks with rows
   const char* text;
 };
@@ -188,6 +190,19 @@ struct F8MoePlan {
 //   it does not pay: 16 of 2048 x 768 with 100 84 / 57.
 // - Blocks of 32 rows above 8 an expert (16 / 32 rows): 10.7 rows 392 / 372 and 441 /
 //   402, 16 rows 530 / 385 and 588 / 426, 4 rows 353 / 355 and 363 / 367.
+// - Large tiles: gate_up in fp32 sums below 64 rows an expert, where the weights' bytes
+//   are still the bound, else summed by the 8-bit instruction (fp32 / 8-bit): 43 rows
+//   443 / 443 and 552 / 556, 54 rows 455 / 454, 71 rows 498 / 483, 85 rows 532 / 504 and
+//   716 / 703, 128 rows 658 / 568, 170 rows 797 / 634 (48 experts of 7168 x 2048, 384 of
+//   7168 x 256); 100 rows 61 / 57 (16 of 2048 x 768).  CHORD_F8_FP32_SUMS=1
+//   (environment, read once) takes fp32 sums at every size.
+bool fp32_sums() {
+  static const bool on = [] {
+    const char* s = getenv("CHORD_F8_FP32_SUMS");
+    return s != nullptr && atoi(s) != 0;
+  }();
+  return on;
+}
 F8MoePlan f8_moe_plan(int T, int k, int E_g, int E_l, int I, int cus) {
   const int eg = E_g > E_l ? E_g : E_l;
   const double tok_e = (double)T * k / eg;
@@ -199,6 +214,7 @@ F8MoePlan f8_moe_plan(int T, int k, int E_g, int E_l, int I, int cus) {
   p.small = p.stream_gate_up || tok_e < 24.0 || blocks(32) * (2 * I / 256) < cus;
   p.block_m = p.small && !p.stream_gate_up && tok_e > 8.0 ? 32 : 16;
   p.blocks = (int)std::min(blocks(p.block_m), 1e9);
+  p.exact = tok_e < 64.0 || fp32_sums();
   p.text = !p.small ? "f8 moe: tiles of up to 224 rows"
            : p.stream_gate_up ? "f8 moe: blocks of 16 rows, streaming gate_up"
            : p.block_m == 16 ? "f8 moe: blocks of 16 rows" : "f8 moe: blocks of 32 rows";
@@ -508,6 +524,7 @@ chord_status chord_f8_moe(const chord_bf16* x, int T, int H, int I, const chord_
   } else {
     g.out = hq;
     g.hs = hs;
+    g.exact = plan.exact;
     HIP_TRY(launch_f8_tile(g, plan.small, st), "gate_up launch");
   }
 

@@ -42,6 +42,7 @@ constexpr int kTiles = 16;                // weight tiles per workgroup
 constexpr int kStages = 4;                // chunks: one in use, three on their way
 constexpr int kXcds = 8;
 constexpr int kStreamAux = 2;             // non-temporal
+constexpr int kEvery = 16;                // EXACT: every group of a tall tile
 
 typedef const __attribute__((address_space(4))) float ConstFloat;
 
@@ -139,8 +140,11 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
   const int o1 = f8_block(t1, c_lo, a.n_tiles, a.n_chunks) * kF8BlockBytes;
   const int wstep = f8_slice_width(t0, a.n_tiles) * kF8BlockBytes;  // chunk to chunk
   // Weight registers: as far ahead as the tokens where the accumulators leave
-  // room, else one chunk.
-  constexpr int WR = G <= 12 ? 4 : 2;
+  // room, else one chunk; two where weights are widened when a chunk begins, which
+  // frees their registers for those of the next but one.
+  constexpr bool kWiden = EXACT == kEvery;
+  constexpr int WR = G <= 12 && !kWiden ? 4 : 2;
+  constexpr int kAhead = WR == 4 ? 3 : kWiden ? 2 : 1;
   u32x4_t w[WR][2][2];
   constexpr int kW = 4;  // loads of weights per chunk
   auto load_x = [&](int j, int b, int c) {
@@ -180,7 +184,8 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
   };
   auto read_s = [&](int half, int ph, int g) { return scales.s[half][g * 16 + col][ph]; };
   const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-  // EXACT: f8_exact_product for this many groups, the rest of a block being empty.
+  // EXACT: f8_exact_product for this many groups, the rest of a block being empty
+  // (kEvery: for all, below).
   // (With a constant 1 the widened weights of the next products would be kept, and
   // spill.)
   auto product = [&](i32x8_t wv, i32x8_t x, int g) {
@@ -220,24 +225,34 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
   // may be younger than the tokens of chunk c + 1: a chunk's weights, the tokens
   // of chunk c + 2 with (in two chunks of four) half of the next scales in front
   // of them, and this chunk's weights.
-  // Behind the loop (last) nothing is loaded any more, but for the next chunk's
-  // weights where they are only one chunk ahead; the counts there take no weights
-  // for granted, since the compiler drops loads whose registers nobody reads.
+  // Behind the loop (last) nothing is loaded any more, but for the weights that a
+  // chunk there needs where they are one or two chunks ahead; the counts there take
+  // no weights for granted, since the compiler drops loads whose registers nobody
+  // reads.
   // (With one chunk ahead the chunk's own weights, already waited for, are
   // younger than the tokens of chunk c + 1.)
   constexpr int kBehind = 2 * kW + kDma;
-  constexpr int kBehindLast = WR == 4 ? 0 : kW;
+  constexpr int kBehindLast = kAhead == 3 ? 0 : kW;
   auto chunk = [&](int b, int c, int half, auto is_last) {
     constexpr bool last = decltype(is_last)::value;
     const int nb = (b + 1) % kStages, fb = (b + 3) % kStages;
-    const int c1 = min(c + 1, nc - 1), c3 = min(c + 3, nc - 1);
+    const int c1 = min(c + 1, nc - 1), c3 = min(c + 3, nc - 1), cw = min(c + kAhead, nc - 1);
     const float n0 = s0[c1], n1 = s1[c1];
     const i32x8_t w0 = operand(w[b % WR][0][0], w[b % WR][0][1]);
     const i32x8_t w1 = operand(w[b % WR][1][0], w[b % WR][1][1]);
-    if constexpr (EXACT > 0) {
-      if (!last)
+    half8_t h[2][4];
+    if constexpr (kWiden) {
 #pragma unroll
-        for (int j = 0; j < kW; ++j) load_w(j, (b + WR - 1) % WR, c3);
+      for (int j = 0; j < 4; ++j) {
+        h[0][j] = f8_widen(w0[2 * j], w0[2 * j + 1], 1.f);
+        h[1][j] = f8_widen(w1[2 * j], w1[2 * j + 1], 1.f);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (EXACT > 0) {
+      if (!last || (kWiden && b == 0))
+#pragma unroll
+        for (int j = 0; j < kW; ++j) load_w(j, (b + kAhead) % WR, cw);
       __builtin_amdgcn_sched_barrier(0);
     }
     // Fences after every matrix instruction keep this order: one matrix
@@ -249,8 +264,24 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
       if (g == G / 2 && !last && (b == 1 || b == 2)) barrier(std::integral_constant<int, kBehind + 1>{});
       if (g == G / 2 && !last && (b == 0 || b == 3)) barrier(std::integral_constant<int, kBehind>{});
       if (g == G / 2 && last && b == 0) barrier(std::integral_constant<int, kBehindLast + kDma>{});
-      if (g == G / 2 && last && b == 1) barrier(std::integral_constant<int, kBehindLast>{});
-      if constexpr (EXACT > 0) {
+      if (g == G / 2 && last && b == 1) barrier(std::integral_constant<int, kWiden ? 0 : kBehindLast>{});
+      if constexpr (kWiden) {
+        const i32x8_t x = xv[g & 1];
+        xv[(g + 1) & 1] = g + 1 < G ? read_x(b, g + 1) : read_x(nb, 0);
+        f32x4_t p0 = zero, p1 = zero;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const half8_t xh = f8_widen(x[2 * j], x[2 * j + 1], 1.f);
+          p0 = __builtin_amdgcn_mfma_f32_16x16x32_f16(h[0][j], xh, p0, 0, 0, 0);
+          p1 = __builtin_amdgcn_mfma_f32_16x16x32_f16(h[1][j], xh, p1, 0, 0, 0);
+          if (j == 0) scale_in(0, (g + G - 1) % G);
+          if (j == 1) scale_in(1, (g + G - 1) % G);
+        }
+        r[g & 1][0] = p0;
+        r[g & 1][1] = p1;
+        f0 = sx[g & 1] * sw0;
+        f1 = sx[g & 1] * sw1;
+      } else if constexpr (EXACT > 0) {
         // (Scaled at once: the registers that hold results over a group would spill.)
         r[g & 1][0] = product(w0, xv[g & 1], g);
         r[g & 1][1] = product(w1, xv[g & 1], g);
@@ -272,7 +303,7 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
       sx[(g + 1) & 1] = g + 1 < G ? read_s(half, b, g + 1) : read_s(b == 3 ? 1 - half : half, nb, 0);
 #pragma unroll
       for (int j = 0; j < kW; ++j)
-        if (EXACT == 0 && (!last || WR == 2) && g < G / 2 && j * (G / 2) / kW == g) load_w(j, (b + WR - 1) % WR, WR == 4 ? c3 : c1);
+        if (EXACT == 0 && (!last || WR == 2) && g < G / 2 && j * (G / 2) / kW == g) load_w(j, (b + kAhead) % WR, cw);
       if (!last && g == G / 2 && b < 2) load_s(b, 1 - half, c - b + 4);
 #pragma unroll
       for (int j = 0; j < kDma; ++j)
@@ -293,17 +324,15 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
   };
   // (Weights stand between the tokens of chunks 1 and 2, as the count at the
   // barrier has it.)
-  if (WR == 4) {
-    load_all_w(0);
-    load_all_w(1);
-  }
+#pragma unroll
+  for (int c = 0; c + 1 < kAhead; ++c) load_all_w(c);
   load_s(0, 0, 0);
   load_s(1, 0, 0);
   load_all_x(0);
   __builtin_amdgcn_sched_barrier(0);
   load_all_x(1);
   __builtin_amdgcn_sched_barrier(0);
-  load_all_w(WR == 4 ? 2 : 0);
+  load_all_w(kAhead - 1);
   __builtin_amdgcn_sched_barrier(0);
   load_all_x(2);
   barrier(std::integral_constant<int, kW + 2 * kDma>{});
@@ -332,7 +361,7 @@ __device__ __forceinline__ void run_item(const F8GemmArgs& a, Smem<ROWS>& sm, Sc
   else used(1);
   if (c + 2 < nc) chunk(2, c + 2, half, behind_loop);
   else used(2);
-  if (EXACT == 0) {
+  if (EXACT == 0 || kWiden) {
     scale_in(0, G - 1);
     scale_in(1, G - 1);
   }
@@ -515,7 +544,8 @@ __global__ __launch_bounds__(256) void f8_add_parts(F8GemmArgs a) {
 }
 
 // Persistent workgroups.  Workgroup b runs on XCD b % 8.  OCC: waves per SIMD.
-// EXACT: token groups by f8_exact_product (gate_up over alignment blocks: 1 or 2).
+// EXACT: token groups whose products are summed in fp32 (gate_up: 1 or 2 over
+// alignment blocks, kEvery over tall tiles).
 template <int KIND, int ROWS, int OCC, int EXACT>
 __global__ __launch_bounds__(kThreads, OCC) void f8_tile(F8GemmArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -610,7 +640,8 @@ hipError_t launch_f8_tile(const F8GemmArgs& a, bool small, hipStream_t stream) {
     return hipGetLastError();
   }
   if (a.kind == kF8GateUp)
-    return !small             ? run(f8_tile<kF8GateUp, R, 2, 0>, 1, sizeof(Smem<R>))
+    return !small             ? a.exact ? run(f8_tile<kF8GateUp, R, 2, kEvery>, 1, sizeof(Smem<R>))
+                                         : run(f8_tile<kF8GateUp, R, 2, 0>, 1, sizeof(Smem<R>))
            : a.block_m <= 16 ? run(f8_tile<kF8GateUp, S, 4, 1>, 2, sizeof(Smem<S>))
                              : run(f8_tile<kF8GateUp, S, 4, 2>, 2, sizeof(Smem<S>));
   return small ? run(f8_tile<kF8Down, S, 4, 0>, 2, sizeof(Smem<S>))

@@ -318,6 +318,7 @@ struct F8GemmArgs {
   // alignment blocks of at most kF8SmallRows rows)
   const TileDesc* tiles;
   const DevStatus* status;
+  bool exact;          // tall tiles, gate_up: products summed in fp32
   // tiled kernel, plain: rows per tile (a multiple of 32), and parts of K whose
   // fp32 sums [parts, a_rows, n_tiles * 16] a second launch adds
   int tile_rows, parts;

@@ -1,6 +1,10 @@
 """Further GPU tests of the W8A8 layer and the dense 8-bit product against the
 fp64 oracle: every form on its own, named by its plan."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -141,14 +145,17 @@ MANY_ROWS = [
     (450, 640, 128, 70, 3, 0, "blocks of 32 rows"),
     (230, 768, 640, 24, 2, 0, "blocks of 32 rows"),
     (420, 640, 768, 16, 2, 0, "blocks of 32 rows"),
-    (800, 384, 768, 16, 2, 0, "tiles of up to 224 rows"),
+    (900, 384, 1152, 20, 1, 0, "tiles of up to 224 rows"),   # 45 rows an expert: fp32 sums
+    (1500, 640, 768, 40, 1, 1, "tiles of up to 224 rows"),
+    (1100, 896, 896, 30, 1, 2, "tiles of up to 224 rows"),
+    (800, 384, 768, 16, 2, 0, "tiles of up to 224 rows"),    # 100 rows: 8-bit sums
     (1000, 640, 640, 18, 2, 2, "tiles of up to 224 rows"),
     (1400, 896, 896, 12, 1, 1, "tiles of up to 224 rows"),
     (1900, 512, 640, 10, 2, 0, "tiles of up to 224 rows"),
 ]
 
 
-@pytest.mark.parametrize("T,H,I,E,k,hot,plan", [(*c[:5], 0, c[5]) for c in LAYER_FORMS] + MANY_ROWS[1:4] + MANY_ROWS[5:])
+@pytest.mark.parametrize("T,H,I,E,k,hot,plan", [(*c[:5], 0, c[5]) for c in LAYER_FORMS] + MANY_ROWS[1:4] + MANY_ROWS[4:7] + MANY_ROWS[8:])
 def test_moe_every_row_with_exact_sums(C, T, H, I, E, k, hot, plan):  # noqa: F811
     """Inputs whose gate_up products are exact (tests/f8_inputs.py): every token is
     within half a step of bf16 of its norm.  At the norms of an fp32 error of
@@ -173,9 +180,9 @@ def test_moe_every_row_with_exact_sums(C, T, H, I, E, k, hot, plan):  # noqa: F8
 
 @pytest.mark.parametrize("T,H,I,E,k,hot,plan", MANY_ROWS)
 def test_moe_every_row_of_many(C, T, H, I, E, k, hot, plan):  # noqa: F811
-    """Ordinary inputs.  gate_up of blocks of 32 rows is summed in fp32, so the
-    tokens are as exact as bf16 but for 1 % (see above).  Tiles of up to 224 rows sum
-    eights of products on a grid of 2^-13: h is off by about 1e-4 of itself and every
+    """Ordinary inputs.  gate_up below 64 rows an expert is summed in fp32, so the
+    tokens are as exact as bf16 but for 1 % (see above).  Above, eights of products are
+    summed on a grid of 2^-13: h is off by about 1e-4 of itself and every
     few hundredth value takes the neighbouring code, an eighth of it away at most.
     No token may be off by more than 0.04: that would take a flip of a value that
     makes up a third of the token's norm (the largest of each 128, whose code is 448
@@ -190,7 +197,7 @@ def test_moe_every_row_of_many(C, T, H, I, E, k, hot, plan):  # noqa: F811
     off = f8.rows_off(f64(got), ref)
     banner(f"  worst token {off.max():.5f}, over half a step of bf16 {(off > f8.HALF_BF16).mean():.3f}")
     assert off.max() <= 0.04
-    if plan == "blocks of 32 rows":
+    if plan == "blocks of 32 rows" or T * k < 64 * E:
         assert (off > f8.HALF_BF16).sum() <= max(1, T // 100), np.sort(off)[-T // 100 - 3:]
 
 
@@ -237,3 +244,49 @@ def test_moe_slots_past_32_bits(C):  # noqa: F811
     part = f64(got[at])
     assert np.all(np.abs(part - ref) <= bound)
     assert f8.rows_off(part, ref).max() <= 0.04
+
+
+CHILD = """
+import torch
+from quantized_moe_amd import chord as C
+from quantized_moe_amd.moe import W8A8MoE
+s = torch.load(r"{path}", weights_only=True)
+w = [t.view(torch.float8_e4m3fn).cuda() if t.dtype is torch.uint8 else t.cuda() for t in s["weights"]]
+layer, a = W8A8MoE(*w), (s["x"].cuda(), s["ids"].cuda(), s["w"].cuda(), 0, {E})
+junk = torch.empty(1 << 27, device="cuda")
+outs = []
+for i in range(4):
+    junk.fill_(i)   # pushes the inputs out of the caches
+    outs.append(layer.indexed(*a))
+torch.cuda.synchronize()
+same = all(torch.equal(o, outs[0]) for o in outs)
+torch.save({{"out": outs[0].cpu(), "plan": C.last_plan(), "same": same}}, r"{path}")
+"""
+
+
+def test_moe_fp32_sums_at_every_size(C, tmp_path):  # noqa: F811
+    """CHORD_F8_FP32_SUMS=1, in a process of its own: large tiles, in every number of
+    token groups and of chunks behind the loop, give every token as exact as bf16
+    (but for 1 %, as above), and equal bits on every call."""
+    for T, H, I, E, k, hot in ((800, 384, 768, 16, 2, 0), (1000, 640, 640, 18, 2, 2), (1500, 768, 384, 30, 2, 0),
+                               (1400, 896, 896, 12, 1, 1), (1900, 512, 640, 10, 2, 0)):
+        check_fp32_sums(T, H, I, E, k, hot, str(tmp_path / f"layer{T}.pt"))
+
+
+def check_fp32_sums(T, H, I, E, k, hot, path):
+    banner(f"f8 moe fp32 sums T={T} H={H} I={I} E={E} k={k} hot={hot}")
+    c13, s13, d13 = weights(E, 2 * I, H, 31)
+    c2, s2, d2 = weights(E, H, I, 32)
+    ids, w = routing(T, E, k, 33, hot)
+    x = activations(T, H, 34)
+    torch.save({"weights": [c13.view(torch.uint8), s13, c2.view(torch.uint8), s2], "x": x,
+                "ids": torch.from_numpy(ids), "w": torch.from_numpy(w)}, path)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", CHILD.format(path=path, E=E)], cwd=root, timeout=100,
+                       env=dict(os.environ, CHORD_F8_FP32_SUMS="1"), capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
+    got = torch.load(path, weights_only=True)
+    assert got["plan"] == "f8 moe: tiles of up to 224 rows" and got["same"]
+    ref, _, _ = f8.moe(f64(x), ids, w, d13, d2, 0)
+    off = f8.rows_off(f64(got["out"]), ref)
+    assert (off > f8.HALF_BF16).sum() <= T // 100 and off.max() <= 0.04, np.sort(off)[-10:]

@@ -132,7 +132,7 @@ def faults(blocks):
 
 def test_rows_have_landed_at_every_barrier(assembly):
     found = kernels(assembly)
-    assert len(found) == 6, sorted(found)
+    assert len(found) == 7, sorted(found)
     for name, blocks in found.items():
         wrong, looked = faults(blocks)
         assert not wrong, (name, sorted(wrong)[:5])
