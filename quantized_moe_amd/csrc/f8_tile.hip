@@ -6,8 +6,8 @@
 // and their scales go straight from memory into LDS (buffer_load ... lds), three
 // chunks of 128 along K ahead, in four buffers.  (With weights in LDS too only
 // one chunk fits in flight, and the loads alone took as long as the products.)
-// 8192 x 4096 x 7168 takes 203 us, 2.37 PFLOP/s, matrix units busy for 59 % of
-// 1.83 GHz, to which the clock falls under them; weights of 48 experts of 4096 x 7168
+// 8192 x 4096 x 7168 takes 203 to 212 us, 2.3 PFLOP/s, matrix units busy for 57 to 60 %
+// of 1.85 GHz, to which the clock falls under them; weights of 48 experts of 4096 x 7168
 // with 170 rows each 330 us, 4.5 TB/s of them.
 //
 // A matrix instruction covers the chunk; its result is scaled into the fp32
@@ -26,7 +26,9 @@
 //
 // gate_up: 256 interleaved rows are one block of 128 features of h, gate and up,
 // so the epilogue quantises that block (maximum over the eight waves through
-// LDS) and stores codes: h never exists in memory in more bits.
+// LDS) and stores codes: h never exists in memory in more bits.  Where rows are few it
+// sums its products in fp32 (f8_exact_product says why): over alignment blocks each
+// product widens its operands, over large tiles the chunk's weights are widened once.
 #include <type_traits>
 
 #include "f8_common.h"

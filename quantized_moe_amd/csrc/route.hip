@@ -30,7 +30,9 @@
 // minimum and a maximum per pair, and a round one look at the lanes' heads.
 // Bound by instruction issue: 8192 tokens of 384 experts took 16 us with 64-bit
 // scores for every candidate, 19 with all keys scanned every round, 15 with
-// places sorted beside the keys, 11 so; its bytes would take 2.6 us.
+// places sorted beside the keys, 11 so; its bytes would take 2.6 us.  (550 vector and
+// 238 scalar instructions a token; the vector units issue in 61 % of the cycles, and
+// the waves wait for an issue slot in 38 % of theirs.)
 #include <type_traits>
 
 #include "device_common.h"
