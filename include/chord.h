@@ -639,8 +639,9 @@ size_t chord_f8_moe_workspace_bytes(int T, int k, int E_l, int H, int I);
  *
  * Products of gate_up are summed in fp32 below 64 rows an expert (on average over
  * the global experts): a token is then off by its rounding to bf16, 0.0017 of its
- * norm, at most 0.0026 in the tests.  With more rows, where fp32 sums would take up to
- * a quarter more time, the 8-bit matrix instruction sums them (as chord_f8_gemm
+ * norm, at most 0.0026 in the tests but for one in a thousand, where a value of h lies
+ * on the border of two codes (0.005).  With more rows, where fp32 sums would take up
+ * to a quarter more time, the 8-bit matrix instruction sums them (as chord_f8_gemm
  * says), which can give a value of h the neighbouring code: 2 to 4 of a hundred tokens
  * are off by more than half a step of bf16 (2^-8 of the norm), the worst by 0.0185.
  * CHORD_F8_FP32_SUMS=1 in the environment (read once) takes fp32 sums at every size.
