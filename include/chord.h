@@ -1,7 +1,8 @@
 /*
  * chord.h -- C ABI of libchord.so, mixture-of-experts layers for AMD Instinct
  * MI355X (gfx950): W4A16 (below), its W8A8 form in 8-bit floating point, the
- * router in front of both, and the dense 8-bit matrix product next to them.
+ * router in front of both with its balance loss, dense matrix products in 8 and
+ * 16 bits next to them, and the norms between blocks.
  *
  * The layer: BF16 activations, unsigned 4-bit weight codes with one BF16 scale
  * per group of 32 along K, dequantised as (q - 8) * s.  Each routed row goes
@@ -526,6 +527,57 @@ chord_status chord_moe_route(const void* logits, int dtype, int64_t ld, int T, i
                              float* topk_weights, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Balance of the router's choice
+ * ------------------------------------------------------------------------- */
+
+/* Workspace bytes of chord_moe_balance; 0 for bad arguments. */
+size_t chord_moe_balance_workspace_bytes(int T, int E, int k, int n_seq);
+
+/*
+ * How evenly tokens went to experts: counts, the balance loss and its gradient
+ * by the logits.  The T rows are n_seq sequences of L = T / n_seq rows each (1: the
+ * whole batch).  A row none of whose ids is in [0, E) is padding.  In a sequence
+ * with n other rows:
+ *
+ *   c(e)   = slots of its rows with id e
+ *   f(e)   = E c(e) / (k n)
+ *   p(t,e) = softmax of the row's logits, or its sigmoids over (their sum + 1e-20)
+ *   P(e)   = sum over its rows of p(t,e) / n
+ *   loss   = sum over e of f(e) P(e)        (1 where tokens and scores are even)
+ *
+ * f is a constant to the gradient, so with g = grad_loss of the sequence
+ *
+ *   d/dlogit(t,e) = g / n * p(t,e) * (f(e) - sum over e' of f(e') p(t,e'))
+ *                   [* (1 - sigmoid(t,e))]
+ *
+ * and 0 for padding.  Experts whose logit or bias is -inf or NaN have score 0 as in
+ * chord_moe_route; +inf counts as the largest finite number.  A sequence without a
+ * token has counts, probs and loss 0.  Scores are in fp32, sums over rows in fp32
+ * and then fp64, in an order that depends on the sizes alone: equal calls give equal
+ * bits.
+ *
+ * logits:      device [T, ld] of `dtype` (fp32, bf16, fp16), ld >= E.
+ * bias:        device fp32 [E], or NULL; as chord_moe_route's, read only for what is
+ *              not available.
+ * topk_ids:    device int32 [T, k]; other ids than 0 .. E - 1 are left out.  The same
+ *              expert may stand in several slots of a row, and counts each time.
+ * counts:      device int32 [n_seq, E] out; tokens: device int32 [n_seq] out (n).
+ * probs:       device fp32 [n_seq, E] out (P); loss: device fp32 [n_seq] out.
+ * grad_loss:   device fp32 [n_seq], or NULL (1 each).
+ * grad_logits: device fp32 [T, E] out, or NULL (no gradient).
+ * workspace:   chord_moe_balance_workspace_bytes(...) bytes, 16-byte aligned,
+ *              caller-owned (NULL where that is 0); calls that may overlap need one
+ *              each.
+ * 1 <= E <= 1024; 1 <= k <= 1024; n_seq >= 1 divides T; T at most 2^25, T*k below
+ * 2^31 and n_seq at most 65535.  Enqueued on `stream`.
+ */
+chord_status chord_moe_balance(const void* logits, int dtype, int64_t ld, int T, int E,
+                               const float* bias, const int32_t* topk_ids, int k, int scoring,
+                               int n_seq, int32_t* counts, int32_t* tokens, float* probs,
+                               float* loss, const float* grad_loss, float* grad_logits,
+                               void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * 8-bit floating point (OCP e4m3fn codes) with one fp32 scale for each 128
  * columns of an activation row and each 128 x 128 block of a weight.
  * ------------------------------------------------------------------------- */
@@ -666,6 +718,108 @@ chord_status chord_f8_moe(const chord_bf16* x, int T, int H, int I, const chord_
                           const float* topk_weights, int k, int expert_begin,
                           int num_global_experts, chord_bf16* out, void* workspace,
                           size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Norms between blocks
+ * ------------------------------------------------------------------------- */
+
+typedef enum { CHORD_NORM_RMS = 0, CHORD_NORM_LAYER = 1 } chord_norm_kind;
+
+/* One norm: N(v) = (v - m) / sqrt(q + eps) * (weight + offset) + bias, where RMS has
+ * m = 0 and q = mean of v^2, LAYER m = mean of v and q = mean of (v - m)^2. */
+typedef struct {
+  int32_t kind;        /* chord_norm_kind */
+  int32_t dtype;       /* chord_dtype of weight and bias */
+  float eps;           /* finite, >= 0 */
+  float offset;        /* finite; 1 for weights that are held less one */
+  const void* weight;  /* device [H] */
+  const void* bias;    /* device [H], or NULL */
+} chord_norm_weight;
+
+/*
+ * The norms in front of and behind a block, with its gate, residual and residual
+ * scale, in one pass over the rows:
+ *
+ *   u   = x, or post(x)                       (the norm behind the block)
+ *   s   = [residual +] scale * [gate *] u     (gate: as it is, or its sigmoid)
+ *   sum = s rounded to stream_dtype
+ *   y   = pre(s)                              (the norm in front of the next block)
+ *   out = y rounded to dtype; codes, scales = chord_f8_quantize's of y
+ *
+ * Everything between is fp32: y comes from s before its rounding, the codes from
+ * y before its own (so next to a border of two codes they may differ from those of
+ * the rounded `out`).  A row whose squares overflow fp32 is scaled first, so finite
+ * rows have finite norms.
+ *
+ * x:        device [T, ldx] of dtype, ldx >= H.
+ * post:     host struct, or NULL: no norm behind the block.
+ * gate:     device of gate_dtype, or NULL; the value of row t, column h is
+ *           gate[t * gate_row + h * gate_col], gate_col being 0 or 1: one a row
+ *           (stride, 0), one a column (0, 1) or one a value (stride, 1).
+ * residual: device [T, ldr] of stream_dtype, or NULL.
+ * sum:      device [T, lds] of stream_dtype out, or NULL; may be the residual, or x
+ *           where the types are equal, with the same row stride.
+ * pre:      host struct, or NULL: then neither out nor codes.
+ * out:      device [T, ldo] of dtype out, or NULL; may be x with its row stride.
+ * codes:    device [T, ceil(H/128)*128] out, 16-byte aligned, with scales: device
+ *           fp32 [T, ceil(H/128)] out; or NULL both.
+ * One of sum, out and codes is there.  dtype, gate_dtype and the norms' types are
+ * any chord_dtype, stream_dtype is dtype or fp32.  1 <= H <= 32768, T below 2^31;
+ * T == 0 is a no-op.  Any alignment of elements; 16-byte aligned rows with H % 8 ==
+ * 0 are read and written wide.  Columns from H on stay as they are.  Enqueued on
+ * `stream`; needs no workspace.
+ */
+chord_status chord_norm(const void* x, int64_t ldx, int dtype, int64_t T, int H,
+                        const chord_norm_weight* post, const void* gate, int gate_dtype,
+                        int64_t gate_row, int64_t gate_col, int gate_sigmoid, float scale,
+                        const void* residual, int64_t ldr, void* sum, int64_t lds,
+                        int stream_dtype, const chord_norm_weight* pre, void* out, int64_t ldo,
+                        chord_f8* codes, float* scales, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Dense product in 16 bits
+ * ------------------------------------------------------------------------- */
+
+typedef enum {
+  CHORD_ACT_NONE = 0,
+  CHORD_ACT_RELU = 1,
+  CHORD_ACT_SILU = 2,      /* z / (1 + e^-z) */
+  CHORD_ACT_GELU = 3,      /* z (1 + erf(z / sqrt 2)) / 2 */
+  CHORD_ACT_GELU_TANH = 4  /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+} chord_act;
+
+/* Workspace bytes of chord_linear (0: it needs none); 0 for bad arguments.  x and w
+ * are looked at for their alignment only. */
+size_t chord_linear_workspace_bytes(const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                    int64_t M, int N, int K, int gated);
+
+/*
+ * Dense product with its epilogue:
+ *
+ *   z   = x W^T + bias                        (sums in fp32)
+ *   h   = act(z), or gated: act(z[:, :N]) * z[:, N:]
+ *   out = [residual +] scale * h              (rounded once)
+ *
+ * x:        device [M, ldx] of dtype (bf16 or fp16), ldx >= K.
+ * w:        device [N, ldw] of dtype, gated [2N, ldw] with the activated (gate) rows
+ *           first, ldw >= K.
+ * bias:     device [N] ([2N]) of bias_dtype (dtype or fp32), or NULL.
+ * residual: device [M, ldr] of out_dtype, or NULL; may be `out` with its row stride.
+ * out:      device [M, ldo] of out_dtype (dtype or fp32); columns from N on stay as
+ *           they are.
+ * workspace: chord_linear_workspace_bytes(...) bytes, 256-byte aligned, caller-owned
+ *           (NULL where that is 0); calls that may overlap need one each.
+ * 16-byte aligned rows with K % 8 == 0 are read in place; others are first copied to
+ * such rows in the workspace.  Products of few rows split K over workgroups whose
+ * fp32 sums are added in order; which do depends on sizes and alignment alone, so
+ * equal calls give equal bits.  M, N (2N) below 2^31 / 4 and K up to 2^20; M == 0 is
+ * a no-op.  Enqueued on `stream`.
+ */
+chord_status chord_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, int dtype,
+                          int64_t M, int N, int K, const void* bias, int bias_dtype, int act,
+                          int gated, float scale, const void* residual, int64_t ldr, void* out,
+                          int64_t ldo, int out_dtype, void* workspace, size_t ws_bytes,
+                          void* stream);
 
 #ifdef __cplusplus
 }

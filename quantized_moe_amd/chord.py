@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -22,6 +22,8 @@ STATUS_NAMES = {0: "CHORD_OK", 1: "CHORD_ERR_INVALID_ARGUMENT", 2: "CHORD_ERR_UN
 MODE_INDEXED, MODE_CONTIGUOUS, MODE_MASKED = 0, 1, 2
 ROLE_GATE_UP, ROLE_DOWN, ROLE_PLAIN = 0, 1, 2
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+NORM_RMS, NORM_LAYER = 0, 1
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2, 3, 4
 FLAG_VALIDATE = 1
 
 EXPORTED = [
@@ -35,6 +37,8 @@ EXPORTED = [
     "chord_moe_dispatch_contiguous", "chord_moe_dispatch_masked", "chord_moe_combine",
     "chord_w4a16_moe_plan", "chord_moe_route", "chord_f8_packed_bytes", "chord_f8_pack",
     "chord_f8_quantize", "chord_f8_gemm_workspace_bytes", "chord_f8_gemm", "chord_f8_moe_workspace_bytes", "chord_f8_moe",
+    "chord_moe_balance_workspace_bytes", "chord_moe_balance", "chord_norm", "chord_linear_workspace_bytes",
+    "chord_linear",
 ]
 
 
@@ -58,6 +62,11 @@ class F8Weight(ctypes.Structure):
                 ("bytes", ctypes.c_size_t)]
 
 
+class NormWeight(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("offset", ctypes.c_float), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
 class Schedule(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int32), ("tokens", ctypes.c_int32),
                 ("gate_up_nt", ctypes.c_int32), ("gate_up_wk", ctypes.c_int32),
@@ -72,7 +81,7 @@ def _load():
     lib = ctypes.CDLL(_LIB_PATH)
     P, I, I64, SZ, U32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_uint32
     WP, FP = ctypes.POINTER(Weight), ctypes.POINTER(F8Weight)
-    F = ctypes.c_float
+    F, NP = ctypes.c_float, ctypes.POINTER(NormWeight)
     sig = {
         "chord_status_string": (ctypes.c_char_p, [I]),
         "chord_last_error": (ctypes.c_char_p, []),
@@ -111,6 +120,11 @@ def _load():
         "chord_f8_gemm": (I, [P, P, I64, FP, P, I64, P, SZ, P]),
         "chord_f8_moe_workspace_bytes": (SZ, [I, I, I, I, I]),
         "chord_f8_moe": (I, [P, I, I, I, FP, FP, P, P, I, I, I, P, P, SZ, P]),
+        "chord_moe_balance_workspace_bytes": (SZ, [I, I, I, I]),
+        "chord_moe_balance": (I, [P, I, I64, I, I, P, P, I, I, I, P, P, P, P, P, P, P, SZ, P]),
+        "chord_norm": (I, [P, I64, I, I64, I, NP, P, I, I64, I64, I, F, P, I64, P, I64, I, NP, P, I64, P, P, P]),
+        "chord_linear_workspace_bytes": (SZ, [P, I64, P, I64, I64, I, I, I]),
+        "chord_linear": (I, [P, I64, P, I64, I, I64, I, I, P, I, I, I, F, P, I64, P, I64, I, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -393,7 +407,7 @@ def chord_moe_combine(rows, flat_to_row, topk_weights, out=None, stream=None):
 
 
 # ---------------------------------------------------------------------------
-# router and 8-bit floating point
+# router, 8-bit floating point, and the operators around a layer
 #
 # These wrappers check types, shapes, layouts and devices (the C ABI sees only
 # addresses), run on the device of their first tensor whichever is current, and
@@ -634,6 +648,272 @@ def chord_f8_moe(x, w13: F8PackedWeight, w2: F8PackedWeight, topk_ids, topk_weig
     st = lib.chord_f8_moe(x.data_ptr(), T, H, I, w13.ref, w2.ref, topk_ids.data_ptr(),
                           topk_weights.data_ptr(), k, expert_begin, num_global_experts,
                           out.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(dev))
+    if st:
+        _check(st)
+    return out
+
+
+class Balance(NamedTuple):
+    counts: torch.Tensor            # int32 [n_seq, E]
+    tokens: torch.Tensor            # int32 [n_seq]
+    probs: torch.Tensor             # fp32 [n_seq, E]
+    loss: torch.Tensor              # fp32 [n_seq]
+    grad: Optional[torch.Tensor]    # fp32 [T, E]
+
+
+def chord_moe_balance_workspace_bytes(T: int, E: int, k: int, n_seq: int = 1) -> int:
+    return lib.chord_moe_balance_workspace_bytes(T, E, k, n_seq)
+
+
+def chord_moe_balance(logits, topk_ids, scoring: int = SCORE_SOFTMAX, bias=None, n_seq: int = 1,
+                      grad_loss=None, want_grad: bool = False, out: Optional[Balance] = None,
+                      workspace=None, stream=None) -> Balance:
+    """Counts per expert, the balance loss of each of n_seq sequences of equal
+    length and, if asked for, the gradient of sum(grad_loss * loss) by the logits
+    [T, E] (fp32, bf16 or fp16; rows may be strided).  topk_ids int32 [T, k]; rows
+    without an expert are padding.  `out`: a Balance of tensors to write to (its
+    grad, or None, stands for want_grad)."""
+    if _away(logits, stream):
+        return _elsewhere(chord_moe_balance, logits, stream, topk_ids=topk_ids, scoring=scoring, bias=bias,
+                          n_seq=n_seq, grad_loss=grad_loss, want_grad=want_grad, out=out,
+                          workspace=workspace)
+    dtype = _DTYPES.get(logits.dtype)
+    if dtype is None:
+        _refuse(f"logits have type {logits.dtype}")
+    ld = _row_stride(logits, "logits")
+    T, E = logits.shape
+    dev = logits.get_device()
+    if not isinstance(topk_ids, torch.Tensor) or topk_ids.dim() != 2:
+        _refuse("topk_ids must be a matrix")
+    k = topk_ids.shape[1]
+    _tensor(topk_ids, "topk_ids", _I32, (T, k), dev)
+    if not isinstance(n_seq, int) or n_seq < 1 or T % n_seq != 0:
+        _refuse(f"n_seq={n_seq} must divide T={T}")
+    if bias is not None:
+        _tensor(bias, "bias", _F32, (E,), dev)
+    if grad_loss is not None:
+        _tensor(grad_loss, "grad_loss", _F32, (n_seq,), dev)
+    if out is None:
+        out = Balance(torch.empty((n_seq, E), dtype=_I32, device=dev),
+                      torch.empty((n_seq,), dtype=_I32, device=dev),
+                      torch.empty((n_seq, E), dtype=_F32, device=dev),
+                      torch.empty((n_seq,), dtype=_F32, device=dev),
+                      torch.empty((T, E), dtype=_F32, device=dev) if want_grad else None)
+    else:
+        _tensor(out.counts, "counts", _I32, (n_seq, E), dev)
+        _tensor(out.tokens, "tokens", _I32, (n_seq,), dev)
+        _tensor(out.probs, "probs", _F32, (n_seq, E), dev)
+        _tensor(out.loss, "loss", _F32, (n_seq,), dev)
+        if out.grad is not None:
+            _tensor(out.grad, "grad", _F32, (T, E), dev)
+    ws, nbytes = _scratch(workspace, lib.chord_moe_balance_workspace_bytes, dev, T, E, k, n_seq)
+    st = lib.chord_moe_balance(logits.data_ptr(), dtype, ld, T, E,
+                               None if bias is None else bias.data_ptr(), topk_ids.data_ptr(), k, scoring,
+                               n_seq, out.counts.data_ptr(), out.tokens.data_ptr(), out.probs.data_ptr(),
+                               out.loss.data_ptr(), None if grad_loss is None else grad_loss.data_ptr(),
+                               None if out.grad is None else out.grad.data_ptr(),
+                               None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev))
+    if st:
+        _check(st)
+    return out
+
+
+class Norm:
+    """The weights of one norm: weight [H], and a bias [H] or none, fp32, bf16 or
+    fp16.  `offset` is added to the weights (1 for weights held less one)."""
+
+    def __init__(self, weight, bias=None, eps: float = 1e-6, kind: int = NORM_RMS, offset: float = 0.0):
+        if not isinstance(weight, torch.Tensor) or not weight.is_cuda or weight.dim() != 1:
+            _refuse("weight must be a vector on the GPU")
+        dtype = _DTYPES.get(weight.dtype)
+        if dtype is None:
+            _refuse(f"weight has type {weight.dtype}")
+        self.device, self.H = weight.get_device(), weight.shape[0]
+        _tensor(weight, "weight", weight.dtype, (self.H,), self.device)
+        if bias is not None:
+            _tensor(bias, "bias", weight.dtype, (self.H,), self.device)
+        self.weight, self.bias = weight, bias
+        self.handle = NormWeight(kind, dtype, eps, offset, weight.data_ptr(),
+                                 None if bias is None else bias.data_ptr())
+        self.ref = ctypes.byref(self.handle)
+
+
+class NormResult(NamedTuple):
+    sum: Optional[torch.Tensor]      # [T, H] of the stream's type
+    out: Optional[torch.Tensor]      # [T, H] of x's type
+    codes: Optional[torch.Tensor]    # float8_e4m3fn [T, ceil(H/128)*128]
+    scales: Optional[torch.Tensor]   # fp32 [T, ceil(H/128)]
+
+
+def _norm(n, name: str, H: int, device: int):
+    if not isinstance(n, Norm):
+        _refuse(f"{name} must be a Norm")
+    if n.H != H or n.device != device:
+        _refuse(f"{name} has {n.H} weights on GPU {n.device}, expected {H} on {device}")
+    return n.ref
+
+
+def chord_norm(x, pre: Optional[Norm] = None, post: Optional[Norm] = None, gate=None,
+               gate_sigmoid: bool = False, residual=None, scale: float = 1.0, sum_dtype=None,
+               want_sum: Optional[bool] = None, want_out: Optional[bool] = None, want_codes: bool = False,
+               sum_out=None, out=None, codes_out=None, stream=None) -> NormResult:
+    """s = [residual +] scale * [gate *] (x, or post's norm of it); out and codes are
+    pre's norm of s, from before s is rounded.  x [T, H] bf16, fp16 or fp32; residual
+    and sum are of x's type or fp32 (sum_dtype: that of sum without a residual); gate
+    [T, 1], [H] or [T, H] of any of the three types, behind a sigmoid if asked.  Rows
+    may be strided.  What is written: the sum unless want_sum is False (by default
+    where it is more than x alone), out where there is a `pre` (unless want_out is
+    False), the 8-bit codes of out with their scales if want_codes.  sum_out (may be
+    the residual), out and codes_out = (codes, scales) are tensors to write to."""
+    if _away(x, stream):
+        return _elsewhere(chord_norm, x, stream, pre=pre, post=post, gate=gate, gate_sigmoid=gate_sigmoid,
+                          residual=residual, scale=scale, sum_dtype=sum_dtype, want_sum=want_sum,
+                          want_out=want_out, want_codes=want_codes, sum_out=sum_out, out=out,
+                          codes_out=codes_out)
+    xt = x.dtype
+    dtype = _DTYPES.get(xt)
+    if dtype is None:
+        _refuse(f"x has type {xt}")
+    ldx = _row_stride(x, "x")
+    T, H = x.shape
+    dev = x.get_device()
+    shape = x.shape
+    st_type = xt
+    if residual is not None:
+        st_type = residual.dtype if isinstance(residual, torch.Tensor) else None
+    elif sum_out is not None:
+        st_type = sum_out.dtype if isinstance(sum_out, torch.Tensor) else None
+    elif sum_dtype is not None:
+        st_type = sum_dtype
+    if st_type is not xt and st_type is not _F32 or (sum_dtype is not None and sum_dtype is not st_type):
+        _refuse(f"residual and sum must both be {xt} or torch.float32 tensors")
+    r_ptr, ldr = None, 0
+    if residual is not None:
+        _tensor(residual, "residual", st_type, shape, dev, False)
+        ldr = _row_stride(residual, "residual")
+        r_ptr = residual.data_ptr()
+    g_ptr, g_type, g_row, g_col = None, 0, 0, 0
+    if gate is not None:
+        if not isinstance(gate, torch.Tensor) or gate.get_device() != dev or gate.dtype not in _DTYPES:
+            _refuse("gate must be a floating tensor on x's GPU")
+        g_type = _DTYPES[gate.dtype]
+        if gate.dim() == 1 and gate.shape[0] == H and (H == 1 or gate.stride(0) == 1):
+            g_col = 1
+        elif gate.dim() == 2 and gate.shape[0] == T and gate.shape[1] == H and (H > 1 or T == 1):
+            g_row, g_col = _row_stride(gate, "gate"), 1
+        elif gate.dim() == 2 and gate.shape[0] == T and gate.shape[1] == 1:
+            g_row = gate.stride(0) if T > 1 else 0
+        else:
+            _refuse(f"gate must be [{T}, 1], [{H}] or [{T}, {H}] with contiguous columns, not "
+                    f"{list(gate.shape)} with strides {list(gate.stride())}")
+        g_ptr = gate.data_ptr()
+    if sum_out is None:
+        if want_sum is None:
+            want_sum = pre is None or r_ptr is not None or post is not None or g_ptr is not None or scale != 1.0 \
+                or sum_dtype is not None
+        if want_sum:
+            sum_out = torch.empty((T, H), dtype=st_type, device=dev)
+            lds = H
+    else:
+        _tensor(sum_out, "sum_out", st_type, shape, dev, False)
+        lds = _row_stride(sum_out, "sum_out")
+    if out is None:
+        if pre is not None and want_out is not False:
+            out = torch.empty((T, H), dtype=xt, device=dev)
+            ldo = H
+    else:
+        _tensor(out, "out", xt, shape, dev, False)
+        ldo = _row_stride(out, "out")
+    q = s = None
+    if want_codes or codes_out is not None:
+        groups = -(-H // F8_BLOCK)
+        if codes_out is None:
+            q = torch.empty((T, groups * F8_BLOCK), dtype=_F8, device=dev)
+            s = torch.empty((T, groups), dtype=_F32, device=dev)
+        else:
+            q, s = codes_out
+            _tensor(q, "codes", _F8, (T, groups * F8_BLOCK), dev)
+            _tensor(s, "scales", _F32, (T, groups), dev)
+    st = lib.chord_norm(x.data_ptr(), ldx, dtype, T, H,
+                        None if post is None else _norm(post, "post", H, dev), g_ptr, g_type, g_row, g_col,
+                        gate_sigmoid, scale, r_ptr, ldr,
+                        None if sum_out is None else sum_out.data_ptr(), 0 if sum_out is None else lds,
+                        _DTYPES[st_type], None if pre is None else _norm(pre, "pre", H, dev),
+                        None if out is None else out.data_ptr(), 0 if out is None else ldo,
+                        None if q is None else q.data_ptr(), None if s is None else s.data_ptr(),
+                        _raw_stream(dev))
+    if st:
+        _check(st)
+    return NormResult(sum_out, out, q, s)
+
+
+def _scratch(workspace, query, device: int, *sizes):
+    """A call's workspace (given, or what `query` says from torch's allocator, None
+    where that is nothing) and its bytes."""
+    if workspace is not None:
+        _tensor(workspace, "workspace", torch.uint8, (workspace.numel(),), device)
+        return workspace, workspace.numel()
+    nbytes = query(*sizes)
+    return (torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None), nbytes
+
+
+def chord_linear_workspace_bytes(x, w, gated: bool = False) -> int:
+    """Of chord_linear's product of these tensors."""
+    N = w.shape[0] // 2 if gated else w.shape[0]
+    return lib.chord_linear_workspace_bytes(x.data_ptr(), _row_stride(x, "x"), w.data_ptr(),
+                                            _row_stride(w, "w"), x.shape[0], N, x.shape[1], gated)
+
+
+def chord_linear(x, w, bias=None, act: int = ACT_NONE, gated: bool = False, scale: float = 1.0,
+                 residual=None, out=None, out_dtype=None, workspace=None, stream=None):
+    """[residual +] scale * h, h = act(x W^T + bias), or with `gated` the activation
+    of the first half of W's rows times the second: [M, N] of x's type or fp32
+    (out_dtype).  x [M, K] and w [N, K] ([2N, K]) bf16 or fp16, bias [N] ([2N]) of
+    their type or fp32, residual [M, N] of the output's type (it may be `out`).
+    Rows may be strided."""
+    if _away(x, stream):
+        return _elsewhere(chord_linear, x, stream, w=w, bias=bias, act=act, gated=gated, scale=scale,
+                          residual=residual, out=out, out_dtype=out_dtype, workspace=workspace)
+    xt = x.dtype
+    if xt is not _BF16 and xt is not torch.float16:
+        _refuse(f"x has type {xt}, expected bfloat16 or float16")
+    ldx = _row_stride(x, "x")
+    M, K = x.shape
+    dev = x.get_device()
+    if not isinstance(w, torch.Tensor) or w.dim() != 2 or w.shape[1] != K or (gated and w.shape[0] % 2):
+        _refuse(f"w must be a matrix of rows of {K}, gated an even number of them")
+    rows = w.shape[0]
+    _tensor(w, "w", xt, (rows, K), dev, False)
+    ldw = _row_stride(w, "w")
+    N = rows // 2 if gated else rows
+    b_ptr, b_type = None, 0
+    if bias is not None:
+        b_type = _DTYPES.get(bias.dtype) if isinstance(bias, torch.Tensor) else None
+        _tensor(bias, "bias", _F32 if b_type == 0 else xt, (rows,), dev)
+        b_ptr = bias.data_ptr()
+    if out is None:
+        if out_dtype is None:
+            out_dtype = xt
+        elif out_dtype is not xt and out_dtype is not _F32:
+            _refuse(f"out_dtype={out_dtype}, expected {xt} or torch.float32")
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        ldo = N
+    else:
+        if out_dtype is None:
+            out_dtype = _F32 if isinstance(out, torch.Tensor) and out.dtype is _F32 else xt
+        _tensor(out, "out", out_dtype, (M, N), dev, False)
+        ldo = _row_stride(out, "out")
+    r_ptr, ldr = None, 0
+    if residual is not None:
+        _tensor(residual, "residual", out_dtype, (M, N), dev, False)
+        ldr = _row_stride(residual, "residual")
+        r_ptr = residual.data_ptr()
+    x_ptr, w_ptr = x.data_ptr(), w.data_ptr()
+    ws, nbytes = _scratch(workspace, lib.chord_linear_workspace_bytes, dev, x_ptr, ldx, w_ptr, ldw, M, N, K,
+                          gated)
+    st = lib.chord_linear(x_ptr, ldx, w_ptr, ldw, _DTYPES[xt], M, N, K, b_ptr, b_type, act, gated, scale,
+                          r_ptr, ldr, out.data_ptr(), ldo, _DTYPES[out_dtype],
+                          None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev))
     if st:
         _check(st)
     return out

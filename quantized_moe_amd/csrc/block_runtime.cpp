@@ -1,0 +1,259 @@
+// Host side of the operators around a layer: norms between blocks, the dense 16-bit
+// product and the router's balance.  Argument checks (before any HIP call),
+// workspace layout and launches.
+#include <algorithm>
+#include <cmath>
+#include <cstdio>
+
+#include "host.h"
+
+using namespace chord;
+
+namespace {
+
+bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+bool known(int dtype) {
+  return dtype == CHORD_DTYPE_F32 || dtype == CHORD_DTYPE_BF16 || dtype == CHORD_DTYPE_F16;
+}
+
+// ---- norms -------------------------------------------------------------------
+constexpr int kNormMaxH = 32768;  // 1024 threads x 4 x 8 values
+
+chord_status norm_part(const chord_norm_weight* w, const char* name, NormPart* p) {
+  *p = NormPart{};
+  if (!w) return CHORD_OK;
+  if (!w->weight) return fail(CHORD_ERR_INVALID_ARGUMENT, "%s has no weight", name);
+  if (w->kind != CHORD_NORM_RMS && w->kind != CHORD_NORM_LAYER)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "%s kind %d", name, w->kind);
+  if (!known(w->dtype)) return fail(CHORD_ERR_INVALID_ARGUMENT, "%s dtype %d", name, w->dtype);
+  // (Squares below the smallest normal number vanish beside it.)
+  if (!std::isnormal(w->eps) || w->eps < 0.f)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "%s eps %g must be a positive normal number", name, w->eps);
+  if (!std::isfinite(w->offset)) return fail(CHORD_ERR_INVALID_ARGUMENT, "%s offset is not finite", name);
+  *p = NormPart{w->weight, w->bias, w->dtype, w->kind, w->eps, w->offset};
+  return CHORD_OK;
+}
+
+// ---- balance -----------------------------------------------------------------
+constexpr int kBalanceMaxTokens = 1 << 25;
+constexpr int kBalanceMaxK = 1024;
+constexpr int kBalanceMaxSeq = 65535;  // (grid dimension)
+
+struct BalancePlan {
+  int parts, chunks;
+  int64_t rows;
+  size_t counts, total;
+};
+
+BalancePlan balance_plan(int T, int E, int k, int n_seq) {
+  BalancePlan p{};
+  const int64_t L = T / n_seq;
+  const int64_t slots = L * k;
+  p.parts = slots <= 16384 ? 0 : (int)std::min<int64_t>(16, (slots + 16383) / 16384);
+  // Rows of a workgroup: 32, more where that would be over 1024 workgroups.
+  p.rows = std::max<int64_t>(32, (T + 1023) / 1024);
+  p.chunks = (int)std::max<int64_t>(1, (L + p.rows - 1) / p.rows);
+  size_t off = 0;
+  if (p.parts > 0) off += ((size_t)n_seq * p.parts * (E + 1) * 4 + 15) & ~(size_t)15;
+  p.counts = off;
+  if (p.chunks > 1) off += (size_t)n_seq * p.chunks * E * 4;
+  p.total = off;
+  return p;
+}
+
+chord_status check_balance_sizes(int T, int E, int k, int n_seq) {
+  if (T < 0) return fail(CHORD_ERR_INVALID_ARGUMENT, "T=%d", T);
+  if (E < 1 || E > kMaxExperts) return fail(CHORD_ERR_INVALID_ARGUMENT, "E=%d (1..%d)", E, kMaxExperts);
+  if (k < 1 || k > kBalanceMaxK) return fail(CHORD_ERR_INVALID_ARGUMENT, "k=%d (1..%d)", k, kBalanceMaxK);
+  if (n_seq < 1 || T % n_seq != 0)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "n_seq=%d must divide T=%d", n_seq, T);
+  if (n_seq > kBalanceMaxSeq) return fail(CHORD_ERR_UNSUPPORTED, "n_seq=%d above %d", n_seq, kBalanceMaxSeq);
+  if (T > kBalanceMaxTokens) return fail(CHORD_ERR_UNSUPPORTED, "T=%d above %d", T, kBalanceMaxTokens);
+  if ((int64_t)T * k >= (int64_t)1 << 31) return fail(CHORD_ERR_UNSUPPORTED, "T*k=%lld", (long long)T * k);
+  return CHORD_OK;
+}
+
+// ---- product -----------------------------------------------------------------
+constexpr int64_t kLinearMaxRows = (int64_t)1 << 29;  // of x, and of W
+constexpr int kLinearMaxK = 1 << 20;
+
+chord_status check_linear_sizes(int64_t ldx, int64_t ldw, int64_t M, int N, int K, int gated) {
+  if (M < 0 || N < 1 || K < 1)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "M=%lld N=%d K=%d", (long long)M, N, K);
+  if (ldx < K || ldw < K)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "row strides %lld (x) and %lld (w) below K=%d", (long long)ldx,
+                (long long)ldw, K);
+  if (M >= kLinearMaxRows || (int64_t)N * (gated ? 2 : 1) >= kLinearMaxRows || K > kLinearMaxK)
+    return fail(CHORD_ERR_UNSUPPORTED, "M=%lld N=%d K=%d", (long long)M, N, K);
+  return CHORD_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+chord_status chord_norm(const void* x, int64_t ldx, int dtype, int64_t T, int H,
+                        const chord_norm_weight* post, const void* gate, int gate_dtype,
+                        int64_t gate_row, int64_t gate_col, int gate_sigmoid, float scale,
+                        const void* residual, int64_t ldr, void* sum, int64_t lds,
+                        int stream_dtype, const chord_norm_weight* pre, void* out, int64_t ldo,
+                        chord_f8* codes, float* scales, void* stream) {
+  clear_last_error();
+  NormArgs a{};
+  CHORD_CHECK(norm_part(post, "post", &a.post));
+  CHORD_CHECK(norm_part(pre, "pre", &a.pre));
+  if (!known(dtype)) return fail(CHORD_ERR_INVALID_ARGUMENT, "dtype %d", dtype);
+  if (stream_dtype != dtype && stream_dtype != CHORD_DTYPE_F32)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "stream_dtype %d (dtype %d or fp32)", stream_dtype, dtype);
+  if (T < 0 || H < 1) return fail(CHORD_ERR_INVALID_ARGUMENT, "T=%lld H=%d", (long long)T, H);
+  if (H > kNormMaxH) return fail(CHORD_ERR_UNSUPPORTED, "H=%d above %d", H, kNormMaxH);
+  if (T >= (int64_t)1 << 31) return fail(CHORD_ERR_UNSUPPORTED, "T=%lld", (long long)T);
+  if (!std::isfinite(scale)) return fail(CHORD_ERR_INVALID_ARGUMENT, "scale is not finite");
+  if (T == 0) return CHORD_OK;
+  if (!sum && !out && !codes) return fail(CHORD_ERR_INVALID_ARGUMENT, "nothing to write");
+  if ((out || codes) && !pre)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "out and codes are the norm's, and pre is NULL");
+  if (pre && !out && !codes) return fail(CHORD_ERR_INVALID_ARGUMENT, "pre without out or codes");
+  if (!codes != !scales) return fail(CHORD_ERR_INVALID_ARGUMENT, "codes and scales come together");
+  if (ldx < H || (residual && ldr < H) || (sum && lds < H) || (out && ldo < H))
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "a row stride is below H=%d", H);
+  if (gate) {
+    if (!known(gate_dtype)) return fail(CHORD_ERR_INVALID_ARGUMENT, "gate_dtype %d", gate_dtype);
+    if ((gate_col != 0 && gate_col != 1) || gate_row < 0)
+      return fail(CHORD_ERR_INVALID_ARGUMENT, "gate strides %lld, %lld", (long long)gate_row, (long long)gate_col);
+  }
+  if (!x) return fail(CHORD_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (codes && !aligned(codes, 16)) return fail(CHORD_ERR_INVALID_ARGUMENT, "codes must be 16-byte aligned");
+  CHORD_CHECK(check_device(nullptr));
+  a.x = x;
+  a.ldx = ldx;
+  a.dtype = dtype;
+  a.T = T;
+  a.H = H;
+  a.gate = gate;
+  a.gate_dtype = gate_dtype;
+  a.gate_row = gate_row;
+  a.gate_col = gate_col;
+  a.gate_sigmoid = gate_sigmoid != 0;
+  a.scale = scale;
+  a.residual = residual;
+  a.ldr = ldr;
+  a.sum = sum;
+  a.lds = lds;
+  a.stream_dtype = stream_dtype;
+  a.out = out;
+  a.ldo = ldo;
+  a.codes = codes;
+  a.code_scales = scales;
+  HIP_TRY(launch_norm(a, static_cast<hipStream_t>(stream)), "norm launch");
+  return CHORD_OK;
+}
+
+size_t chord_moe_balance_workspace_bytes(int T, int E, int k, int n_seq) {
+  clear_last_error();
+  if (check_balance_sizes(T, E, k, n_seq) != CHORD_OK) return 0;
+  return balance_plan(T, E, k, n_seq).total;
+}
+
+chord_status chord_moe_balance(const void* logits, int dtype, int64_t ld, int T, int E,
+                               const float* bias, const int32_t* topk_ids, int k, int scoring,
+                               int n_seq, int32_t* counts, int32_t* tokens, float* probs,
+                               float* loss, const float* grad_loss, float* grad_logits,
+                               void* workspace, size_t ws_bytes, void* stream) {
+  clear_last_error();
+  if (!known(dtype)) return fail(CHORD_ERR_INVALID_ARGUMENT, "dtype %d", dtype);
+  if (scoring != CHORD_SCORE_SOFTMAX && scoring != CHORD_SCORE_SIGMOID)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "scoring %d", scoring);
+  CHORD_CHECK(check_balance_sizes(T, E, k, n_seq));
+  if (ld < E) return fail(CHORD_ERR_INVALID_ARGUMENT, "row stride %lld below E=%d", (long long)ld, E);
+  if (!counts || !tokens || !probs || !loss || (T > 0 && (!logits || !topk_ids)))
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "null pointer argument");
+  const BalancePlan plan = balance_plan(T, E, k, n_seq);
+  if (plan.total > 0 && (!workspace || ws_bytes < plan.total))
+    return fail(CHORD_ERR_WORKSPACE, "workspace %zu bytes, %zu needed", ws_bytes, plan.total);
+  if (plan.total > 0 && !aligned(workspace, 16))
+    return fail(CHORD_ERR_WORKSPACE, "the workspace must be 16-byte aligned");
+  CHORD_CHECK(check_device(nullptr));
+  BalanceArgs a{};
+  a.logits = logits;
+  a.dtype = dtype;
+  a.ld = ld;
+  a.L = T / n_seq;
+  a.E = E;
+  a.k = k;
+  a.n_seq = n_seq;
+  a.bias = bias;
+  a.sigmoid = scoring == CHORD_SCORE_SIGMOID;
+  a.ids = topk_ids;
+  a.counts = counts;
+  a.tokens = tokens;
+  a.probs = probs;
+  a.loss = loss;
+  a.grad_loss = grad_loss;
+  a.grad = grad_logits;
+  a.parts = plan.parts;
+  a.chunks = plan.chunks;
+  a.rows = plan.rows;
+  a.part_counts = reinterpret_cast<int32_t*>(workspace);
+  a.part_probs = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.counts);
+  HIP_TRY(launch_balance(a, static_cast<hipStream_t>(stream)), "balance launch");
+  return CHORD_OK;
+}
+
+size_t chord_linear_workspace_bytes(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t M,
+                                    int N, int K, int gated) {
+  clear_last_error();
+  (void)x;
+  (void)w;
+  if (check_linear_sizes(ldx, ldw, M, N, K, gated) != CHORD_OK) return 0;
+  return 0;
+}
+
+chord_status chord_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, int dtype,
+                          int64_t M, int N, int K, const void* bias, int bias_dtype, int act,
+                          int gated, float scale, const void* residual, int64_t ldr, void* out,
+                          int64_t ldo, int out_dtype, void* workspace, size_t ws_bytes,
+                          void* stream) {
+  clear_last_error();
+  (void)workspace;
+  (void)ws_bytes;
+  if (!known(dtype)) return fail(CHORD_ERR_INVALID_ARGUMENT, "dtype %d", dtype);
+  if (dtype == CHORD_DTYPE_F32) return fail(CHORD_ERR_UNSUPPORTED, "x and w must be bf16 or fp16");
+  if (out_dtype != dtype && out_dtype != CHORD_DTYPE_F32)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "out_dtype %d (dtype %d or fp32)", out_dtype, dtype);
+  if (bias && bias_dtype != dtype && bias_dtype != CHORD_DTYPE_F32)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "bias_dtype %d (dtype %d or fp32)", bias_dtype, dtype);
+  if (act < CHORD_ACT_NONE || act > CHORD_ACT_GELU_TANH) return fail(CHORD_ERR_INVALID_ARGUMENT, "act %d", act);
+  if (!std::isfinite(scale)) return fail(CHORD_ERR_INVALID_ARGUMENT, "scale is not finite");
+  CHORD_CHECK(check_linear_sizes(ldx, ldw, M, N, K, gated));
+  if (ldo < N || (residual && ldr < N))
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "a row stride is below N=%d", N);
+  if (M == 0) return CHORD_OK;
+  if (!x || !w || !out) return fail(CHORD_ERR_INVALID_ARGUMENT, "null pointer argument");
+  int cus = 0;
+  CHORD_CHECK(check_device(&cus));
+  LinearArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.ldx = ldx;
+  a.w = static_cast<const uint16_t*>(w);
+  a.ldw = ldw;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.f16 = dtype == CHORD_DTYPE_F16;
+  a.gated = gated != 0;
+  a.act = act;
+  a.bias = bias;
+  a.bias_f32 = bias_dtype == CHORD_DTYPE_F32;
+  a.scale = scale;
+  a.residual = residual;
+  a.ldr = ldr;
+  a.out = out;
+  a.ldo = ldo;
+  a.out_f32 = out_dtype == CHORD_DTYPE_F32;
+  a.num_cus = cus;
+  HIP_TRY(launch_linear(a, static_cast<hipStream_t>(stream)), "product launch");
+  return CHORD_OK;
+}
+
+}  // extern "C"

@@ -357,6 +357,76 @@ struct F8CombineArgs {
   uint16_t* out;            // bf16 [T, H]
 };
 
+// One norm of a launch (weight null: none).
+struct NormPart {
+  const void* weight;  // [H]
+  const void* bias;    // [H] or null
+  int dtype, kind;
+  float eps, offset;
+};
+struct NormArgs {
+  const void* x;       // [T, ldx] of dtype
+  int64_t ldx;
+  int dtype;
+  int64_t T;
+  int H;
+  NormPart post, pre;
+  const void* gate;    // or null
+  int gate_dtype;
+  int64_t gate_row, gate_col;
+  int gate_sigmoid;
+  float scale;
+  const void* residual;  // [T, ldr] of stream_dtype, or null
+  int64_t ldr;
+  void* sum;             // [T, lds] of stream_dtype, or null
+  int64_t lds;
+  int stream_dtype;
+  void* out;             // [T, ldo] of dtype, or null
+  int64_t ldo;
+  uint8_t* codes;        // [T, chunks * 128], or null
+  float* code_scales;    // [T, chunks]
+  int threads;           // of a row (set by the launcher)
+};
+
+struct BalanceArgs {
+  const void* logits;   // [n_seq * L, ld]
+  int dtype;
+  int64_t ld, L;
+  int E, k, n_seq;
+  const float* bias;    // [E] or null
+  int sigmoid;
+  const int32_t* ids;   // [n_seq * L, k]
+  int32_t *counts, *tokens;  // [n_seq, E], [n_seq]
+  float *probs, *loss;
+  const float* grad_loss;  // [n_seq] or null
+  float* grad;             // [n_seq * L, E] or null
+  int parts;               // workgroups that count a sequence (0: each counts it whole)
+  int chunks;              // workgroups that go over its rows,
+  int64_t rows;            // this many each
+  int32_t* part_counts;    // [n_seq, parts, E + 1]
+  float* part_probs;       // [n_seq, chunks, E] where chunks > 1
+};
+
+struct LinearArgs {
+  const uint16_t* x;   // [M, ldx]
+  int64_t ldx;
+  const uint16_t* w;   // [N or 2N, ldw]
+  int64_t ldw;
+  int64_t M;
+  int N, K;
+  bool f16, gated;
+  int act;
+  const void* bias;    // or null
+  bool bias_f32;
+  float scale;
+  const void* residual;  // [M, ldr] of the output's type, or null
+  int64_t ldr;
+  void* out;             // [M, ldo]
+  int64_t ldo;
+  bool out_f32;
+  int num_cus;
+};
+
 // Launchers (defined in the .hip files).  All enqueue on `stream` and return
 // hipSuccess or the launch error.
 hipError_t launch_pack(const int32_t* q, const uint16_t* s, int E, int N, int K, int gate_up,
@@ -394,6 +464,9 @@ hipError_t launch_f8_short_down(const F8GemmArgs& a, hipStream_t stream);
 bool f8_small_fits(int T, int k, int H, int I);
 hipError_t launch_f8_small(const F8SmallArgs& a, hipStream_t stream);
 hipError_t launch_f8_combine(const F8CombineArgs& a, hipStream_t stream);
+hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
+hipError_t launch_balance(const BalanceArgs& a, hipStream_t stream);
+hipError_t launch_linear(const LinearArgs& a, hipStream_t stream);
 
 constexpr int kAlignSingle = 8192;      // align in one workgroup up to this many entries
 constexpr int kAlignMinChunk = 1024;    // entries per align workgroup (at least)

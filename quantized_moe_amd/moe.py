@@ -127,3 +127,30 @@ class F8Linear:
             raise C.ChordError(1, f"x must be [M, {self.K}], not {list(x.shape)}")
         q, s = C.chord_f8_quantize(x, stream=stream)
         return C.chord_f8_gemm(q, s, self.w, out=out, stream=stream)
+
+
+class Linear:
+    """y = [residual +] scale * act(x W^T + b) with a 16-bit weight [N, K] (bf16 or
+    fp16; gated: [2N, K], the activated rows first).  A router's logits are
+    Linear(w)(x, out_dtype=torch.float32)."""
+
+    def __init__(self, w, bias=None, act: int = C.ACT_NONE, gated: bool = False):
+        self.w, self.bias, self.act, self.gated = w, bias, act, gated
+        self.N, self.K = w.shape[0] // 2 if gated else w.shape[0], w.shape[1]
+
+    def __call__(self, x, residual=None, scale: float = 1.0, out=None, out_dtype=None, stream=None):
+        return C.chord_linear(x, self.w, self.bias, self.act, self.gated, scale, residual, out, out_dtype,
+                              stream=stream)
+
+
+class SharedExpert:
+    """The expert that every token goes through, beside the routed ones: W2 (silu(W1
+    x) * W3 x) with 16-bit weights w13 [2I, H] (gate rows first) and w2 [H, I], added
+    to the routed experts' output if that is given (`out` may be that output)."""
+
+    def __init__(self, w13, w2, act: int = C.ACT_SILU):
+        self.gate_up, self.down = Linear(w13, act=act, gated=True), Linear(w2)
+
+    def __call__(self, x, routed=None, scale: float = 1.0, out=None, stream=None):
+        h = self.gate_up(x, stream=stream)
+        return self.down(h, residual=routed, scale=scale, out=out, stream=stream)
