@@ -24,7 +24,8 @@ LIB = os.path.join(PKG, "libchord.so")
 SOURCES = ["runtime.cpp", "align.hip", "pack.hip", "moe_kernels.hip", "gemm_stream.hip",
            "gemm_tile.hip", "dispatch.hip", "f8_runtime.cpp", "route.hip", "f8_quantize.hip",
            "f8_gemm.hip", "f8_tile.hip",
-           "f8_short.hip", "f8_small.hip", "block_runtime.cpp", "norm.hip", "balance.hip", "linear.hip"]
+           "f8_short.hip", "f8_small.hip", "block_runtime.cpp", "norm.hip", "balance.hip", "linear.hip",
+           "linear_tile.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

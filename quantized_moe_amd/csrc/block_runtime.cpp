@@ -88,6 +88,65 @@ chord_status check_linear_sizes(int64_t ldx, int64_t ldw, int64_t M, int N, int 
   return CHORD_OK;
 }
 
+// Whether rows can be read in place: 16-byte pieces, and offsets inside a tile of up
+// to 256 rows that stay below 2^31.
+bool rows_in_place(const void* p, int64_t ld, int K) {
+  return aligned(p, 16) && ld % 8 == 0 && K % 8 == 0 && ld <= (int64_t)1 << 21;
+}
+
+// How a product runs: the weight-streaming form, or tiles with K in parts.
+struct LinearPlan {
+  bool stream;
+  int shape, parts;
+  bool copy_x, copy_w;
+  int K;  // of the rows that are read
+  size_t x, w, partials, total;  // workspace: copies, sums
+};
+
+const struct {
+  int rows, outs;
+} kLinearShapes[] = {{256, 256}, {128, 256}, {128, 128}, {64, 128}};
+
+LinearPlan linear_plan(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t M, int N, int K, int gated) {
+  constexpr int64_t kCus = 256;  // (of the model, so that the workspace depends on sizes alone)
+  LinearPlan p{};
+  p.copy_x = !rows_in_place(x, ldx, K);
+  p.copy_w = !rows_in_place(w, ldw, K);
+  p.K = (K + 7) / 8 * 8;
+  const int64_t rows = (int64_t)N * (gated ? 2 : 1);
+  const int chunks = (p.K + 63) / 64;
+  p.parts = 1;
+  p.stream = M <= 64;
+  if (!p.stream) {
+    double best = 1e30;
+    for (int s = 0; s < 4; ++s) {
+      const int64_t items = (M + kLinearShapes[s].rows - 1) / kLinearShapes[s].rows *
+                            ((rows + kLinearShapes[s].outs - 1) / kLinearShapes[s].outs);
+      for (int parts : {1, 2, 4, 8, 16}) {
+        if (parts > chunks || (parts > 1 && items * parts > 2 * kCus)) break;
+        const double rounds = (double)((items * parts + kCus - 1) / kCus);
+        const double area = (double)kLinearShapes[s].rows * kLinearShapes[s].outs / 65536.0;
+        double c = rounds * (4.0 + (chunks + parts - 1) / parts * (0.2 + 1.2 * area));
+        if (parts > 1) c += 4.5 + parts * (double)M * rows * 8 / 4e6;
+        if (c < best) {
+          best = c;
+          p.shape = s;
+          p.parts = parts;
+        }
+      }
+    }
+  }
+  auto take = [&](bool on, int64_t bytes) {
+    const size_t o = p.total;
+    if (on) p.total += ((size_t)bytes + 255) & ~(size_t)255;
+    return o;
+  };
+  p.x = take(p.copy_x, M * p.K * 2);
+  p.w = take(p.copy_w, rows * p.K * 2);
+  p.partials = take(p.parts > 1, (int64_t)p.parts * M * ((N + 15) / 16 * 16) * (gated ? 2 : 1) * 4);
+  return p;
+}
+
 }  // namespace
 
 extern "C" {
@@ -203,10 +262,8 @@ chord_status chord_moe_balance(const void* logits, int dtype, int64_t ld, int T,
 size_t chord_linear_workspace_bytes(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t M,
                                     int N, int K, int gated) {
   clear_last_error();
-  (void)x;
-  (void)w;
-  if (check_linear_sizes(ldx, ldw, M, N, K, gated) != CHORD_OK) return 0;
-  return 0;
+  if (check_linear_sizes(ldx, ldw, M, N, K, gated) != CHORD_OK || M == 0) return 0;
+  return linear_plan(x, ldx, w, ldw, M, N, K, gated).total;
 }
 
 chord_status chord_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, int dtype,
@@ -215,8 +272,6 @@ chord_status chord_linear(const void* x, int64_t ldx, const void* w, int64_t ldw
                           int64_t ldo, int out_dtype, void* workspace, size_t ws_bytes,
                           void* stream) {
   clear_last_error();
-  (void)workspace;
-  (void)ws_bytes;
   if (!known(dtype)) return fail(CHORD_ERR_INVALID_ARGUMENT, "dtype %d", dtype);
   if (dtype == CHORD_DTYPE_F32) return fail(CHORD_ERR_UNSUPPORTED, "x and w must be bf16 or fp16");
   if (out_dtype != dtype && out_dtype != CHORD_DTYPE_F32)
@@ -230,8 +285,15 @@ chord_status chord_linear(const void* x, int64_t ldx, const void* w, int64_t ldw
     return fail(CHORD_ERR_INVALID_ARGUMENT, "a row stride is below N=%d", N);
   if (M == 0) return CHORD_OK;
   if (!x || !w || !out) return fail(CHORD_ERR_INVALID_ARGUMENT, "null pointer argument");
+  const LinearPlan plan = linear_plan(x, ldx, w, ldw, M, N, K, gated);
+  if (plan.total > 0 && (!workspace || ws_bytes < plan.total))
+    return fail(CHORD_ERR_WORKSPACE, "workspace %zu bytes, %zu needed", ws_bytes, plan.total);
+  if (plan.total > 0 && !aligned(workspace, 256))
+    return fail(CHORD_ERR_WORKSPACE, "the workspace must be 256-byte aligned");
   int cus = 0;
   CHORD_CHECK(check_device(&cus));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   LinearArgs a{};
   a.x = static_cast<const uint16_t*>(x);
   a.ldx = ldx;
@@ -252,7 +314,35 @@ chord_status chord_linear(const void* x, int64_t ldx, const void* w, int64_t ldw
   a.ldo = ldo;
   a.out_f32 = out_dtype == CHORD_DTYPE_F32;
   a.num_cus = cus;
-  HIP_TRY(launch_linear(a, static_cast<hipStream_t>(stream)), "product launch");
+  a.parts = plan.parts;
+  a.partials = reinterpret_cast<float*>(ws + plan.partials);
+  const int out_size = a.out_f32 ? 4 : 2;
+  if (aligned(bias, a.bias_f32 ? 16 : 8)) a.wide |= kLinWideBias;
+  if (aligned(residual, 4 * out_size) && ldr % 4 == 0) a.wide |= kLinWideResidual;
+  if (aligned(out, 4 * out_size) && ldo % 4 == 0) a.wide |= kLinWideOut;
+  if (plan.copy_x) {
+    uint16_t* to = reinterpret_cast<uint16_t*>(ws + plan.x);
+    HIP_TRY(launch_copy_rows(a.x, ldx, M, K, plan.K, to, st), "copy launch");
+    a.x = to;
+    a.ldx = plan.K;
+  }
+  if (plan.copy_w) {
+    uint16_t* to = reinterpret_cast<uint16_t*>(ws + plan.w);
+    HIP_TRY(launch_copy_rows(a.w, ldw, (int64_t)N * (a.gated ? 2 : 1), K, plan.K, to, st), "copy launch");
+    a.w = to;
+    a.ldw = plan.K;
+  }
+  a.K = plan.K;
+  HIP_TRY(plan.stream ? launch_linear_stream(a, st) : launch_linear_tile(a, plan.shape, st), "product launch");
+  if (plan.parts > 1) HIP_TRY(launch_linear_join(a, st), "product sum launch");
+  if (plan.stream) {
+    set_last_plan("linear: streaming");
+  } else {
+    char text[64];
+    snprintf(text, sizeof(text), "linear: tiles of %d x %d, K in %d", kLinearShapes[plan.shape].rows,
+             kLinearShapes[plan.shape].outs, plan.parts);
+    set_last_plan(text);
+  }
   return CHORD_OK;
 }
 

@@ -424,8 +424,14 @@ struct LinearArgs {
   void* out;             // [M, ldo]
   int64_t ldo;
   bool out_f32;
+  int wide;            // kLinWide*: what may be taken four values at a time
+  int parts;           // of K, whose fp32 sums [parts, M, N (gated: and N) rounded up
+  float* partials;     // to 16] a second launch adds
   int num_cus;
 };
+constexpr int kLinWideBias = 1, kLinWideResidual = 2, kLinWideOut = 4;
+// Tokens x rows of W of a workgroup of the tiled form.
+enum LinearShape : int { kLin256x256 = 0, kLin128x256 = 1, kLin128x128 = 2, kLin64x128 = 3 };
 
 // Launchers (defined in the .hip files).  All enqueue on `stream` and return
 // hipSuccess or the launch error.
@@ -466,7 +472,11 @@ hipError_t launch_f8_small(const F8SmallArgs& a, hipStream_t stream);
 hipError_t launch_f8_combine(const F8CombineArgs& a, hipStream_t stream);
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t stream);
-hipError_t launch_linear(const LinearArgs& a, hipStream_t stream);
+hipError_t launch_linear_stream(const LinearArgs& a, hipStream_t stream);
+hipError_t launch_linear_tile(const LinearArgs& a, int shape, hipStream_t stream);
+hipError_t launch_linear_join(const LinearArgs& a, hipStream_t stream);
+hipError_t launch_copy_rows(const uint16_t* src, int64_t ld, int64_t rows, int K, int to, uint16_t* dst,
+                            hipStream_t stream);
 
 constexpr int kAlignSingle = 8192;      // align in one workgroup up to this many entries
 constexpr int kAlignMinChunk = 1024;    // entries per align workgroup (at least)

@@ -1,5 +1,5 @@
-// Device pieces of the 16-bit dense product: the matrix instruction of either type
-// and the epilogue.
+// Device pieces of the 16-bit dense product: loads, the matrix instruction of either
+// type, and the epilogue.
 #pragma once
 
 #include "device_common.h"
@@ -8,20 +8,23 @@ namespace chord {
 
 typedef __attribute__((ext_vector_type(8))) _Float16 f16x8_t;
 
-// Eight neighbouring values along K.
-union Operand {
-  uint16_t h[8];
-  u32x4_t u;
-};
+constexpr int kLinRsrcWord3 = 0x00020000;
+constexpr uint32_t kLinNothing = 0xC0000000u;  // byte offset past any buffer: reads as zeros
 
 template <bool F16>
-__device__ __forceinline__ f32x4_t mfma(const Operand& a, const Operand& b, f32x4_t c) {
+__device__ __forceinline__ f32x4_t mfma16(u32x4_t a, u32x4_t b, f32x4_t c) {
   if constexpr (F16)
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a.u), __builtin_bit_cast(f16x8_t, b.u),
-                                                  c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c,
+                                                  0, 0, 0);
   else
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a.u),
-                                                   __builtin_bit_cast(bf16x8_t, b.u), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                   __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
+// Buffer over `rows` rows of K values, `ld` apart.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const uint16_t* p, int64_t rows, int64_t ld, int K) {
+  const int64_t bytes = ((rows - 1) * ld + K) * 2;
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)bytes, kLinRsrcWord3);
 }
 
 // Activation in fp32.  The results are rounded to 16 bits, or stand beside sums of
@@ -38,28 +41,75 @@ __device__ __forceinline__ float activate(int act, float z) {
   }
 }
 
-__device__ __forceinline__ float value16(uint16_t h, bool f16) {
-  return f16 ? (float)__builtin_bit_cast(_Float16, h) : bf16_to_f32(h);
+__device__ __forceinline__ float value16(uint32_t h, bool f16) {
+  return f16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)h) : bf16_to_f32(h);
 }
 __device__ __forceinline__ uint16_t round16(float v, bool f16) {
   return f16 ? __builtin_bit_cast(uint16_t, (_Float16)v) : to_bf16(v);
 }
-__device__ __forceinline__ float bias_at(const LinearArgs& a, int64_t n) {
-  if (a.bias == nullptr) return 0.f;
-  return a.bias_f32 ? static_cast<const float*>(a.bias)[n] : value16(static_cast<const uint16_t*>(a.bias)[n], a.f16);
+__device__ __forceinline__ uint32_t round16x2(float a, float b, bool f16) {
+  return (uint32_t)round16(a, f16) | (uint32_t)round16(b, f16) << 16;
 }
 
-// One output from its sums over K (up: the up row's, where gated).
-__device__ __forceinline__ void store_out(const LinearArgs& a, int64_t m, int n, float z, float up) {
-  float h = activate(a.act, z + bias_at(a, n));
-  if (a.gated) h *= up + bias_at(a, (int64_t)a.N + n);
-  h *= a.scale;
-  if (a.out_f32) {
-    if (a.residual != nullptr) h += static_cast<const float*>(a.residual)[m * a.ldr + n];
-    static_cast<float*>(a.out)[m * a.ldo + n] = h;
+// n (of four) neighbouring values of 16 bits or fp32 at p[i], by words where `wide`.
+__device__ __forceinline__ f32x4_t load4(const void* p, int64_t i, bool f32, bool f16, bool wide, int n) {
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+  if (f32) {
+    const float* q = static_cast<const float*>(p) + i;
+    if (wide) return *reinterpret_cast<const f32x4_t*>(q);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < n) v[j] = q[j];
   } else {
-    if (a.residual != nullptr) h += value16(static_cast<const uint16_t*>(a.residual)[m * a.ldr + n], a.f16);
-    static_cast<uint16_t*>(a.out)[m * a.ldo + n] = round16(h, a.f16);
+    const uint16_t* q = static_cast<const uint16_t*>(p) + i;
+    if (wide) {
+      const uint2 u = *reinterpret_cast<const uint2*>(q);
+      return f32x4_t{value16(u.x & 0xFFFF, f16), value16(u.x >> 16, f16), value16(u.y & 0xFFFF, f16),
+                     value16(u.y >> 16, f16)};
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < n) v[j] = value16(q[j], f16);
+  }
+  return v;
+}
+
+// The outputs n .. n + 3 of row m (those below N) from their sums over K; `up` holds
+// the up rows' where gated.
+__device__ __forceinline__ void store_out4(const LinearArgs& a, int64_t m, int n, f32x4_t z, f32x4_t up) {
+  const int left = a.N - n;
+  if (left <= 0) return;
+  const bool whole = left >= 4;
+  if (a.bias != nullptr) {
+    const bool wide = whole && (a.wide & kLinWideBias);
+    z += load4(a.bias, n, a.bias_f32, a.f16, wide, left);
+    if (a.gated) up += load4(a.bias, (int64_t)a.N + n, a.bias_f32, a.f16, wide && a.N % 4 == 0, left);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) z[i] = activate(a.act, z[i]);
+  if (a.gated) z *= up;
+  z *= a.scale;
+  if (a.residual != nullptr)
+    z += load4(a.residual, m * a.ldr + n, a.out_f32, a.f16, whole && (a.wide & kLinWideResidual), left);
+  const bool wide = whole && (a.wide & kLinWideOut);
+  if (a.out_f32) {
+    float* o = static_cast<float*>(a.out) + m * a.ldo + n;
+    if (wide) {
+      *reinterpret_cast<f32x4_t*>(o) = z;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < left) o[i] = z[i];
+    }
+  } else {
+    uint16_t* o = static_cast<uint16_t*>(a.out) + m * a.ldo + n;
+    if (wide) {
+      *reinterpret_cast<uint2*>(o) = make_uint2(round16x2(z[0], z[1], a.f16), round16x2(z[2], z[3], a.f16));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < left) o[i] = round16(z[i], a.f16);
+    }
   }
 }
 
