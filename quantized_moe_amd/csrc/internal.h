@@ -414,16 +414,16 @@ struct LinearArgs {
   int64_t ldw;
   int64_t M;
   int N, K;
-  bool f16, gated;
+  int f16, gated;      // truth values
   int act;
   const void* bias;    // or null
-  bool bias_f32;
+  int bias_f32;
   float scale;
   const void* residual;  // [M, ldr] of the output's type, or null
   int64_t ldr;
   void* out;             // [M, ldo]
   int64_t ldo;
-  bool out_f32;
+  int out_f32;
   int wide;            // kLinWide*: what may be taken four values at a time
   int parts;           // of K, whose fp32 sums [parts, M, N (gated: and N) rounded up
   float* partials;     // to 16] a second launch adds

@@ -21,9 +21,9 @@ __device__ __forceinline__ f32x4_t mfma16(u32x4_t a, u32x4_t b, f32x4_t c) {
                                                    __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
 }
 
-// Buffer over `rows` rows of K values, `ld` apart.
+// Buffer over `rows` rows (0: empty) of K values, `ld` apart.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const uint16_t* p, int64_t rows, int64_t ld, int K) {
-  const int64_t bytes = ((rows - 1) * ld + K) * 2;
+  const int64_t bytes = rows > 0 ? ((rows - 1) * ld + K) * 2 : 0;
   return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)bytes, kLinRsrcWord3);
 }
 
@@ -74,43 +74,64 @@ __device__ __forceinline__ f32x4_t load4(const void* p, int64_t i, bool f32, boo
   return v;
 }
 
-// The outputs n .. n + 3 of row m (those below N) from their sums over K; `up` holds
-// the up rows' where gated.
-__device__ __forceinline__ void store_out4(const LinearArgs& a, int64_t m, int n, f32x4_t z, f32x4_t up) {
-  const int left = a.N - n;
-  if (left <= 0) return;
-  const bool whole = left >= 4;
-  if (a.bias != nullptr) {
-    const bool wide = whole && (a.wide & kLinWideBias);
-    z += load4(a.bias, n, a.bias_f32, a.f16, wide, left);
-    if (a.gated) up += load4(a.bias, (int64_t)a.N + n, a.bias_f32, a.f16, wide && a.N % 4 == 0, left);
+// The outputs n .. n + 3 (those below N) of any row: what does not depend on the row.
+struct OutQuad {
+  int n, left;
+  bool whole, wide_res, wide_out;
+  f32x4_t bias, bias_up;
+};
+__device__ __forceinline__ OutQuad out_quad(const LinearArgs& a, int n) {
+  OutQuad o;
+  o.n = n;
+  o.left = a.N - n;
+  o.whole = o.left >= 4;
+  o.wide_res = o.whole && (a.wide & kLinWideResidual);
+  o.wide_out = o.whole && (a.wide & kLinWideOut);
+  o.bias = o.bias_up = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  if (a.bias != nullptr && o.left > 0) {
+    const bool wide = o.whole && (a.wide & kLinWideBias);
+    o.bias = load4(a.bias, n, a.bias_f32, a.f16, wide, o.left);
+    if (a.gated) o.bias_up = load4(a.bias, (int64_t)a.N + n, a.bias_f32, a.f16, wide && a.N % 4 == 0, o.left);
   }
+  return o;
+}
+__device__ __forceinline__ f32x4_t out_residual(const LinearArgs& a, const OutQuad& o, int64_t m) {
+  if (a.residual == nullptr) return f32x4_t{0.f, 0.f, 0.f, 0.f};
+  return load4(a.residual, m * a.ldr + o.n, a.out_f32, a.f16, o.wide_res, o.left);
+}
+// From the sums over K; `up` holds the up rows' where gated.
+__device__ __forceinline__ void out_store(const LinearArgs& a, const OutQuad& o, int64_t m, f32x4_t z, f32x4_t up,
+                                          f32x4_t residual) {
+  z += o.bias;
+  if (a.act != CHORD_ACT_NONE) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) z[i] = activate(a.act, z[i]);
-  if (a.gated) z *= up;
-  z *= a.scale;
-  if (a.residual != nullptr)
-    z += load4(a.residual, m * a.ldr + n, a.out_f32, a.f16, whole && (a.wide & kLinWideResidual), left);
-  const bool wide = whole && (a.wide & kLinWideOut);
+    for (int i = 0; i < 4; ++i) z[i] = activate(a.act, z[i]);
+  }
+  if (a.gated) z *= up + o.bias_up;
+  z = z * a.scale + residual;
   if (a.out_f32) {
-    float* o = static_cast<float*>(a.out) + m * a.ldo + n;
-    if (wide) {
-      *reinterpret_cast<f32x4_t*>(o) = z;
+    float* p = static_cast<float*>(a.out) + m * a.ldo + o.n;
+    if (o.wide_out) {
+      *reinterpret_cast<f32x4_t*>(p) = z;
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (i < left) o[i] = z[i];
+        if (i < o.left) p[i] = z[i];
     }
   } else {
-    uint16_t* o = static_cast<uint16_t*>(a.out) + m * a.ldo + n;
-    if (wide) {
-      *reinterpret_cast<uint2*>(o) = make_uint2(round16x2(z[0], z[1], a.f16), round16x2(z[2], z[3], a.f16));
+    uint16_t* p = static_cast<uint16_t*>(a.out) + m * a.ldo + o.n;
+    if (o.wide_out) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(round16x2(z[0], z[1], a.f16), round16x2(z[2], z[3], a.f16));
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (i < left) o[i] = round16(z[i], a.f16);
+        if (i < o.left) p[i] = round16(z[i], a.f16);
     }
   }
+}
+__device__ __forceinline__ void store_out4(const LinearArgs& a, int64_t m, int n, f32x4_t z, f32x4_t up) {
+  const OutQuad o = out_quad(a, n);
+  if (o.left > 0) out_store(a, o, m, z, up, out_residual(a, o, m));
 }
 
 }  // namespace chord
