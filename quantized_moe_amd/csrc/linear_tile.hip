@@ -34,21 +34,22 @@ constexpr int kRowBytes = 2 * kChunk;
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-template <int WM, int WN, int MG, int NT, int STAGES>
+// XS, WS: chunks of x and of W that LDS holds.
+template <int WM, int WN, int MG, int NT, int XS, int WS>
 struct Shape {
   static constexpr int kTM = WM * MG * 16, kTN = WN * NT * 16;
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
-  static constexpr int kStageBytes = (kTM + kTN) * kRowBytes;
+  static constexpr int kXBytes = kTM * kRowBytes, kWBytes = kTN * kRowBytes;  // of a chunk
+  static constexpr int kRing = XS * kXBytes + WS * kWBytes;
   static constexpr int kPitch = kTN + 4;  // floats of a token in the epilogue
   static constexpr int kOutRows = kTM > 128 ? 128 : kTM;
-  static constexpr size_t kLds = STAGES * kStageBytes > kOutRows * kPitch * 4 ? STAGES * kStageBytes
-                                                                             : kOutRows * kPitch * 4;
+  static constexpr size_t kLds = kRing > kOutRows * kPitch * 4 ? kRing : kOutRows * kPitch * 4;
 };
 
-template <bool F16, int WM, int WN, int MG, int NT, int STAGES>
+template <bool F16, int WM, int WN, int MG, int NT, int XS, int WS>
 __device__ __forceinline__ void run_item(const LinearArgs& a, uint8_t* lds, int tile, int slice, int part) {
-  using S = Shape<WM, WN, MG, NT, STAGES>;
-  constexpr int TM = S::kTM, TN = S::kTN, kWaves = S::kWaves, kThreads = S::kThreads, SB = S::kStageBytes;
+  using S = Shape<WM, WN, MG, NT, XS, WS>;
+  constexpr int TM = S::kTM, TN = S::kTN, kWaves = S::kWaves, kThreads = S::kThreads, XB = S::kXBytes, WB = S::kWBytes;
   constexpr int kSteps = 2 * MG;
   constexpr int kAhead = MG >= 8 ? 6 : MG >= 4 ? 3 : 2, kRing = MG >= 8 ? 8 : 4;
   static_assert(kSteps % kRing == 0 && kAhead < kRing && kAhead <= MG && NT % 2 == 0);
@@ -67,45 +68,53 @@ __device__ __forceinline__ void run_item(const LinearArgs& a, uint8_t* lds, int 
   const int outs = a.gated ? TN / 2 : TN;  // outputs of a slice
   const int first = slice * outs;          // ... and its first one
 
-  // Instruction i of a wave brings rows 8 (wave + kWaves i) .. + 7 of the stage, one row
-  // per 8 lanes: first x, then the lower half of the slice's rows of W (gated: the gate
-  // rows), then the upper half (the up rows).
-  constexpr int kX = TM / 8 / kWaves, kW = TN / 2 / 8 / kWaves, kDma = kX + 2 * kW;
-  static_assert(kX >= 1 && kW >= 1);
+  // Instruction i of a wave for x brings rows 8 (wave + kWaves i) .. + 7, one row per 8
+  // lanes.  W: the same of the lower half of the slice's rows (gated: the gate rows)
+  // for the first kW / 2, then of the upper half (the up rows).
+  constexpr int kX = TM / 8 / kWaves, kW = TN / 8 / kWaves;
+  static_assert(kX >= 1 && kW >= 2);
   const int w_lo = min(TN / 2, a.N - first), w_hi = a.gated ? w_lo : max(0, min(TN / 2, a.N - first - TN / 2));
   const __amdgpu_buffer_rsrc_t xres = row_buffer(a.x + m0 * a.ldx, rows, a.ldx, a.K);
   const __amdgpu_buffer_rsrc_t wres = row_buffer(a.w + (int64_t)first * a.ldw, w_lo, a.ldw, a.K);
   const __amdgpu_buffer_rsrc_t ures =
       row_buffer(a.w + ((int64_t)(a.gated ? a.N : TN / 2) + first) * a.ldw, w_hi, a.ldw, a.K);
-  uint32_t off[kDma];
+  uint32_t xo[kX], wo[kW];
   bool in_tail;
   {
     const int r = lane >> 3, p = (lane & 7) ^ (r & 6);
     in_tail = p * 8 < tail;
 #pragma unroll
-    for (int i = 0; i < kDma; ++i) {
-      const int k = i < kX ? i : i < kX + kW ? i - kX : i - kX - kW;
-      const int row = 8 * (wave + kWaves * k) + r, end = i < kX ? rows : i < kX + kW ? w_lo : w_hi;
-      const int64_t ld = i < kX ? a.ldx : a.ldw;
-      off[i] = row < end ? (uint32_t)(row * ld * 2 + (c_lo * 8 + p) * 16) : kLinNothing;
+    for (int i = 0; i < kX; ++i) {
+      const int row = 8 * (wave + kWaves * i) + r;
+      xo[i] = row < rows ? (uint32_t)(row * a.ldx * 2 + (c_lo * 8 + p) * 16) : kLinNothing;
+    }
+#pragma unroll
+    for (int i = 0; i < kW; ++i) {
+      const int row = 8 * (wave + kWaves * (i % (kW / 2))) + r;
+      wo[i] = row < (i < kW / 2 ? w_lo : w_hi) ? (uint32_t)(row * a.ldw * 2 + (c_lo * 8 + p) * 16) : kLinNothing;
     }
   }
-  auto load = [&](int i, int at, int c) {
-    const uint32_t o = c == last && !in_tail ? kLinNothing : off[i];
-    // (x rows, then W rows: kWaves 1 KB pieces an instruction)
-    auto to = (__attribute__((address_space(3))) void*)(lds + at + (wave + kWaves * i) * 1024);
-    if (i < kX) __builtin_amdgcn_raw_ptr_buffer_load_lds(xres, to, 16, o, c * kRowBytes, 0, 0);
-    else if (i < kX + kW) __builtin_amdgcn_raw_ptr_buffer_load_lds(wres, to, 16, o, c * kRowBytes, 0, 0);
+  typedef __attribute__((address_space(3))) void* Lds;
+  uint8_t* const w_lds = lds + XS * XB;
+  auto load_x = [&](int i, int at, int c) {
+    const uint32_t o = c == last && !in_tail ? kLinNothing : xo[i];
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(xres, (Lds)(lds + at + (wave + kWaves * i) * 1024), 16, o, c * kRowBytes,
+                                             0, 0);
+  };
+  auto load_w = [&](int i, int at, int c) {
+    const uint32_t o = c == last && !in_tail ? kLinNothing : wo[i];
+    const Lds to = (Lds)(w_lds + at + (wave + kWaves * i) * 1024);
+    if (i < kW / 2) __builtin_amdgcn_raw_ptr_buffer_load_lds(wres, to, 16, o, c * kRowBytes, 0, 0);
     else __builtin_amdgcn_raw_ptr_buffer_load_lds(ures, to, 16, o, c * kRowBytes, 0, 0);
   };
   const int piece[2] = {(q ^ (col & 6)) * 16, ((4 + q) ^ (col & 6)) * 16};
-  const int x_at = (wm * MG * 16 + col) * kRowBytes, w_at = (TM + wn * (NT / 2) * 16 + col) * kRowBytes;
+  const int x_at = (wm * MG * 16 + col) * kRowBytes, w_at = (wn * (NT / 2) * 16 + col) * kRowBytes;
   auto read_x = [&](int at, int j, int g) {
     return *reinterpret_cast<const u32x4_t*>(lds + at + (x_at + piece[j]) + g * 16 * kRowBytes);
   };
   auto read_w = [&](int at, int j, int n) {
     const int r = n < NT / 2 ? n * 16 : TN / 2 + (n - NT / 2) * 16;
-    return *reinterpret_cast<const u32x4_t*>(lds + at + (w_at + piece[j]) + r * kRowBytes);
+    return *reinterpret_cast<const u32x4_t*>(w_lds + at + (w_at + piece[j]) + r * kRowBytes);
   };
 
   f32x4_t acc[MG][NT];
@@ -123,48 +132,69 @@ __device__ __forceinline__ void run_item(const LinearArgs& a, uint8_t* lds, int 
     __builtin_amdgcn_sched_barrier(0);
   };
   u32x4_t x[kRing], w[2][NT];  // w[j]: of the chunk's half j
+  // Chunk c loads x of chunk c + XS - 1 before its barrier and W of chunk c + WS behind
+  // it (each where its buffer is free), so the loads are spread over the chunk; here
+  // those of the chunks before the first.
+  constexpr int kMost = XS - 1 > WS ? XS - 1 : WS;
 #pragma unroll
-  for (int c = 0; c < STAGES; ++c) {
-    if (c < nc)
+  for (int c = -kMost; c < 0; ++c) {
+    if (c + XS - 1 >= 0 && c + XS - 1 < nc) {
 #pragma unroll
-      for (int i = 0; i < kDma; ++i) load(i, c * SB, c);
+      for (int i = 0; i < kX; ++i) load_x(i, (c + XS - 1) * XB, c + XS - 1);
+    }
+    if (c + WS >= 0 && c + WS < nc) {
+#pragma unroll
+      for (int i = 0; i < kW; ++i) load_w(i, (c + WS) * WB, c + WS);
+    }
     __builtin_amdgcn_sched_barrier(0);
   }
-  if (nc >= STAGES) barrier(std::integral_constant<int, (STAGES - 1) * kDma>{});
+  if (nc >= kMost) barrier(std::integral_constant<int, (XS - 2) * kX + (WS - 1) * kW>{});
   else barrier(std::integral_constant<int, 0>{});
 #pragma unroll
   for (int n = 0; n < NT; ++n) w[0][n] = read_w(0, 0, n);
 #pragma unroll
   for (int r = 0; r < kAhead; ++r) x[r] = read_x(0, 0, r);
-  int at = 0;
-  for (int c = 0; c < nc; ++c) {
-    const int next = at + SB == STAGES * SB ? 0 : at + SB;
-    const bool more = c + STAGES < nc;
+  int xat = 0, wat = 0, xfar = (XS - 1) * XB;  // buffers of chunk c, and x's of chunk c + XS - 1
+  // Younger than x and W of chunk c + 1, at the barrier of chunk c (steady: none is left
+  // out near the end).
+  constexpr int kFromX = (XS - 2) * (kX + kW), kFromW = (WS - 1) * kX + (WS - 2) * kW;
+  constexpr int kYounger = kFromX < kFromW ? kFromX : kFromW;
+  auto chunk = [&](int c, auto is_steady) {
+    constexpr bool steady = decltype(is_steady)::value;
+    const int xnext = xat + XB == XS * XB ? 0 : xat + XB, wnext = wat + WB == WS * WB ? 0 : wat + WB;
+    const bool more_x = steady || c + XS - 1 < nc, more_w = steady || c + WS < nc;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      const int j = s / MG, g = s % MG, r = s + kAhead, past = s - (kSteps - kAhead);
-      if (past == 0) {
-        // (The loads of chunks c + 2 .. c + STAGES - 1 are younger than those of c + 1.)
-        if (STAGES > 2 && c + STAGES <= nc) barrier(std::integral_constant<int, (STAGES - 2) * kDma>{});
-        else barrier(std::integral_constant<int, 0>{});
-      }
-      x[r % kRing] = r < kSteps ? read_x(at, r / MG, r % MG) : read_x(next, 0, r - kSteps);
+      constexpr int kBefore = kSteps - kAhead;
+      const int j = s / MG, g = s % MG, r = s + kAhead, past = s - kBefore;
+      if (past == 0) barrier(std::integral_constant<int, steady ? kYounger : 0>{});
+      x[r % kRing] = r < kSteps ? read_x(xat, r / MG, r % MG) : read_x(xnext, 0, r - kSteps);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        if (n * (MG / 2) / NT == s) w[1][n] = read_w(at, 1, n);
-        if (past >= 0 && n * kAhead / NT == past) w[0][n] = read_w(next, 0, n);
+        if (n * (MG / 2) / NT == s) w[1][n] = read_w(wat, 1, n);
+        if (past >= 0 && n * kAhead / NT == past) w[0][n] = read_w(wnext, 0, n);
       }
-      if (past >= 0 && more) {
+      if (past < 0 && more_x) {
 #pragma unroll
-        for (int i = 0; i < kDma; ++i)
-          if (i * kAhead / kDma == past) load(i, at, c + STAGES);
+        for (int i = 0; i < kX; ++i)
+          if (i * kBefore / kX == s) load_x(i, xfar, c + XS - 1);
+      }
+      if (past >= 0 && more_w) {
+#pragma unroll
+        for (int i = 0; i < kW; ++i)
+          if (i * kAhead / kW == past) load_w(i, wat, c + WS);
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) acc[g][n] = mfma16<F16>(w[j][n], x[s % kRing], acc[g][n]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    at = next;
-  }
+    xfar = xat;  // (chunk c + XS lies where chunk c did)
+    xat = xnext;
+    wat = wnext;
+  };
+  int c = 0;
+  for (; c + (XS - 1 > WS ? XS - 1 : WS) < nc; ++c) chunk(c, std::true_type{});
+  for (; c < nc; ++c) chunk(c, std::false_type{});
 
   // Row of W (inside the slice's two halves) of tile n.
   auto w_row = [&](int n) { return (n < NT / 2 ? 0 : TN / 2) + (wn * (NT / 2) + n % (NT / 2)) * 16; };
@@ -232,10 +262,10 @@ __device__ __forceinline__ void run_item(const LinearArgs& a, uint8_t* lds, int 
 // Persistent workgroups; workgroup b runs on XCD b % 8.  Runs of consecutive items go
 // to one XCD at a time, and items walk blocks of 8 token tiles slice by slice, so
 // those that run together share few token tiles and few slices through their L2.
-template <bool F16, int WM, int WN, int MG, int NT, int STAGES, int OCC>
+template <bool F16, int WM, int WN, int MG, int NT, int XS, int WS, int OCC>
 __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile(LinearArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  using S = Shape<WM, WN, MG, NT, STAGES>;
+  using S = Shape<WM, WN, MG, NT, XS, WS>;
   const int outs = a.gated ? S::kTN / 2 : S::kTN;
   const int slices = (a.N + outs - 1) / outs;
   const int64_t tiles = (a.M + S::kTM - 1) / S::kTM, whole = tiles * slices;
@@ -247,7 +277,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile(LinearArgs a) {
     const int wide = (int)min((int64_t)8, tiles - block * 8);
     const int rest = (int)(u - block * 8 * slices);
     __syncthreads();  // the last item's epilogue has left LDS
-    run_item<F16, WM, WN, MG, NT, STAGES>(a, lds, uniform((int)(block * 8) + rest % wide), uniform(rest / wide),
+    run_item<F16, WM, WN, MG, NT, XS, WS>(a, lds, uniform((int)(block * 8) + rest % wide), uniform(rest / wide),
                                   uniform((int)(i / whole)));
   }
 }
@@ -264,16 +294,16 @@ hipError_t launch_linear_tile(const LinearArgs& a, int shape, hipStream_t stream
     return hipGetLastError();
   };
 // (PER: workgroups of a CU)
-#define CHORD_LINEAR_SHAPE(WM, WN, MG, NT, STAGES, PER)                                                      \
-  return a.f16 ? run(linear_tile<true, WM, WN, MG, NT, STAGES, PER * WM * WN / 4>, WM * WN, PER,              \
-                     Shape<WM, WN, MG, NT, STAGES>::kLds)                                                    \
-               : run(linear_tile<false, WM, WN, MG, NT, STAGES, PER * WM * WN / 4>, WM * WN, PER,             \
-                     Shape<WM, WN, MG, NT, STAGES>::kLds)
+#define CHORD_LINEAR_SHAPE(WM, WN, MG, NT, XS, WS, PER)                                                      \
+  return a.f16 ? run(linear_tile<true, WM, WN, MG, NT, XS, WS, PER * WM * WN / 4>, WM * WN, PER,              \
+                     Shape<WM, WN, MG, NT, XS, WS>::kLds)                                                    \
+               : run(linear_tile<false, WM, WN, MG, NT, XS, WS, PER * WM * WN / 4>, WM * WN, PER,             \
+                     Shape<WM, WN, MG, NT, XS, WS>::kLds)
   switch (shape) {
-    case kLin256x256: CHORD_LINEAR_SHAPE(2, 4, 8, 4, 2, 1);
-    case kLin128x256: CHORD_LINEAR_SHAPE(2, 4, 4, 4, 3, 1);
-    case kLin128x128: CHORD_LINEAR_SHAPE(2, 4, 4, 2, 4, 1);
-    default: CHORD_LINEAR_SHAPE(2, 4, 2, 2, 3, 2);
+    case kLin256x256: CHORD_LINEAR_SHAPE(2, 4, 8, 4, 3, 2, 1);
+    case kLin128x256: CHORD_LINEAR_SHAPE(2, 4, 4, 4, 3, 3, 1);
+    case kLin128x128: CHORD_LINEAR_SHAPE(2, 4, 4, 2, 4, 4, 1);
+    default: CHORD_LINEAR_SHAPE(2, 4, 2, 2, 3, 3, 2);
   }
 #undef CHORD_LINEAR_SHAPE
 }
