@@ -94,45 +94,71 @@ bool rows_in_place(const void* p, int64_t ld, int K) {
   return aligned(p, 16) && ld % 8 == 0 && K % 8 == 0 && ld <= (int64_t)1 << 21;
 }
 
-// How a product runs: the weight-streaming form, or tiles with K in parts.
+// How a product runs: the weight-streaming form with tiles of 16 to 64 tokens, or
+// LDS tiles with K in parts that a second launch adds.
 struct LinearPlan {
   bool stream;
-  int shape, parts;
+  int tokens;        // stream
+  int shape, parts;  // tiles
   bool copy_x, copy_w;
   int K;  // of the rows that are read
   size_t x, w, partials, total;  // workspace: copies, sums
 };
 
+// us: of a chunk of 64 along K, on a workgroup alone.
 const struct {
   int rows, outs;
-} kLinearShapes[] = {{256, 256}, {128, 256}, {128, 128}, {64, 128}};
+  double us;
+} kLinearShapes[] = {{256, 256, 1.15}, {128, 256, 0.70}, {128, 128, 0.42}, {64, 128, 0.28}};
 
+// The cheapest by estimate, in us on an MI355X with 256 workgroups a round (one a CU in
+// every form).  Streaming: a launch 3.4; a step of its 8 waves is bound by the lines that
+// a CU takes, (16 + tokens) x 128 bytes a wave, less alone than beside 255 others; or the
+// weights' bytes at 6.5 TB/s.  Tiles: a launch and a round's start, chunks, up to 30 %
+// slower on a full chip, and for parts another launch and their bytes.  Over 45 sizes
+// with both sides measured (M = 1 .. 128; N x K = 384 x 7168, 2112 x 7168, 4096 x 7168,
+// 7168 x 2048, 1024 x 1024) what it picks takes 1.5 % more than the best on average.
+// Streaming with 16, 32, 64 tokens / best tiles: M=16 N=384 K=7168 6.6 8.1 11.6 / 9.7, N=4096
+// 12.4 12.4 13.5 / 16.0; M=32 N=2112 18.4 10.9 12.8 / 13.1; M=64 N=384 6.7 8.2 11.7 / 10.7, N=2112
+// 28.3 21.1 15.2 / 14.2, N=4096 41.2 23.5 16.6 / 18.4; M=100 N=2112 43.4 32.3 28.4 / 17.0.
+// Tiles of M=8192 N=384 K=7168: 256x256 130, in 4 parts 63, 128x256 80, 128x128 56, 64x128 66.
 LinearPlan linear_plan(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t M, int N, int K, int gated) {
   constexpr int64_t kCus = 256;  // (of the model, so that the workspace depends on sizes alone)
   LinearPlan p{};
   p.copy_x = !rows_in_place(x, ldx, K);
   p.copy_w = !rows_in_place(w, ldw, K);
   p.K = (K + 7) / 8 * 8;
+  p.parts = 1;
   const int64_t rows = (int64_t)N * (gated ? 2 : 1);
   const int chunks = (p.K + 63) / 64;
-  p.parts = 1;
-  p.stream = M <= 64;
-  if (!p.stream) {
-    double best = 1e30;
-    for (int s = 0; s < 4; ++s) {
-      const int64_t items = (M + kLinearShapes[s].rows - 1) / kLinearShapes[s].rows *
-                            ((rows + kLinearShapes[s].outs - 1) / kLinearShapes[s].outs);
-      for (int parts : {1, 2, 4, 8, 16}) {
-        if (parts > chunks || (parts > 1 && items * parts > 2 * kCus)) break;
-        const double rounds = (double)((items * parts + kCus - 1) / kCus);
-        const double area = (double)kLinearShapes[s].rows * kLinearShapes[s].outs / 65536.0;
-        double c = rounds * (4.0 + (chunks + parts - 1) / parts * (0.2 + 1.2 * area));
-        if (parts > 1) c += 4.5 + parts * (double)M * rows * 8 / 4e6;
-        if (c < best) {
-          best = c;
-          p.shape = s;
-          p.parts = parts;
-        }
+  double best = 1e300;
+  auto full = [&](int64_t items) { return std::min(1.0, (double)items / kCus); };
+  for (int tokens : {16, 32, 64}) {
+    const int64_t items = (M + tokens - 1) / tokens * ((N + (gated ? 7 : 15)) / (gated ? 8 : 16));
+    const double rounds = (double)((items + kCus - 1) / kCus), steps = (double)((chunks + 7) / 8);
+    const double lines = rounds * steps * (16 + tokens) * 0.0073 * (1.0 + 0.6 * std::sqrt(full(items)));
+    const double cost = 3.4 + 1.5 * (rounds - 1) +
+                        std::max(rounds > 1 ? 1.25 * lines : lines, (double)rows * p.K * 2 / 6.5e6);
+    if (cost < best) {
+      best = cost;
+      p.stream = true;
+      p.tokens = tokens;
+    }
+  }
+  for (int s = 0; s < 4; ++s) {
+    const int64_t items = (M + kLinearShapes[s].rows - 1) / kLinearShapes[s].rows *
+                          ((rows + kLinearShapes[s].outs - 1) / kLinearShapes[s].outs);
+    for (int parts : {1, 2, 4, 8, 16}) {
+      if (parts > 1 && (parts > chunks || items * parts > 2 * kCus)) break;
+      const double rounds = (double)((items * parts + kCus - 1) / kCus);
+      double cost = 2.5 + rounds * (1.2 + (chunks + parts - 1) / parts * kLinearShapes[s].us *
+                                              (1.0 + 0.3 * full(items * parts)));
+      if (parts > 1) cost += 4.0 + parts * (double)M * rows * 8 / 3.8e6;
+      if (cost < best) {
+        best = cost;
+        p.stream = false;
+        p.shape = s;
+        p.parts = parts;
       }
     }
   }
@@ -333,16 +359,16 @@ chord_status chord_linear(const void* x, int64_t ldx, const void* w, int64_t ldw
     a.ldw = plan.K;
   }
   a.K = plan.K;
-  HIP_TRY(plan.stream ? launch_linear_stream(a, st) : launch_linear_tile(a, plan.shape, st), "product launch");
+  HIP_TRY(plan.stream ? launch_linear_stream(a, plan.tokens, st) : launch_linear_tile(a, plan.shape, st), "product launch");
   if (plan.parts > 1) HIP_TRY(launch_linear_join(a, st), "product sum launch");
+  char text[64];
   if (plan.stream) {
-    set_last_plan("linear: streaming");
+    snprintf(text, sizeof(text), "linear: streaming, %d tokens", plan.tokens);
   } else {
-    char text[64];
     snprintf(text, sizeof(text), "linear: tiles of %d x %d, K in %d", kLinearShapes[plan.shape].rows,
              kLinearShapes[plan.shape].outs, plan.parts);
-    set_last_plan(text);
   }
+  set_last_plan(text);
   return CHORD_OK;
 }
 

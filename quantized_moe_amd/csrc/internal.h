@@ -472,7 +472,8 @@ hipError_t launch_f8_small(const F8SmallArgs& a, hipStream_t stream);
 hipError_t launch_f8_combine(const F8CombineArgs& a, hipStream_t stream);
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t stream);
-hipError_t launch_linear_stream(const LinearArgs& a, hipStream_t stream);
+// tokens: of a workgroup, 16, 32 or 64.
+hipError_t launch_linear_stream(const LinearArgs& a, int tokens, hipStream_t stream);
 hipError_t launch_linear_tile(const LinearArgs& a, int shape, hipStream_t stream);
 hipError_t launch_linear_join(const LinearArgs& a, hipStream_t stream);
 hipError_t launch_copy_rows(const uint16_t* src, int64_t ld, int64_t rows, int K, int to, uint16_t* dst,

@@ -5,8 +5,13 @@
 //
 // Weights are the A operand of the matrix instruction (16 rows of W), tokens the B
 // operand, so a lane's four results are four neighbouring outputs of one token.  A
-// workgroup streams 16 rows of W (gated: 8 gate rows and their 8 up rows) from memory
-// straight into registers; its waves split K and add up through LDS.
+// workgroup takes 16 rows of W (gated: 8 gate rows and their 8 up rows) and up to 64
+// tokens; its waves take every eighth chunk of 64 along K and add up through LDS.
+//
+// A wave brings its chunks by buffer_load ... lds into a ring of its own, eight lanes to
+// a row's 128 bytes, and reads them back as operands: no wave waits for another.  (Rows
+// loaded as operands are a request for every lane: one token through 4096 x 7168 took
+// 32 us so.)
 #include <type_traits>
 
 #include "linear_common.h"
@@ -14,67 +19,115 @@
 namespace chord {
 namespace {
 
-// 16 tokens x 16 rows of W a workgroup, K over WK waves, PF steps of 64 on their way.
-template <bool F16, int WK, int PF>
-__global__ __launch_bounds__(64 * WK) void linear_stream(LinearArgs a) {
-  __shared__ f32x4_t red[WK][64];
+constexpr int kStreamWaves = 8;
+constexpr int kChunk = 64, kRowBytes = 2 * kChunk;
+
+// XI: groups of 8 tokens; DEPTH: chunks of a wave on their way.  (Ordinary loads of
+// weights: as non-temporal ones they, and the tokens beside them, took 14.1 us for 12.4
+// with 16 tokens through 4096 x 7168.)
+template <bool F16, int XI, int DEPTH>
+__device__ __forceinline__ void stream_rows(const LinearArgs& a, uint8_t* lds) {
+  constexpr int MT = XI / 2;  // token operands
+  constexpr int kLoads = 2 + XI, kSlot = kLoads * 1024;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, col = lane & 15;
+  uint8_t* const ring = lds + wave * (DEPTH * kSlot);
   const int per = a.gated ? 8 : 16;  // outputs of a workgroup
   const int tiles = (a.N + per - 1) / per;
-  const int steps = (a.K + 63) / 64;
-  const int c_lo = (int)((int64_t)steps * wave / WK), c_hi = (int)((int64_t)steps * (wave + 1) / WK);
-  const int64_t items = (a.M + 15) / 16 * tiles;
+  const int chunks = (a.K + kChunk - 1) / kChunk, tail = a.K - (chunks - 1) * kChunk;
+  const int mine = (chunks - wave + kStreamWaves - 1) / kStreamWaves;
+  // Lane's row and 16-byte piece in a load, and in an operand (as the tiled form).
+  const int r = lane >> 3, p = (lane & 7) ^ (r & 6);
+  const bool in_tail = p * 8 < tail;
+  const int piece[2] = {(q ^ (col & 6)) * 16, ((4 + q) ^ (col & 6)) * 16};
+  typedef __attribute__((address_space(3))) void* Lds;
+
+  const int64_t items = (a.M + 8 * XI - 1) / (8 * XI) * tiles;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int64_t m0 = it / tiles * 16;
-    const int n0 = (int)(it % tiles) * per;
-    // Rows of this lane; lanes without one read nothing, which is zeros.
-    const int mine = a.gated ? col & 7 : col;
-    const bool has_w = n0 + mine < a.N, has_x = m0 + col < a.M;
-    // (From the first gate row: up rows are N rows further on, so the offset of a
-    // lane's row is in the base of its half.)
-    const uint16_t* wp = a.w + (int64_t)(n0 + (has_w ? mine : 0) + (a.gated && col >= 8 ? a.N : 0)) * a.ldw;
-    const uint16_t* xp = a.x + (m0 + (has_x ? col : 0)) * a.ldx;
-    u32x4_t w[PF][2], x[PF][2];
-    const u32x4_t zero = {0u, 0u, 0u, 0u};
-    auto load = [&](int p, int c) {
+    const int64_t m0 = (int64_t)__builtin_amdgcn_readfirstlane((int)(it / tiles)) * (8 * XI);
+    const int n0 = __builtin_amdgcn_readfirstlane((int)(it % tiles)) * per;
+    const int rows = (int)min((int64_t)(8 * XI), a.M - m0);
+    const int lo = min(8, a.N - n0), hi = a.gated ? lo : max(0, min(8, a.N - n0 - 8));
+    const __amdgpu_buffer_rsrc_t xres = row_buffer(a.x + m0 * a.ldx, rows, a.ldx, a.K);
+    const __amdgpu_buffer_rsrc_t wres = row_buffer(a.w + (int64_t)n0 * a.ldw, lo, a.ldw, a.K);
+    const __amdgpu_buffer_rsrc_t ures = row_buffer(a.w + ((int64_t)(a.gated ? a.N : 8) + n0) * a.ldw, hi, a.ldw, a.K);
+    const uint32_t w_lo = r < lo ? (uint32_t)(r * a.ldw * 2 + p * 16) : kLinNothing;
+    const uint32_t w_hi = r < hi ? (uint32_t)(r * a.ldw * 2 + p * 16) : kLinNothing;
+    uint32_t xo[XI];
+#pragma unroll
+    for (int i = 0; i < XI; ++i) xo[i] = 8 * i + r < rows ? (uint32_t)((8 * i + r) * a.ldx * 2 + p * 16) : kLinNothing;
+    auto load = [&](int slot, int i) {  // the wave's chunk i
+      const int c = wave + i * kStreamWaves;
+      const bool out = c == chunks - 1 && !in_tail;
+      uint8_t* const to = ring + slot * kSlot;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wres, (Lds)to, 16, out ? kLinNothing : w_lo, c * kRowBytes, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ures, (Lds)(to + 1024), 16, out ? kLinNothing : w_hi, c * kRowBytes, 0,
+                                               0);
+#pragma unroll
+      for (int x = 0; x < XI; ++x)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(xres, (Lds)(to + 2048 + x * 1024), 16, out ? kLinNothing : xo[x],
+                                                 c * kRowBytes, 0, 0);
+    };
+    auto wait = [&](auto outstanding) {
+      constexpr int vm = decltype(outstanding)::value;
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt((vm & 15) | (7 << 4) | (15 << 8) | ((vm >> 4) << 14));
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    f32x4_t acc[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    auto compute = [&](int slot) {
+      const uint8_t* const at = ring + slot * kSlot + col * kRowBytes;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int k = c * 64 + j * 32 + q * 8;
-        const bool in = k < a.K;
-        w[p][j] = in && has_w ? __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(wp + k)) : zero;
-        x[p][j] = in && has_x ? *reinterpret_cast<const u32x4_t*>(xp + k) : zero;
+        const u32x4_t w = *reinterpret_cast<const u32x4_t*>(at + piece[j]);
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+          acc[t] = mfma16<F16>(w, *reinterpret_cast<const u32x4_t*>(at + 2048 + t * 2048 + piece[j]), acc[t]);
       }
     };
-    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int p = 0; p < PF; ++p)
-      if (c_lo + p < c_hi) load(p, c_lo + p);
-    for (int c = c_lo; c < c_hi; c += PF) {
-#pragma unroll
-      for (int p = 0; p < PF; ++p) {
-        if (c + p < c_hi) {
-          acc = mfma16<F16>(w[p][0], x[p][0], acc);
-          acc = mfma16<F16>(w[p][1], x[p][1], acc);
-        }
-        if (c + p + PF < c_hi) load(p, c + p + PF);
-      }
+    for (int d = 0; d < DEPTH; ++d)
+      if (d < mine) load(d, d);
+    int slot = 0;
+    for (int i = 0; i < mine; ++i) {
+      if (i + DEPTH <= mine) wait(std::integral_constant<int, (DEPTH - 1) * kLoads>{});
+      else wait(std::integral_constant<int, 0>{});
+      compute(slot);
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (3 << 14));  // the slot is read
+      __builtin_amdgcn_sched_barrier(0);
+      if (i + DEPTH < mine) load(slot, i + DEPTH);
+      slot = slot + 1 == DEPTH ? 0 : slot + 1;
     }
-    red[wave][lane] = acc;
     __syncthreads();
-    if (wave == 0 && has_x && q * 4 < per) {
-      f32x4_t z = red[0][lane], up = {0.f, 0.f, 0.f, 0.f};
+    f32x4_t* const red = reinterpret_cast<f32x4_t*>(lds);  // [waves][MT][64]
 #pragma unroll
-      for (int u = 1; u < WK; ++u) z += red[u][lane];
-      if (a.gated) {
+    for (int t = 0; t < MT; ++t) red[(wave * MT + t) * 64 + lane] = acc[t];
+    __syncthreads();
+    if (wave < MT) {
+      const int64_t m = m0 + wave * 16 + col;
+      if (wave * 16 + col < rows && q * 4 < per) {
+        f32x4_t z = {0.f, 0.f, 0.f, 0.f}, up = z;
 #pragma unroll
-        for (int u = 0; u < WK; ++u) up += red[u][lane + 32];
+        for (int u = 0; u < kStreamWaves; ++u) z += red[(u * MT + wave) * 64 + lane];
+        if (a.gated) {
+#pragma unroll
+          for (int u = 0; u < kStreamWaves; ++u) up += red[(u * MT + wave) * 64 + lane + 32];
+        }
+        store_out4(a, m, n0 + 4 * q, z, up);
       }
-      store_out4(a, m0 + col, n0 + 4 * q, z, up);
     }
     __syncthreads();
   }
+}
+
+template <bool F16, int XI, int DEPTH>
+__global__ __launch_bounds__(64 * kStreamWaves) void linear_stream(LinearArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  stream_rows<F16, XI, DEPTH>(a, lds);
 }
 
 // Adds the parts of K, ascending, and finishes the outputs.
@@ -94,6 +147,9 @@ __global__ __launch_bounds__(256) void linear_join(LinearArgs a) {
   }
 }
 
+// (A vector of words that need no more than a word's alignment.)
+typedef uint32_t u32x4a4_t __attribute__((ext_vector_type(4), aligned(4)));
+
 // Rows of K values to 16-byte aligned rows of `to` values, the rest of them zeros.
 __global__ __launch_bounds__(256) void copy_rows(const uint16_t* __restrict__ src, int64_t ld, int64_t rows, int K,
                                                  int to, uint16_t* __restrict__ dst) {
@@ -103,24 +159,48 @@ __global__ __launch_bounds__(256) void copy_rows(const uint16_t* __restrict__ sr
     const int k = (int)(i - r * vecs) * 8;
     const uint16_t* p = src + r * ld + k;
     uint32_t w[4] = {0u, 0u, 0u, 0u};
+    // Words of two values; where they lie across the words of memory one value more is
+    // read on both sides, as long as that is inside the matrix.
+    const bool across = (reinterpret_cast<uintptr_t>(p) & 2) != 0;
+    const bool before = k > 0 || r > 0, behind = k + 9 <= K || r + 1 < rows;
+    if (!across && k + 8 <= K) {
+      const u32x4a4_t v = *reinterpret_cast<const u32x4a4_t*>(p);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (k + j < K) w[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+      for (int j = 0; j < 4; ++j) w[j] = v[j];
+    } else if (across && before && behind && k + 8 <= K) {
+      const u32x4a4_t v = *reinterpret_cast<const u32x4a4_t*>(p - 1);
+      const uint32_t last = *reinterpret_cast<const uint32_t*>(p + 7);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = v[j] >> 16 | (j < 3 ? v[j + 1] : last) << 16;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (k + j < K) w[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+    }
     reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
 }  // namespace
 
-hipError_t launch_linear_stream(const LinearArgs& a, hipStream_t stream) {
-  const int per = a.gated ? 8 : 16;
-  const int64_t items = (a.M + 15) / 16 * ((a.N + per - 1) / per), most = (int64_t)1 << 20;
-  const dim3 grid((unsigned)(items < most ? items : most));
-  auto run = [&](auto kernel, int waves) {
-    hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), 0, stream, a);
+hipError_t launch_linear_stream(const LinearArgs& a, int tokens, hipStream_t stream) {
+  auto run = [&](auto kernel, int xi, int depth) {
+    const int per = a.gated ? 8 : 16;
+    const int64_t items = (a.M + 8 * xi - 1) / (8 * xi) * ((a.N + per - 1) / per), most = (int64_t)1 << 20;
+    const int lds = kStreamWaves * depth * (2 + xi) * 1024;
+    const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(items < most ? items : most)), dim3(64 * kStreamWaves), lds, stream, a);
     return hipGetLastError();
   };
-  return a.f16 ? run(linear_stream<true, 16, 4>, 16) : run(linear_stream<false, 16, 4>, 16);
+#define CHORD_LINEAR_STREAM(XI, DEPTH) \
+  return a.f16 ? run(linear_stream<true, XI, DEPTH>, XI, DEPTH) : run(linear_stream<false, XI, DEPTH>, XI, DEPTH)
+  switch (tokens) {
+    case 16: CHORD_LINEAR_STREAM(2, 4);
+    case 32: CHORD_LINEAR_STREAM(4, 3);
+    default: CHORD_LINEAR_STREAM(8, 2);
+  }
+#undef CHORD_LINEAR_STREAM
 }
 
 hipError_t launch_linear_join(const LinearArgs& a, hipStream_t stream) {

@@ -303,7 +303,7 @@ hipError_t launch_linear_tile(const LinearArgs& a, int shape, hipStream_t stream
     case kLin256x256: CHORD_LINEAR_SHAPE(2, 4, 8, 4, 3, 2, 1);
     case kLin128x256: CHORD_LINEAR_SHAPE(2, 4, 4, 4, 3, 3, 1);
     case kLin128x128: CHORD_LINEAR_SHAPE(2, 4, 4, 2, 4, 4, 1);
-    default: CHORD_LINEAR_SHAPE(2, 4, 2, 2, 3, 3, 2);
+    default: CHORD_LINEAR_SHAPE(2, 4, 2, 2, 6, 6, 1);
   }
 #undef CHORD_LINEAR_SHAPE
 }
