@@ -763,11 +763,10 @@ typedef struct {
  * out:      device [T, ldo] of dtype out, or NULL; may be x with its row stride.
  * codes:    device [T, ceil(H/128)*128] out, 16-byte aligned, with scales: device
  *           fp32 [T, ceil(H/128)] out; or NULL both.
- * One of sum, out and codes is there.  dtype, gate_dtype and the norms' types are
- * any chord_dtype, stream_dtype is dtype or fp32.  1 <= H <= 32768, T below 2^31;
- * T == 0 is a no-op.  Any alignment of elements; 16-byte aligned rows with H % 8 ==
- * 0 are read and written wide.  Columns from H on stay as they are.  Enqueued on
- * `stream`; needs no workspace.
+ * One of sum, out and codes is there.  dtype is any chord_dtype; stream_dtype,
+ * gate_dtype and the norms' types are dtype or fp32.  1 <= H <= 32768, T below 2^31;
+ * T == 0 is a no-op.  Rows need no more than their elements' alignment.  Columns from H
+ * on stay as they are.  Enqueued on `stream`; needs no workspace.
  */
 chord_status chord_norm(const void* x, int64_t ldx, int dtype, int64_t T, int H,
                         const chord_norm_weight* post, const void* gate, int gate_dtype,

@@ -760,8 +760,8 @@ def chord_norm(x, pre: Optional[Norm] = None, post: Optional[Norm] = None, gate=
     """s = [residual +] scale * [gate *] (x, or post's norm of it); out and codes are
     pre's norm of s, from before s is rounded.  x [T, H] bf16, fp16 or fp32; residual
     and sum are of x's type or fp32 (sum_dtype: that of sum without a residual); gate
-    [T, 1], [H] or [T, H] of any of the three types, behind a sigmoid if asked.  Rows
-    may be strided.  What is written: the sum unless want_sum is False (by default
+    [T, 1], [H] or [T, H] of x's type or fp32, as the norms, behind a sigmoid if asked.
+    Rows may be strided.  What is written: the sum unless want_sum is False (by default
     where it is more than x alone), out where there is a `pre` (unless want_out is
     False), the 8-bit codes of out with their scales if want_codes.  sum_out (may be
     the residual), out and codes_out = (codes, scales) are tensors to write to."""

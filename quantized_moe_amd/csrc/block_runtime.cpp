@@ -19,13 +19,14 @@ bool known(int dtype) {
 // ---- norms -------------------------------------------------------------------
 constexpr int kNormMaxH = 32768;  // 1024 threads x 4 x 8 values
 
-chord_status norm_part(const chord_norm_weight* w, const char* name, NormPart* p) {
+chord_status norm_part(const chord_norm_weight* w, const char* name, int dtype, NormPart* p) {
   *p = NormPart{};
   if (!w) return CHORD_OK;
   if (!w->weight) return fail(CHORD_ERR_INVALID_ARGUMENT, "%s has no weight", name);
   if (w->kind != CHORD_NORM_RMS && w->kind != CHORD_NORM_LAYER)
     return fail(CHORD_ERR_INVALID_ARGUMENT, "%s kind %d", name, w->kind);
-  if (!known(w->dtype)) return fail(CHORD_ERR_INVALID_ARGUMENT, "%s dtype %d", name, w->dtype);
+  if (w->dtype != dtype && w->dtype != CHORD_DTYPE_F32)
+    return fail(CHORD_ERR_INVALID_ARGUMENT, "%s dtype %d (dtype %d or fp32)", name, w->dtype, dtype);
   // (Squares below the smallest normal number vanish beside it.)
   if (!std::isnormal(w->eps) || w->eps < 0.f)
     return fail(CHORD_ERR_INVALID_ARGUMENT, "%s eps %g must be a positive normal number", name, w->eps);
@@ -185,9 +186,9 @@ chord_status chord_norm(const void* x, int64_t ldx, int dtype, int64_t T, int H,
                         chord_f8* codes, float* scales, void* stream) {
   clear_last_error();
   NormArgs a{};
-  CHORD_CHECK(norm_part(post, "post", &a.post));
-  CHORD_CHECK(norm_part(pre, "pre", &a.pre));
   if (!known(dtype)) return fail(CHORD_ERR_INVALID_ARGUMENT, "dtype %d", dtype);
+  CHORD_CHECK(norm_part(post, "post", dtype, &a.post));
+  CHORD_CHECK(norm_part(pre, "pre", dtype, &a.pre));
   if (stream_dtype != dtype && stream_dtype != CHORD_DTYPE_F32)
     return fail(CHORD_ERR_INVALID_ARGUMENT, "stream_dtype %d (dtype %d or fp32)", stream_dtype, dtype);
   if (T < 0 || H < 1) return fail(CHORD_ERR_INVALID_ARGUMENT, "T=%lld H=%d", (long long)T, H);
@@ -203,13 +204,16 @@ chord_status chord_norm(const void* x, int64_t ldx, int dtype, int64_t T, int H,
   if (ldx < H || (residual && ldr < H) || (sum && lds < H) || (out && ldo < H))
     return fail(CHORD_ERR_INVALID_ARGUMENT, "a row stride is below H=%d", H);
   if (gate) {
-    if (!known(gate_dtype)) return fail(CHORD_ERR_INVALID_ARGUMENT, "gate_dtype %d", gate_dtype);
+    if (gate_dtype != dtype && gate_dtype != CHORD_DTYPE_F32)
+      return fail(CHORD_ERR_INVALID_ARGUMENT, "gate_dtype %d (dtype %d or fp32)", gate_dtype, dtype);
     if ((gate_col != 0 && gate_col != 1) || gate_row < 0)
       return fail(CHORD_ERR_INVALID_ARGUMENT, "gate strides %lld, %lld", (long long)gate_row, (long long)gate_col);
   }
   if (!x) return fail(CHORD_ERR_INVALID_ARGUMENT, "null pointer argument");
   if (codes && !aligned(codes, 16)) return fail(CHORD_ERR_INVALID_ARGUMENT, "codes must be 16-byte aligned");
-  CHORD_CHECK(check_device(nullptr));
+  int cus = 0;
+  CHORD_CHECK(check_device(&cus));
+  a.num_cus = cus;
   a.x = x;
   a.ldx = ldx;
   a.dtype = dtype;

@@ -385,6 +385,7 @@ struct NormArgs {
   int64_t ldo;
   uint8_t* codes;        // [T, chunks * 128], or null
   float* code_scales;    // [T, chunks]
+  int num_cus;
   int threads;           // of a row (set by the launcher)
 };
 

@@ -6,6 +6,8 @@
 // A row lives in the registers of its threads from the one time it is read to the
 // one time it is written, so the pass is bound by memory, whichever of the stages
 // it has.
+#include <type_traits>
+
 #include "f8_common.h"
 
 namespace chord {
@@ -14,296 +16,393 @@ namespace {
 constexpr int kMaxWaves = 16;
 constexpr float kShrink = 0x1p-96f;  // of rows whose squares overflow (2^128 2^-96 squared is far below)
 
-// Eight neighbouring values as they lie in memory: fp32, or 16 bits each in lo.
+// Eight neighbouring values as they lie in memory.  (Vectors that need no more than an
+// element's alignment: the instruction is the same as for aligned ones.)
+typedef uint32_t u32x4a2_t __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4a4_t __attribute__((ext_vector_type(4), aligned(4)));
+template <int DT>
 struct Raw8 {
+  u32x4_t lo;
+};
+template <>
+struct Raw8<CHORD_DTYPE_F32> {
   u32x4_t lo, hi;
 };
 
-template <bool WIDE>
-__device__ __forceinline__ Raw8 load_raw(const void* base, int dtype, int64_t at, int n) {
-  Raw8 r;
-  r.lo = r.hi = u32x4_t{0u, 0u, 0u, 0u};
-  if (n <= 0) return r;
-  if (dtype == CHORD_DTYPE_F32) {
-    const uint32_t* p = static_cast<const uint32_t*>(base) + at;
-    if (WIDE) {
-      r.lo = *reinterpret_cast<const u32x4_t*>(p);
-      r.hi = *reinterpret_cast<const u32x4_t*>(p + 4);
-    } else {
+// n of the eight values at base[row + at], row being the same for all lanes (n >= 8: all; without TAIL that or none).
+template <int DT, bool TAIL>
+__device__ __forceinline__ Raw8<DT> load_raw(const void* base, int64_t row, uint32_t at, int n) {
+  Raw8<DT> r{};
+  if constexpr (DT == CHORD_DTYPE_F32) {
+    const uint32_t* p = static_cast<const uint32_t*>(base) + row + at;
+    if (n >= 8) {
+      r.lo = *reinterpret_cast<const u32x4a4_t*>(p);
+      r.hi = *reinterpret_cast<const u32x4a4_t*>(p + 4);
+    } else if (TAIL) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (i < n) r.lo[i] = p[i];
-        if (i + 4 < n) r.hi[i] = p[i + 4];
-      }
+      for (int i = 0; i < 7; ++i)
+        if (i < n) (i < 4 ? r.lo : r.hi)[i & 3] = p[i];
     }
   } else {
-    const uint16_t* p = static_cast<const uint16_t*>(base) + at;
-    if (WIDE) {
-      r.lo = *reinterpret_cast<const u32x4_t*>(p);
-    } else {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + row + at;
+    if (n >= 8) {
+      r.lo = *reinterpret_cast<const u32x4a2_t*>(p);
+    } else if (TAIL) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < 7; ++i)
         if (i < n) r.lo[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
     }
   }
   return r;
 }
-__device__ __forceinline__ void widen(const Raw8& r, int dtype, float (&v)[8]) {
-  if (dtype == CHORD_DTYPE_F32) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = __uint_as_float(r.lo[i]);
-      v[i + 4] = __uint_as_float(r.hi[i]);
-    }
-  } else if (dtype == CHORD_DTYPE_BF16) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = bf16_to_f32(r.lo[i] & 0xFFFFu);
-      v[2 * i + 1] = __uint_as_float(r.lo[i] & 0xFFFF0000u);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const half2_t h = __builtin_bit_cast(half2_t, (uint32_t)r.lo[i]);
-      v[2 * i] = (float)h[0];
-      v[2 * i + 1] = (float)h[1];
-    }
-  }
+template <int DT>
+__device__ __forceinline__ float raw_value(const Raw8<DT>& r, int i) {
+  if constexpr (DT == CHORD_DTYPE_F32) return __uint_as_float(i < 4 ? r.lo[i] : r.hi[i & 3]);
+  const uint32_t w = r.lo[i >> 1];
+  if constexpr (DT == CHORD_DTYPE_BF16) return i & 1 ? __uint_as_float(w & 0xFFFF0000u) : bf16_to_f32(w);
+  return (float)__builtin_bit_cast(half2_t, w)[i & 1];
 }
-__device__ __forceinline__ float one_value(const void* base, int dtype, int64_t at) {
-  if (dtype == CHORD_DTYPE_F32) return static_cast<const float*>(base)[at];
+template <int DT>
+__device__ __forceinline__ float one_value(const void* base, int64_t at) {
+  if constexpr (DT == CHORD_DTYPE_F32) return static_cast<const float*>(base)[at];
   const uint16_t h = static_cast<const uint16_t*>(base)[at];
-  return dtype == CHORD_DTYPE_BF16 ? bf16_to_f32(h) : (float)__builtin_bit_cast(_Float16, h);
+  if constexpr (DT == CHORD_DTYPE_BF16) return bf16_to_f32(h);
+  return (float)__builtin_bit_cast(_Float16, h);
 }
-template <bool WIDE>
-__device__ __forceinline__ void store8(void* base, int dtype, int64_t at, int n, const float (&v)[8]) {
-  if (n <= 0) return;
-  if (dtype == CHORD_DTYPE_F32) {
-    float* p = static_cast<float*>(base) + at;
-    if (WIDE) {
-      *reinterpret_cast<f32x4_t*>(p) = f32x4_t{v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<f32x4_t*>(p + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
-    } else {
+template <int DT, bool TAIL>
+__device__ __forceinline__ void store8(void* base, int64_t row, uint32_t at, int n, const float (&v)[8]) {
+  if constexpr (DT == CHORD_DTYPE_F32) {
+    float* p = static_cast<float*>(base) + row + at;
+    if (n >= 8) {
+      *reinterpret_cast<u32x4a4_t*>(p) = u32x4a4_t{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                                   __float_as_uint(v[3])};
+      *reinterpret_cast<u32x4a4_t*>(p + 4) = u32x4a4_t{__float_as_uint(v[4]), __float_as_uint(v[5]),
+                                                       __float_as_uint(v[6]), __float_as_uint(v[7])};
+    } else if (TAIL) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < 7; ++i)
         if (i < n) p[i] = v[i];
     }
-    return;
-  }
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = dtype == CHORD_DTYPE_BF16 ? pk_bf16(v[2 * i], v[2 * i + 1]) : pk_f16(v[2 * i], v[2 * i + 1]);
-  uint16_t* p = static_cast<uint16_t*>(base) + at;
-  if (WIDE) {
-    *reinterpret_cast<u32x4_t*>(p) = u32x4_t{w[0], w[1], w[2], w[3]};
   } else {
+    u32x4a2_t w;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+    for (int i = 0; i < 4; ++i)
+      w[i] = DT == CHORD_DTYPE_BF16 ? pk_bf16(v[2 * i], v[2 * i + 1]) : pk_f16(v[2 * i], v[2 * i + 1]);
+    uint16_t* p = static_cast<uint16_t*>(base) + row + at;
+    if (n >= 8) {
+      *reinterpret_cast<u32x4a2_t*>(p) = w;
+    } else if (TAIL) {
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (i < n) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+    }
   }
 }
 
-// Sum over the threads of a row: register moves inside a wave, LDS between waves.
-// `slot` alternates, so one barrier a sum is enough.
-struct RowSum {
-  float (*part)[kMaxWaves];
-  int waves, slot;
-  __device__ __forceinline__ float operator()(float x) {
-    for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d, 64);
-    if (waves == 1) return x;
-    const int wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) part[slot][wave] = x;
-    __syncthreads();
-    x = 0.f;
-    for (int w = 0; w < waves; ++w) x += part[slot][w];
-    slot ^= 1;
-    return x;
-  }
-};
+// Sum over a wave, in every lane: neighbours 1, 2, 4 and 8 away inside the rows of 16
+// lanes, then the four rows.
+template <int CTRL>
+__device__ __forceinline__ float add_step(float x) {
+  return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float wave_sum(float x) {
+  x = add_step<0x118>(add_step<0x114>(add_step<0x112>(add_step<0x111>(x))));
+  auto lane = [&](int l) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), l)); };
+  return (lane(15) + lane(31)) + (lane(47) + lane(63));
+}
 
-// v (0 from column H on) less its mean (LAYER), times the factor that is returned, is
-// the norm without its weights.
-template <int V>
-__device__ __forceinline__ float centre(float (&v)[V][8], const int (&n)[V], const NormPart& p, int H,
-                                        RowSum& sum) {
-  float eps = p.eps, total = 0.f;
-  for (int round = 0;; ++round) {
-    float shift = 0.f;
-    if (p.kind == CHORD_NORM_LAYER) {
-      float t = 0.f;
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) t += v[i][j];
-      shift = sum(t) / (float)H;
-    }
+// x where value j of a thread's eight is one of the row's (n of them are; without TAIL
+// all or none), else 0: what stands behind a row is 0 and stays so.
+template <bool TAIL>
+__device__ __forceinline__ float only(float x, int n, int j) {
+  return (TAIL ? j < n : n > 0) ? x : 0.f;
+}
+
+// Sums over the threads of a row: register moves inside a wave, LDS between waves.
+// `slot` alternates, so one barrier is enough.
+struct RowSum {
+  float2 (*part)[kMaxWaves];
+  int waves, slot;
+  float own;  // values of this wave
+  const float* count;  // ... of each wave
+
+  __device__ __forceinline__ void share(float x, float y) {
+    slot ^= 1;
+    if ((threadIdx.x & 63) == 0) part[slot][threadIdx.x >> 6] = make_float2(x, y);
+    __syncthreads();
+  }
+  // Sum of squares.
+  template <int V>
+  __device__ __forceinline__ float squares(const float (&v)[V][8]) {
     float t = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
+      for (int j = 0; j < 8; ++j) t += v[i][j] * v[i][j];
+    t = wave_sum(t);
+    if (waves == 1) return t;
+    share(t, 0.f);
+    t = 0.f;
+    for (int w = 0; w < waves; ++w) t += part[slot][w].x;
+    return t;
+  }
+  // Mean, and sum of squares from it: of each wave from its own mean, which the
+  // distance of that mean from the row's adds to.  (One barrier; nothing cancels.)
+  template <int V, bool TAIL>
+  __device__ __forceinline__ float spread(const float (&v)[V][8], const int (&n)[V], int H, float* mean) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t += v[i][j];
+    const float m = own > 0.f ? wave_sum(t) / own : 0.f;
+    t = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float d = j < n[i] ? v[i][j] - shift : 0.f;
+        const float d = v[i][j] - only<TAIL>(m, n[i], j);
         t += d * d;
       }
-    total = sum(t);
-    // (Uniform over the row's threads.  A row with an infinity or NaN stays so.)
-    if (round == 1 || __builtin_isfinite(total)) {
-      if (p.kind == CHORD_NORM_LAYER) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[i][j] = j < n[i] ? v[i][j] - shift : 0.f;
-      }
-      break;
+    t = wave_sum(t);
+    *mean = m;
+    if (waves == 1) return t;
+    share(m, t);
+    float all = 0.f;
+    for (int w = 0; w < waves; ++w) all += part[slot][w].x * count[w];
+    const float centre = all / (float)H;
+    t = 0.f;
+    for (int w = 0; w < waves; ++w) {
+      const float2 p = part[slot][w];
+      const float d = p.x - centre;
+      t += p.y + count[w] * d * d;
     }
+    *mean = centre;
+    return t;
+  }
+};
+
+// v (0 from column H on), less its mean (LAYER), times the factor that is returned is
+// the norm without its weights.
+template <int V, bool TAIL>
+__device__ __forceinline__ float centre(float (&v)[V][8], const int (&n)[V], const NormPart& p, int H, RowSum& sum) {
+  const bool layer = p.kind == CHORD_NORM_LAYER;
+  float mean = 0.f, eps = p.eps;
+  float total = layer ? sum.spread<V, TAIL>(v, n, H, &mean) : sum.squares<V>(v);
+  if (!__builtin_isfinite(total + mean)) {
+    // (Uniform over the row's threads.  A row with an infinity or NaN stays so in small
+    // values, too.)
     eps *= kShrink * kShrink;
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[i][j] *= kShrink;
+    total = layer ? sum.spread<V, TAIL>(v, n, H, &mean) : sum.squares<V>(v);
+  }
+  if (layer) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] -= only<TAIL>(mean, n[i], j);
   }
   return 1.f / sqrtf(total / (float)H + eps);
 }
 
-// B threads hold a row, V times 8 neighbouring values each; a workgroup has one
-// row, or one a wave where a wave is enough.
-template <int V, bool WIDE>
-__global__ __launch_bounds__(1024) void norm_kernel(NormArgs a) {
-  __shared__ float part[2][kMaxWaves];
+template <int WT, int V, bool TAIL>
+__device__ __forceinline__ void load_row(const void* p, int64_t row, const int (&col)[V], const int (&n)[V],
+                                         Raw8<WT> (&r)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) r[i] = load_raw<WT, TAIL>(p, row, col[i], n[i]);
+}
+
+// Values of weights, biases or a gate: of type XT, or fp32 if `wide`.
+template <int XT, int V, bool TAIL>
+__device__ __forceinline__ void load_values(const void* p, bool wide, int64_t row, const int (&col)[V],
+                                            const int (&n)[V], float (&f)[V][8]) {
+  if (XT != CHORD_DTYPE_F32 && wide) {
+    Raw8<CHORD_DTYPE_F32> r[V];
+    load_row<CHORD_DTYPE_F32, V, TAIL>(p, row, col, n, r);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[i][j] = raw_value<CHORD_DTYPE_F32>(r[i], j);
+  } else {
+    Raw8<XT> r[V];
+    load_row<XT, V, TAIL>(p, row, col, n, r);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[i][j] = raw_value<XT>(r[i], j);
+  }
+}
+
+// v becomes its norm.
+template <int XT, int V, bool TAIL>
+__device__ __forceinline__ void apply_norm(float (&v)[V][8], const float (&w)[V][8], const int (&col)[V],
+                                           const int (&n)[V], const NormPart& p, int H, RowSum& sum) {
+  const float inv = centre<V, TAIL>(v, n, p, H, sum);
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * inv * w[i][j];
+  if (p.bias != nullptr) {
+    float b[V][8];
+    load_values<XT, V, TAIL>(p.bias, p.dtype == CHORD_DTYPE_F32, 0, col, n, b);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] += b[i][j];
+  }
+}
+
+// XT: type of x, out, and (unless fp32) of weights and gate; ST: of residual and sum.
+// The threads of a row hold V times 8 neighbouring values each; a workgroup has a row
+// at a time, or one a wave where a wave is enough.  The next row is on its way while
+// one is worked on, and weights stay in registers from row to row.
+// FULL: with a norm behind the block or a gate.  TAIL: H is no multiple of 8.
+template <int XT, int ST, int V, bool FULL, bool TAIL>
+__global__ __launch_bounds__(1024, TAIL && V == 1 && !FULL ? 8 : 4) void norm_kernel(NormArgs a) {
+  __shared__ float2 part[2][kMaxWaves];
+  __shared__ float count[kMaxWaves];
   const bool alone = a.threads > 64;  // ... in its workgroup
   const int tid = alone ? threadIdx.x : threadIdx.x & 63;
-  RowSum sum{part, alone ? a.threads >> 6 : 1, 0};
-  int col[V], n[V];
+  int col[V], n[V], held = 0;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     col[i] = (i * a.threads + tid) * 8;
     n[i] = min(8, a.H - col[i]);
+    held += max(n[i], 0);
   }
-  auto load = [&](const void* p, int dtype, int64_t row, Raw8 (&r)[V]) {
+  RowSum sum{part, alone ? a.threads >> 6 : 1, 0, wave_sum((float)held), count};
+  if (alone) {
+    if ((threadIdx.x & 63) == 0) count[threadIdx.x >> 6] = sum.own;
+    __syncthreads();
+  }
+  auto weights = [&](const NormPart& p, float (&w)[V][8]) {
+    if (p.weight == nullptr) return;
+    load_values<XT, V, TAIL>(p.weight, p.dtype == CHORD_DTYPE_F32, 0, col, n, w);
 #pragma unroll
-    for (int i = 0; i < V; ++i) r[i] = load_raw<WIDE>(p, dtype, row + col[i], n[i]);
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[i][j] += p.offset;
   };
+  auto gated = [&](float g) { return a.gate_sigmoid ? 1.f / (1.f + expf(-g)) : g; };
   // (Whole waves leave, where a wave has a row; else the workgroup's rows are there
   // for all of its waves.)
-  const int64_t step = alone ? (int64_t)gridDim.x : (int64_t)gridDim.x * (blockDim.x >> 6);
-  for (int64_t t = alone ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6);
-       t < a.T; t += step) {
-    Raw8 x[V], r[V], w[V], b[V];
-    load(a.x, a.dtype, t * a.ldx, x);
-    if (a.residual != nullptr) load(a.residual, a.stream_dtype, t * a.ldr, r);
-    float v[V][8];
+  const uint32_t of = alone ? 1 : blockDim.x >> 6, mine = alone ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t step = (int64_t)gridDim.x * of;
+  int64_t t = (int64_t)blockIdx.x * of + mine;
+  if (t >= a.T) return;
+  Raw8<XT> x[V];
+  Raw8<ST> r[V];
+  auto load = [&](int64_t row) {
+    load_row<XT, V, TAIL>(a.x, row * a.ldx, col, n, x);
+    if (a.residual != nullptr) load_row<ST, V, TAIL>(a.residual, row * a.ldr, col, n, r);
+  };
+  load(t);
+  float pre[V][8], post[V][8];
+  weights(a.pre, pre);
+  if (FULL) weights(a.post, post);
+  for (; t < a.T; t += step) {
+    float v[V][8], s[V][8];
 #pragma unroll
-    for (int i = 0; i < V; ++i) widen(x[i], a.dtype, v[i]);
-
-    auto norm = [&](const NormPart& p) {
-      load(p.weight, p.dtype, 0, w);
-      if (p.bias != nullptr) load(p.bias, p.dtype, 0, b);
-      const float inv = centre<V>(v, n, p, a.H, sum);
+    for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float f[8];
-        widen(w[i], p.dtype, f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * inv * (f[j] + p.offset);
-        if (p.bias != nullptr) {
-          widen(b[i], p.dtype, f);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[i][j] += f[j];
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = j < n[i] ? v[i][j] : 0.f;
+      for (int j = 0; j < 8; ++j) {
+        v[i][j] = raw_value<XT>(x[i], j);
+        s[i][j] = a.residual != nullptr ? raw_value<ST>(r[i], j) : 0.f;
       }
-    };
-    auto gated = [&](float g) { return a.gate_sigmoid ? 1.f / (1.f + expf(-g)) : g; };
-
-    if (a.post.weight != nullptr) norm(a.post);
+    if (t + step < a.T) load(t + step);
+    if (FULL && a.post.weight != nullptr) apply_norm<XT, V, TAIL>(v, post, col, n, a.post, a.H, sum);
     float scale = a.scale;
-    if (a.gate != nullptr) {
+    if (FULL && a.gate != nullptr) {
+      const bool wide = a.gate_dtype == CHORD_DTYPE_F32;
+      const int64_t row = t * a.gate_row;
       if (a.gate_col == 0) {
-        scale *= gated(one_value(a.gate, a.gate_dtype, t * a.gate_row));
+        scale *= gated(wide ? one_value<CHORD_DTYPE_F32>(a.gate, row) : one_value<XT>(a.gate, row));
       } else {
-        load(a.gate, a.gate_dtype, t * a.gate_row, w);
+        float g[V][8];
+        load_values<XT, V, TAIL>(a.gate, wide, row, col, n, g);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          float f[8];
-          widen(w[i], a.gate_dtype, f);
+        for (int i = 0; i < V; ++i)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[i][j] *= gated(f[j]);
-        }
+          for (int j = 0; j < 8; ++j) v[i][j] *= gated(g[i][j]);
       }
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      float f[8];
-      if (a.residual != nullptr) {
-        widen(r[i], a.stream_dtype, f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = __builtin_fmaf(v[i][j], scale, f[j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] *= scale;
-      }
-      if (a.sum != nullptr) store8<WIDE>(a.sum, a.stream_dtype, t * a.lds + col[i], n[i], v[i]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = j < n[i] ? v[i][j] : 0.f;  // (0 * an infinite gate)
+      for (int j = 0; j < 8; ++j) v[i][j] = __builtin_fmaf(v[i][j], scale, s[i][j]);
+      if (a.sum != nullptr) store8<ST, TAIL>(a.sum, t * a.lds, col[i], n[i], v[i]);
     }
     if (a.pre.weight == nullptr) continue;
-    norm(a.pre);
-    const int groups = (a.H + kF8Block - 1) / kF8Block;
+    apply_norm<XT, V, TAIL>(v, pre, col, n, a.pre, a.H, sum);
+    if (a.out != nullptr) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      if (a.out != nullptr) store8<WIDE>(a.out, a.dtype, t * a.ldo + col[i], n[i], v[i]);
-      if (a.codes != nullptr) {  // 16 lanes hold a group (by all of them)
+      for (int i = 0; i < V; ++i) store8<XT, TAIL>(a.out, t * a.ldo, col[i], n[i], v[i]);
+    }
+    if (a.codes != nullptr) {  // 16 lanes hold a group (by all of them)
+      const int groups = (a.H + kF8Block - 1) / kF8Block;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
         uint32_t m = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[i][j]) & 0x7FFFFFFFu);
         const F8Group q = f8_group(row_max16(m));
-        float c[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) c[j] = q.inv != 0.f ? f8_value(q, v[i][j]) : 0.f;
+        for (int j = 0; j < 8; ++j) v[i][j] = q.inv != 0.f ? f8_value(q, v[i][j]) : 0.f;
         if (col[i] < groups * kF8Block) {
           uint2 o;
-          o.x = f8_pack4(c[0], c[1], c[2], c[3]);
-          o.y = f8_pack4(c[4], c[5], c[6], c[7]);
-          *reinterpret_cast<uint2*>(a.codes + t * groups * kF8Block + col[i]) = o;
-          if ((tid & 15) == 0) a.code_scales[t * groups + col[i] / kF8Block] = q.scale;
+          o.x = f8_pack4(v[i][0], v[i][1], v[i][2], v[i][3]);
+          o.y = f8_pack4(v[i][4], v[i][5], v[i][6], v[i][7]);
+          *reinterpret_cast<uint2*>(a.codes + t * groups * kF8Block + (uint32_t)col[i]) = o;
+          if ((tid & 15) == 0) (a.code_scales + t * groups)[(uint32_t)col[i] / kF8Block] = q.scale;
         }
       }
     }
   }
 }
 
-bool wide_rows(const void* p, int64_t ld, int dtype) {
-  const int size = dtype == CHORD_DTYPE_F32 ? 4 : 2;
-  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0);
-}
-bool wide_part(const NormPart& p) {
-  return wide_rows(p.weight, 0, p.dtype) && wide_rows(p.bias, 0, p.dtype);
+template <int XT, int ST>
+hipError_t launch(const NormArgs& args, hipStream_t stream) {
+  NormArgs a = args;
+  const bool full = a.post.weight != nullptr || a.gate != nullptr;
+  const int vectors = (a.H + kF8Block - 1) / kF8Block * (kF8Block / 8);  // with those of a group's end
+  // Values a thread: 8 up to H = 8192 (with the stages of FULL 4096, whose registers
+  // leave less than two such workgroups a CU), as long as a workgroup's threads reach.
+  // us, 8 / 16 a thread: 8192 x 7168 85 / 90, with a norm behind the block 106 / 93.
+  const int v = vectors <= (full ? 512 : 1024) ? 1 : vectors <= 2048 ? 2 : 4;
+  a.threads = ((vectors + v - 1) / v + 63) / 64 * 64;
+  const int rows = a.threads == 64 ? 4 : 1;
+  // 16 waves a CU, the next row of each on its way (32 where rows end inside a vector:
+  // their loads take longer), and every workgroup as many rows as the others.  us, 16 /
+  // 32 waves: 8192 x 7168 85 / 89, x 7110 155 / 114.  (A workgroup a row without a next
+  // one: 134.)
+  const bool tail = a.H % 8 != 0;
+  const int waves = a.threads * rows / 64, fit = (tail && v == 1 && !full ? 32 : 16) / waves;
+  const int64_t most = (int64_t)a.num_cus * (fit > 1 ? fit : 1), blocks = (a.T + rows - 1) / rows;
+  const int64_t each = (blocks + most - 1) / most;
+  const dim3 grid((unsigned)((blocks + each - 1) / each)), block(a.threads * rows);
+  auto run = [&](auto full, auto tail) {
+    constexpr bool F = decltype(full)::value, L = decltype(tail)::value;
+    if (v == 1) hipLaunchKernelGGL((norm_kernel<XT, ST, 1, F, L>), grid, block, 0, stream, a);
+    else if (v == 2) hipLaunchKernelGGL((norm_kernel<XT, ST, 2, F, L>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((norm_kernel<XT, ST, 4, F, L>), grid, block, 0, stream, a);
+    return hipGetLastError();
+  };
+  const std::true_type yes{};
+  const std::false_type no{};
+  if (tail) return full ? run(yes, yes) : run(no, yes);
+  return full ? run(yes, no) : run(no, no);
 }
 
 }  // namespace
 
-hipError_t launch_norm(const NormArgs& args, hipStream_t stream) {
-  NormArgs a = args;
-  const bool wide = a.H % 8 == 0 && wide_rows(a.x, a.ldx, a.dtype) &&
-                    wide_rows(a.residual, a.ldr, a.stream_dtype) && wide_rows(a.sum, a.lds, a.stream_dtype) &&
-                    wide_rows(a.out, a.ldo, a.dtype) && wide_part(a.post) && wide_part(a.pre) &&
-                    (a.gate_col == 0 || wide_rows(a.gate, a.gate_row, a.gate_dtype));
-  const int vectors = (a.H + kF8Block - 1) / kF8Block * (kF8Block / 8);  // with those of a group's end
-  const int v = vectors <= 256 ? 1 : vectors <= 1024 ? 2 : 4;
-  a.threads = ((vectors + v - 1) / v + 63) / 64 * 64;
-  const int rows = a.threads == 64 ? 4 : 1;
-  // (A launch has fewer than 2^32 threads.)
-  const int64_t most = (int64_t)1 << 20, blocks = (a.T + rows - 1) / rows;
-  const dim3 grid((unsigned)(blocks < most ? blocks : most)), block(a.threads * rows);
-  auto run = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, block, 0, stream, a);
-    return hipGetLastError();
-  };
-  if (v == 1) return wide ? run(norm_kernel<1, true>) : run(norm_kernel<1, false>);
-  if (v == 2) return wide ? run(norm_kernel<2, true>) : run(norm_kernel<2, false>);
-  return wide ? run(norm_kernel<4, true>) : run(norm_kernel<4, false>);
+hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
+  constexpr int F32 = CHORD_DTYPE_F32, BF16 = CHORD_DTYPE_BF16, F16 = CHORD_DTYPE_F16;
+  if (a.dtype == F32) return launch<F32, F32>(a, stream);
+  if (a.dtype == BF16) return a.stream_dtype == F32 ? launch<BF16, F32>(a, stream) : launch<BF16, BF16>(a, stream);
+  return a.stream_dtype == F32 ? launch<F16, F32>(a, stream) : launch<F16, F16>(a, stream);
 }
 
 }  // namespace chord
