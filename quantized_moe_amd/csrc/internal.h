@@ -386,7 +386,8 @@ struct NormArgs {
   uint8_t* codes;        // [T, chunks * 128], or null
   float* code_scales;    // [T, chunks]
   int num_cus;
-  int threads;           // of a row (set by the launcher)
+  int threads;           // of a row; whether its threads keep columns in LDS, and how
+  int columns, columns_bytes;  // many bytes (set by the launcher)
 };
 
 struct BalanceArgs {

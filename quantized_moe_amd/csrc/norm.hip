@@ -14,6 +14,7 @@ namespace chord {
 namespace {
 
 constexpr int kMaxWaves = 16;
+constexpr int kColumnsPerCu = 150 << 10;  // LDS for vectors of columns
 constexpr float kShrink = 0x1p-96f;  // of rows whose squares overflow (2^128 2^-96 squared is far below)
 
 // Eight neighbouring values as they lie in memory.  (Vectors that need no more than an
@@ -111,6 +112,12 @@ __device__ __forceinline__ float wave_sum(float x) {
   return (lane(15) + lane(31)) + (lane(47) + lane(63));
 }
 
+// Sum over the first row of 16 lanes, in every lane.
+__device__ __forceinline__ float first_lanes_sum(float x) {
+  x = add_step<0x118>(add_step<0x114>(add_step<0x112>(add_step<0x111>(x))));
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 15));
+}
+
 // x where value j of a thread's eight is one of the row's (n of them are; without TAIL
 // all or none), else 0: what stands behind a row is 0 and stays so.
 template <bool TAIL>
@@ -123,13 +130,19 @@ __device__ __forceinline__ float only(float x, int n, int j) {
 struct RowSum {
   float2 (*part)[kMaxWaves];
   int waves, slot;
-  float own;  // values of this wave
-  const float* count;  // ... of each wave
+  float own;    // values of this wave
+  float count;  // ... of wave l in lane l
 
-  __device__ __forceinline__ void share(float x, float y) {
+  // x and y of wave l come to lane l (zeros to the lanes behind the waves).
+  __device__ __forceinline__ float2 share(float x, float y) {
     slot ^= 1;
     if ((threadIdx.x & 63) == 0) part[slot][threadIdx.x >> 6] = make_float2(x, y);
-    __syncthreads();
+    // (Fences of LDS alone: __syncthreads would wait for the next row as well.)
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    const int lane = threadIdx.x & 63;
+    return lane < waves ? part[slot][lane] : make_float2(0.f, 0.f);
   }
   // Sum of squares.
   template <int V>
@@ -141,10 +154,7 @@ struct RowSum {
       for (int j = 0; j < 8; ++j) t += v[i][j] * v[i][j];
     t = wave_sum(t);
     if (waves == 1) return t;
-    share(t, 0.f);
-    t = 0.f;
-    for (int w = 0; w < waves; ++w) t += part[slot][w].x;
-    return t;
+    return first_lanes_sum(share(t, 0.f).x);
   }
   // Mean, and sum of squares from it: of each wave from its own mean, which the
   // distance of that mean from the row's adds to.  (One barrier; nothing cancels.)
@@ -167,18 +177,10 @@ struct RowSum {
     t = wave_sum(t);
     *mean = m;
     if (waves == 1) return t;
-    share(m, t);
-    float all = 0.f;
-    for (int w = 0; w < waves; ++w) all += part[slot][w].x * count[w];
-    const float centre = all / (float)H;
-    t = 0.f;
-    for (int w = 0; w < waves; ++w) {
-      const float2 p = part[slot][w];
-      const float d = p.x - centre;
-      t += p.y + count[w] * d * d;
-    }
+    const float2 p = share(m, t);
+    const float centre = first_lanes_sum(p.x * count) / (float)H, d = p.x - centre;
     *mean = centre;
-    return t;
+    return first_lanes_sum(p.y + count * d * d);
   }
 };
 
@@ -215,55 +217,80 @@ __device__ __forceinline__ void load_row(const void* p, int64_t row, const int (
   for (int i = 0; i < V; ++i) r[i] = load_raw<WT, TAIL>(p, row, col[i], n[i]);
 }
 
-// Values of weights, biases or a gate: of type XT, or fp32 if `wide`.
+// A vector of columns (weights, a bias, a gate) of type XT, or fp32 if `wide`, as every
+// row needs it.  Each thread keeps its columns in LDS, where waiting for them does not
+// wait for the next row; nobody else reads them, so no barrier is needed.
 template <int XT, int V, bool TAIL>
-__device__ __forceinline__ void load_values(const void* p, bool wide, int64_t row, const int (&col)[V],
-                                            const int (&n)[V], float (&f)[V][8]) {
-  if (XT != CHORD_DTYPE_F32 && wide) {
-    Raw8<CHORD_DTYPE_F32> r[V];
-    load_row<CHORD_DTYPE_F32, V, TAIL>(p, row, col, n, r);
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[i][j] = raw_value<CHORD_DTYPE_F32>(r[i], j);
-  } else {
-    Raw8<XT> r[V];
-    load_row<XT, V, TAIL>(p, row, col, n, r);
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[i][j] = raw_value<XT>(r[i], j);
-  }
-}
+struct Columns {
+  const void* p;
+  bool wide;
+  uint8_t* kept;  // 16-byte pieces, this thread's `step` apart; or null: read again every time
+  int step;
 
-// v becomes its norm.
-template <int XT, int V, bool TAIL>
-__device__ __forceinline__ void apply_norm(float (&v)[V][8], const float (&w)[V][8], const int (&col)[V],
-                                           const int (&n)[V], const NormPart& p, int H, RowSum& sum) {
-  const float inv = centre<V, TAIL>(v, n, p, H, sum);
+  __device__ __forceinline__ static int bytes(bool wide, int threads) { return V * (wide ? 32 : 16) * threads; }
+  // Takes its place at *at.
+  __device__ __forceinline__ void keep(const void* ptr, int dtype, uint8_t** at, int threads, int tid,
+                                       const int (&col)[V], const int (&n)[V]) {
+    p = ptr;
+    wide = XT == CHORD_DTYPE_F32 || dtype == CHORD_DTYPE_F32;
+    kept = nullptr;
+    if (p == nullptr || *at == nullptr) return;
+    kept = *at + tid * 16;
+    step = threads * 16;
+    *at += bytes(wide, threads);
+    u32x4_t* to = reinterpret_cast<u32x4_t*>(kept);
+    const int s = threads;
+    if (wide) {
 #pragma unroll
-  for (int i = 0; i < V; ++i)
+      for (int i = 0; i < V; ++i) {
+        const auto r = load_raw<CHORD_DTYPE_F32, TAIL>(p, 0, col[i], n[i]);
+        to[(2 * i) * s] = r.lo;
+        to[(2 * i + 1) * s] = r.hi;
+      }
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * inv * w[i][j];
-  if (p.bias != nullptr) {
-    float b[V][8];
-    load_values<XT, V, TAIL>(p.bias, p.dtype == CHORD_DTYPE_F32, 0, col, n, b);
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] += b[i][j];
+      for (int i = 0; i < V; ++i) to[i * s] = load_raw<XT, TAIL>(p, 0, col[i], n[i]).lo;
+    }
   }
-}
+  // f(i, j, value) for value j of vector i, of row `row` where the vector has rows.
+  template <typename F>
+  __device__ __forceinline__ void each(int64_t row, const int (&col)[V], const int (&n)[V], F f) const {
+    if (wide) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        Raw8<CHORD_DTYPE_F32> r;
+        if (kept != nullptr) {
+          r.lo = *reinterpret_cast<const u32x4_t*>(kept + (2 * i) * step);
+          r.hi = *reinterpret_cast<const u32x4_t*>(kept + (2 * i + 1) * step);
+        } else {
+          r = load_raw<CHORD_DTYPE_F32, TAIL>(p, row, col[i], n[i]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f(i, j, raw_value<CHORD_DTYPE_F32>(r, j));
+      }
+    } else if constexpr (XT != CHORD_DTYPE_F32) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        Raw8<XT> r;
+        if (kept != nullptr) r.lo = *reinterpret_cast<const u32x4_t*>(kept + i * step);
+        else r = load_raw<XT, TAIL>(p, row, col[i], n[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f(i, j, raw_value<XT>(r, j));
+      }
+    }
+  }
+};
 
 // XT: type of x, out, and (unless fp32) of weights and gate; ST: of residual and sum.
 // The threads of a row hold V times 8 neighbouring values each; a workgroup has a row
 // at a time, or one a wave where a wave is enough.  The next row is on its way while
-// one is worked on, and weights stay in registers from row to row.
-// FULL: with a norm behind the block or a gate.  TAIL: H is no multiple of 8.
+// one is worked on.
+// FULL: with a norm behind the block, a gate or a bias; else the weights stay in
+// registers from row to row.  TAIL: H is no multiple of 8.
 template <int XT, int ST, int V, bool FULL, bool TAIL>
 __global__ __launch_bounds__(1024, TAIL && V == 1 && !FULL ? 8 : 4) void norm_kernel(NormArgs a) {
   __shared__ float2 part[2][kMaxWaves];
-  __shared__ float count[kMaxWaves];
+  extern __shared__ __attribute__((aligned(16))) uint8_t columns[];
   const bool alone = a.threads > 64;  // ... in its workgroup
   const int tid = alone ? threadIdx.x : threadIdx.x & 63;
   int col[V], n[V], held = 0;
@@ -273,19 +300,8 @@ __global__ __launch_bounds__(1024, TAIL && V == 1 && !FULL ? 8 : 4) void norm_ke
     n[i] = min(8, a.H - col[i]);
     held += max(n[i], 0);
   }
-  RowSum sum{part, alone ? a.threads >> 6 : 1, 0, wave_sum((float)held), count};
-  if (alone) {
-    if ((threadIdx.x & 63) == 0) count[threadIdx.x >> 6] = sum.own;
-    __syncthreads();
-  }
-  auto weights = [&](const NormPart& p, float (&w)[V][8]) {
-    if (p.weight == nullptr) return;
-    load_values<XT, V, TAIL>(p.weight, p.dtype == CHORD_DTYPE_F32, 0, col, n, w);
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[i][j] += p.offset;
-  };
+  RowSum sum{part, alone ? a.threads >> 6 : 1, 0, wave_sum((float)held), 0.f};
+  if (alone) sum.count = sum.share(sum.own, 0.f).x;
   auto gated = [&](float g) { return a.gate_sigmoid ? 1.f / (1.f + expf(-g)) : g; };
   // (Whole waves leave, where a wave has a row; else the workgroup's rows are there
   // for all of its waves.)
@@ -295,48 +311,72 @@ __global__ __launch_bounds__(1024, TAIL && V == 1 && !FULL ? 8 : 4) void norm_ke
   if (t >= a.T) return;
   Raw8<XT> x[V];
   Raw8<ST> r[V];
-  auto load = [&](int64_t row) {
-    load_row<XT, V, TAIL>(a.x, row * a.ldx, col, n, x);
+  auto load_x = [&](int64_t row) { load_row<XT, V, TAIL>(a.x, row * a.ldx, col, n, x); };
+  auto load_r = [&](int64_t row) {
     if (a.residual != nullptr) load_row<ST, V, TAIL>(a.residual, row * a.ldr, col, n, r);
   };
-  load(t);
-  float pre[V][8], post[V][8];
-  weights(a.pre, pre);
-  if (FULL) weights(a.post, post);
+#pragma unroll
+  for (int i = 0; i < V; ++i) r[i] = Raw8<ST>{};
+  load_x(t);
+  load_r(t);
+  typedef Columns<XT, V, TAIL> Vector;
+  Vector pre_w, pre_b, post_w, post_b, gate;
+  float pre[V][8];
+  if (FULL) {
+    uint8_t* at = a.columns ? columns + (threadIdx.x - tid) * (a.columns_bytes / a.threads) : nullptr;
+    pre_w.keep(a.pre.weight, a.pre.dtype, &at, a.threads, tid, col, n);
+    pre_b.keep(a.pre.bias, a.pre.dtype, &at, a.threads, tid, col, n);
+    post_w.keep(a.post.weight, a.post.dtype, &at, a.threads, tid, col, n);
+    post_b.keep(a.post.bias, a.post.dtype, &at, a.threads, tid, col, n);
+    uint8_t* none = nullptr;  // (a gate for each value is read with its row)
+    gate.keep(a.gate_col != 0 ? a.gate : nullptr, a.gate_dtype, a.gate_row == 0 ? &at : &none, a.threads, tid, col, n);
+  } else if (a.pre.weight != nullptr) {
+    uint8_t* none = nullptr;
+    pre_w.keep(a.pre.weight, a.pre.dtype, &none, a.threads, tid, col, n);
+    pre_w.each(0, col, n, [&](int i, int j, float w) { pre[i][j] = w + a.pre.offset; });
+  }
   for (; t < a.T; t += step) {
-    float v[V][8], s[V][8];
+    float v[V][8];
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[i][j] = raw_value<XT>(x[i], j);
-        s[i][j] = a.residual != nullptr ? raw_value<ST>(r[i], j) : 0.f;
-      }
-    if (t + step < a.T) load(t + step);
-    if (FULL && a.post.weight != nullptr) apply_norm<XT, V, TAIL>(v, post, col, n, a.post, a.H, sum);
+      for (int j = 0; j < 8; ++j) v[i][j] = raw_value<XT>(x[i], j);
+    const bool more = t + step < a.T;
+    if (more) load_x(t + step);
+    auto norm = [&](const NormPart& p, const Vector& w, const Vector& b) {
+      const float inv = centre<V, TAIL>(v, n, p, a.H, sum);
+      w.each(0, col, n, [&](int i, int j, float f) { v[i][j] = v[i][j] * inv * (f + p.offset); });
+      if (p.bias != nullptr) b.each(0, col, n, [&](int i, int j, float f) { v[i][j] += f; });
+    };
+    if (FULL && a.post.weight != nullptr) norm(a.post, post_w, post_b);
     float scale = a.scale;
     if (FULL && a.gate != nullptr) {
-      const bool wide = a.gate_dtype == CHORD_DTYPE_F32;
       const int64_t row = t * a.gate_row;
-      if (a.gate_col == 0) {
-        scale *= gated(wide ? one_value<CHORD_DTYPE_F32>(a.gate, row) : one_value<XT>(a.gate, row));
-      } else {
-        float g[V][8];
-        load_values<XT, V, TAIL>(a.gate, wide, row, col, n, g);
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[i][j] *= gated(g[i][j]);
-      }
+      if (a.gate_col == 0)
+        scale *= gated(a.gate_dtype == CHORD_DTYPE_F32 ? one_value<CHORD_DTYPE_F32>(a.gate, row)
+                                                       : one_value<XT>(a.gate, row));
+      else
+        gate.each(row, col, n, [&](int i, int j, float g) { v[i][j] *= gated(g); });
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = __builtin_fmaf(v[i][j], scale, s[i][j]);
-      if (a.sum != nullptr) store8<ST, TAIL>(a.sum, t * a.lds, col[i], n[i], v[i]);
+      for (int j = 0; j < 8; ++j) v[i][j] = __builtin_fmaf(v[i][j], scale, raw_value<ST>(r[i], j));
+    if (more) load_r(t + step);
+    if (a.sum != nullptr) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) store8<ST, TAIL>(a.sum, t * a.lds, col[i], n[i], v[i]);
     }
     if (a.pre.weight == nullptr) continue;
-    apply_norm<XT, V, TAIL>(v, pre, col, n, a.pre, a.H, sum);
+    if (FULL) {
+      norm(a.pre, pre_w, pre_b);
+    } else {
+      const float inv = centre<V, TAIL>(v, n, a.pre, a.H, sum);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * inv * pre[i][j];
+    }
     if (a.out != nullptr) {
 #pragma unroll
       for (int i = 0; i < V; ++i) store8<XT, TAIL>(a.out, t * a.ldo, col[i], n[i], v[i]);
@@ -366,29 +406,48 @@ __global__ __launch_bounds__(1024, TAIL && V == 1 && !FULL ? 8 : 4) void norm_ke
 template <int XT, int ST>
 hipError_t launch(const NormArgs& args, hipStream_t stream) {
   NormArgs a = args;
-  const bool full = a.post.weight != nullptr || a.gate != nullptr;
+  const bool full = a.post.weight != nullptr || a.gate != nullptr || a.pre.bias != nullptr;
   const int vectors = (a.H + kF8Block - 1) / kF8Block * (kF8Block / 8);  // with those of a group's end
   // Values a thread: 8 up to H = 8192 (with the stages of FULL 4096, whose registers
-  // leave less than two such workgroups a CU), as long as a workgroup's threads reach.
-  // us, 8 / 16 a thread: 8192 x 7168 85 / 90, with a norm behind the block 106 / 93.
+  // leave one such workgroup a CU), as long as a workgroup's threads reach.  us, 8 / 16 a
+  // thread: 8192 x 7168 85 / 90, with a norm behind the block 107 / 89, both of means and an
+  // fp32 stream at 4099 x 7112 100 / 86.
   const int v = vectors <= (full ? 512 : 1024) ? 1 : vectors <= 2048 ? 2 : 4;
   a.threads = ((vectors + v - 1) / v + 63) / 64 * 64;
   const int rows = a.threads == 64 ? 4 : 1;
   // 16 waves a CU, the next row of each on its way (32 where rows end inside a vector:
   // their loads take longer), and every workgroup as many rows as the others.  us, 16 /
-  // 32 waves: 8192 x 7168 85 / 89, x 7110 155 / 114.  (A workgroup a row without a next
-  // one: 134.)
+  // 32 waves: 8192 x 7168 85 / 89, 8191 x 7110 155 / 117.  (A workgroup a row without a
+  // next one: 134.)
   const bool tail = a.H % 8 != 0;
   const int waves = a.threads * rows / 64, fit = (tail && v == 1 && !full ? 32 : 16) / waves;
   const int64_t most = (int64_t)a.num_cus * (fit > 1 ? fit : 1), blocks = (a.T + rows - 1) / rows;
   const int64_t each = (blocks + most - 1) / most;
   const dim3 grid((unsigned)((blocks + each - 1) / each)), block(a.threads * rows);
+  // What each row of a workgroup keeps in LDS, if a CU's workgroups have room for it.
+  size_t lds = 0;
+  if (full) {
+    auto bytes = [&](const void* p, int dtype) {
+      return p == nullptr ? 0 : v * (dtype == CHORD_DTYPE_F32 ? 32 : 16) * a.threads;
+    };
+    a.columns_bytes = bytes(a.pre.weight, a.pre.dtype) + bytes(a.pre.bias, a.pre.dtype) +
+                      bytes(a.post.weight, a.post.dtype) + bytes(a.post.bias, a.post.dtype) +
+                      (a.gate_col != 0 && a.gate_row == 0 ? bytes(a.gate, a.gate_dtype) : 0);
+    a.columns = (int64_t)a.columns_bytes * rows * (fit > 1 ? fit : 1) <= kColumnsPerCu;
+    if (a.columns) lds = (size_t)a.columns_bytes * rows;
+  }
   auto run = [&](auto full, auto tail) {
     constexpr bool F = decltype(full)::value, L = decltype(tail)::value;
-    if (v == 1) hipLaunchKernelGGL((norm_kernel<XT, ST, 1, F, L>), grid, block, 0, stream, a);
-    else if (v == 2) hipLaunchKernelGGL((norm_kernel<XT, ST, 2, F, L>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((norm_kernel<XT, ST, 4, F, L>), grid, block, 0, stream, a);
-    return hipGetLastError();
+    auto go = [&](auto kernel) {
+      if (lds > 0) {
+        const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (int)lds);
+        if (e != hipSuccess) return e;
+      }
+      hipLaunchKernelGGL(kernel, grid, block, lds, stream, a);
+      return hipGetLastError();
+    };
+    return v == 1 ? go(norm_kernel<XT, ST, 1, F, L>) : v == 2 ? go(norm_kernel<XT, ST, 2, F, L>) : go(norm_kernel<XT, ST, 4, F, L>);
   };
   const std::true_type yes{};
   const std::false_type no{};
