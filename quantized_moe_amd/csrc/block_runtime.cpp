@@ -110,7 +110,7 @@ struct LinearPlan {
 const struct {
   int rows, outs;
   double us;
-} kLinearShapes[] = {{256, 256, 1.15}, {128, 256, 0.70}, {128, 128, 0.42}, {64, 128, 0.28}};
+} kLinearShapes[] = {{256, 256, 1.15}, {128, 256, 0.70}, {128, 128, 0.40}, {64, 128, 0.28}};
 
 // The cheapest by estimate, in us on an MI355X with 256 workgroups a round (one a CU in
 // every form).  Streaming: a launch 3.4; a step of its 8 waves is bound by the lines that
@@ -151,7 +151,9 @@ LinearPlan linear_plan(const void* x, int64_t ldx, const void* w, int64_t ldw, i
                           ((rows + kLinearShapes[s].outs - 1) / kLinearShapes[s].outs);
     for (int parts : {1, 2, 4, 8, 16}) {
       if (parts > 1 && (parts > chunks || items * parts > 2 * kCus)) break;
-      const double rounds = (double)((items * parts + kCus - 1) / kCus);
+      double rounds = (double)((items * parts + kCus - 1) / kCus);
+      const int64_t rest = items * parts % kCus;
+      if (s == 0 && rest > 0 && 2 * rest <= kCus) rounds -= 0.4;  // (the last round in halves)
       double cost = 2.5 + rounds * (1.2 + (chunks + parts - 1) / parts * kLinearShapes[s].us *
                                               (1.0 + 0.3 * full(items * parts)));
       if (parts > 1) cost += 4.0 + parts * (double)M * rows * 8 / 3.8e6;
@@ -350,6 +352,8 @@ chord_status chord_linear(const void* x, int64_t ldx, const void* w, int64_t ldw
   if (aligned(bias, a.bias_f32 ? 16 : 8)) a.wide |= kLinWideBias;
   if (aligned(residual, 4 * out_size) && ldr % 4 == 0) a.wide |= kLinWideResidual;
   if (aligned(out, 4 * out_size) && ldo % 4 == 0) a.wide |= kLinWideOut;
+  auto pieces = [&](const void* p, int64_t ld) { return aligned(p, 16) && ld * out_size % 16 == 0; };
+  a.direct = N % 8 == 0 && act != CHORD_ACT_GELU && pieces(out, ldo) && (!residual || pieces(residual, ldr));
   if (plan.copy_x) {
     uint16_t* to = reinterpret_cast<uint16_t*>(ws + plan.x);
     HIP_TRY(launch_copy_rows(a.x, ldx, M, K, plan.K, to, st), "copy launch");

@@ -427,6 +427,7 @@ struct LinearArgs {
   int64_t ldo;
   int out_f32;
   int wide;            // kLinWide*: what may be taken four values at a time
+  int direct;          // tiled: sums go to memory straight from registers
   int parts;           // of K, whose fp32 sums [parts, M, N (gated: and N) rounded up
   float* partials;     // to 16] a second launch adds
   int num_cus;

@@ -27,18 +27,32 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const uint16_t* p, 
   return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)bytes, kLinRsrcWord3);
 }
 
+// All waves' LDS accesses before it are done; loads and stores of memory go on.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// z / (1 + e^-y) with the hardware's exponential and reciprocal (about a unit of 2^-24
+// each, and of the exponent's argument y one for each unit of y).
+__device__ __forceinline__ float gate_of(float z, float y) {
+  return z * __builtin_amdgcn_rcpf(1.f + __expf(-y));
+}
+// The activations of a few instructions (all but GELU).
+__device__ __forceinline__ float activate_short(int act, float z) {
+  if (act == CHORD_ACT_SILU) return gate_of(z, z);
+  if (act == CHORD_ACT_GELU_TANH)  // (1 + tanh y) / 2 = 1 / (1 + e^-2y)
+    return gate_of(z, 1.5957691216057308f * (z + 0.044715f * z * z * z));
+  return z > 0.f ? z : z < 0.f ? 0.f : z;  // RELU (NaN stays)
+}
 // Activation in fp32.  The results are rounded to 16 bits, or stand beside sums of
 // products whose own error in fp32 is larger.
 __device__ __forceinline__ float activate(int act, float z) {
-  switch (act) {
-    case CHORD_ACT_RELU: return z > 0.f ? z : z < 0.f ? 0.f : z;  // (NaN stays)
-    case CHORD_ACT_SILU: return z / (1.f + expf(-z));
-    case CHORD_ACT_GELU:  // (erfc has no cancellation where the result is small)
-      return 0.5f * z * erfcf(z * -0.70710678118654752f);
-    case CHORD_ACT_GELU_TANH:  // (1 + tanh y) / 2 = 1 / (1 + e^-2y)
-      return z / (1.f + expf(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
-    default: return z;
-  }
+  if (act == CHORD_ACT_NONE) return z;
+  if (act == CHORD_ACT_GELU)  // (erfc has no cancellation where the result is small)
+    return 0.5f * z * erfcf(z * -0.70710678118654752f);
+  return activate_short(act, z);
 }
 
 __device__ __forceinline__ float value16(uint32_t h, bool f16) {
@@ -46,6 +60,17 @@ __device__ __forceinline__ float value16(uint32_t h, bool f16) {
 }
 __device__ __forceinline__ uint16_t round16(float v, bool f16) {
   return f16 ? __builtin_bit_cast(uint16_t, (_Float16)v) : to_bf16(v);
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+  if constexpr (F16) {
+    half2_t r;
+    r[0] = (_Float16)a;
+    r[1] = (_Float16)b;
+    return __builtin_bit_cast(uint32_t, r);
+  } else {
+    return pk_bf16(a, b);
+  }
 }
 __device__ __forceinline__ uint32_t round16x2(float a, float b, bool f16) {
   return (uint32_t)round16(a, f16) | (uint32_t)round16(b, f16) << 16;
@@ -98,6 +123,19 @@ __device__ __forceinline__ OutQuad out_quad(const LinearArgs& a, int n) {
 __device__ __forceinline__ f32x4_t out_residual(const LinearArgs& a, const OutQuad& o, int64_t m) {
   if (a.residual == nullptr) return f32x4_t{0.f, 0.f, 0.f, 0.f};
   return load4(a.residual, m * a.ldr + o.n, a.out_f32, a.f16, o.wide_res, o.left);
+}
+// The residual as it lies in memory (wide_res; 16-bit values in the first two words), so
+// that many loads can be on their way before the first is looked at.
+template <bool F32>
+__device__ __forceinline__ u32x4_t raw_residual(const LinearArgs& a, const OutQuad& o, int64_t m) {
+  if (F32) return *reinterpret_cast<const u32x4_t*>(static_cast<const float*>(a.residual) + m * a.ldr + o.n);
+  const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.residual) + m * a.ldr + o.n);
+  return u32x4_t{u.x, u.y, 0u, 0u};
+}
+__device__ __forceinline__ f32x4_t residual_value(const LinearArgs& a, u32x4_t r) {
+  if (a.out_f32) return __builtin_bit_cast(f32x4_t, r);
+  return f32x4_t{value16(r[0] & 0xFFFF, a.f16), value16(r[0] >> 16, a.f16), value16(r[1] & 0xFFFF, a.f16),
+                 value16(r[1] >> 16, a.f16)};
 }
 // From the sums over K; `up` holds the up rows' where gated.
 __device__ __forceinline__ void out_store(const LinearArgs& a, const OutQuad& o, int64_t m, f32x4_t z, f32x4_t up,

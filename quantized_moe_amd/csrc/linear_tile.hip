@@ -19,8 +19,8 @@
 // rows with piece p ^ 1 of the next four, and these keys put them, and the 16 lanes of
 // two such groups, on different banks.
 //
-// The sums leave through LDS, so that the epilogue is a short loop over neighbouring
-// outputs whatever the activation, and gate and up meet there.
+// Sums leave from registers, rounded, 16 bytes a lane.  Outputs that do not lie so, and
+// the long code of GELU, go through LDS to a short loop over neighbouring outputs.
 #include <type_traits>
 
 #include "linear_common.h"
@@ -42,7 +42,7 @@ struct Shape {
   static constexpr int kXBytes = kTM * kRowBytes, kWBytes = kTN * kRowBytes;  // of a chunk
   static constexpr int kRing = XS * kXBytes + WS * kWBytes;
   static constexpr int kPitch = kTN + 4;  // floats of a token in the epilogue
-  static constexpr int kOutRows = kTM > 128 ? 128 : kTM;
+  static constexpr int kOutRows = 64;  // tokens that pass through LDS at a time
   static constexpr size_t kLds = kRing > kOutRows * kPitch * 4 ? kRing : kOutRows * kPitch * 4;
 };
 
@@ -214,14 +214,125 @@ __device__ __forceinline__ void run_item(const LinearArgs& a, uint8_t* lds, int 
     }
     return;
   }
+  if (a.direct) {
+    // From registers to memory: a lane's four outputs of a tile, or eight of two
+    // neighbouring tiles after a swap between quarters of the wave (quarter q then has
+    // outputs 16 (q & 1) + 8 (q >> 1) on of the 32).
+    constexpr bool kPair = NT == 4;
+    constexpr int kWide = kPair ? 8 : 4;
+    auto store = [&](auto is_gated, auto is_f32) {
+      constexpr bool gated = decltype(is_gated)::value, F32 = decltype(is_f32)::value;
+      constexpr int kTiles = gated ? NT / 2 : NT;         // of outputs,
+      constexpr int kUnits = kPair ? kTiles / 2 : kTiles;  // stored at a time
+      constexpr int kWords = kWide * (F32 ? 4 : 2) / 4;
+      constexpr int kBatch = F32 ? 2 : MG < 4 ? MG : 4;    // token groups whose residuals come together
+      f32x4_t bias[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int f = first + w_row(n) - (gated && n >= NT / 2 ? TN / 2 : 0) + 4 * q;
+        bias[n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        if (a.bias != nullptr && f < a.N)
+          bias[n] = load4(a.bias, (gated && n >= NT / 2 ? a.N : 0) + f, a.bias_f32, F16, false, 4);
+      }
+      typedef uint32_t Words __attribute__((ext_vector_type(kWords)));
+      const int64_t size = F32 ? 4 : 2;
+      int64_t column[kUnits];
+      bool in[kUnits];
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        const int c = first + (kPair ? w_row(2 * u) + 16 * (q & 1) + 8 * (q >> 1) : w_row(u) + 4 * q);
+        column[u] = c;
+        in[u] = c < a.N;
+      }
+      const int64_t m = m0 + wm * MG * 16 + col;
+      const int left = rows - wm * MG * 16 - col;  // rows from this lane's first on
+      uint8_t* const out = static_cast<uint8_t*>(a.out) + m * a.ldo * size;
+      const uint8_t* const more = static_cast<const uint8_t*>(a.residual) + m * a.ldr * size;
+#pragma unroll
+      for (int g0 = 0; g0 < MG; g0 += kBatch) {
+        Words res[kBatch][kUnits];
+        if (a.residual != nullptr) {
+#pragma unroll
+          for (int g = 0; g < kBatch; ++g)
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u)
+              if ((g0 + g) * 16 < left && in[u])
+                res[g][u] = *reinterpret_cast<const Words*>(more + ((g0 + g) * 16 * a.ldr + column[u]) * size);
+        }
+#pragma unroll
+        for (int g = 0; g < kBatch; ++g) {
+          f32x4_t h[kTiles];
+#pragma unroll
+          for (int n = 0; n < kTiles; ++n) {
+            f32x4_t z = acc[g0 + g][n] + bias[n];
+            if (a.act != CHORD_ACT_NONE) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) z[i] = activate_short(a.act, z[i]);
+            }
+            if constexpr (gated) z *= acc[g0 + g][n + NT / 2] + bias[n + NT / 2];
+            h[n] = z * a.scale;
+          }
+#pragma unroll
+          for (int u = 0; u < kUnits; ++u) {
+            float v[kWide];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if constexpr (kPair) {
+                const auto w = __builtin_amdgcn_permlane16_swap(__float_as_uint(h[2 * u][i]),
+                                                                __float_as_uint(h[2 * u + 1][i]), false, false);
+                v[i] = __uint_as_float(w[0]);
+                v[i + 4] = __uint_as_float(w[1]);
+              } else {
+                v[i] = h[u][i];
+              }
+            }
+            if (a.residual != nullptr) {
+#pragma unroll
+              for (int i = 0; i < kWide; ++i)
+                v[i] += F32 ? __uint_as_float(res[g][u][i]) : value16(res[g][u][i / 2] >> (16 * (i & 1)) & 0xFFFF, F16);
+            }
+            Words w;
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
+              w[i] = F32 ? __float_as_uint(v[i]) : F16 ? pack16<true>(v[2 * i], v[2 * i + 1]) : pack16<false>(v[2 * i], v[2 * i + 1]);
+            if ((g0 + g) * 16 < left && in[u])
+              *reinterpret_cast<Words*>(out + ((g0 + g) * 16 * a.ldo + column[u]) * size) = w;
+          }
+        }
+      }
+    };
+    const std::true_type yes{};
+    const std::false_type no{};
+    if (a.out_f32) a.gated ? store(yes, yes) : store(no, yes);
+    else a.gated ? store(yes, no) : store(no, no);
+    return;
+  }
   float* sums = reinterpret_cast<float*>(lds);
   // (Opaque, so that addresses of the epilogue hold no registers during the loop.)
   int tid = threadIdx.x;
   asm volatile("" : "+v"(tid));
   constexpr int kPasses = TM / S::kOutRows, kGroups = S::kOutRows / 16;
+  // A thread has four neighbouring outputs of every kThreads / quads-th row.  Their
+  // residuals are on their way while the sums pass through LDS.
+  const int quads = outs / 4, step = kThreads / quads;
+  const int o = (tid & (quads - 1)) * 4;
+  const OutQuad out = out_quad(a, first + o);
 #pragma unroll
   for (int pass = 0; pass < kPasses; ++pass) {
-    __syncthreads();
+    const int mine = out.left > 0 ? min(rows - pass * S::kOutRows, S::kOutRows) : 0;
+    const int64_t top = m0 + pass * S::kOutRows;
+    // (As many as a thread has where nothing is gated: the fewest rows are there then.)
+    constexpr int kBatch = S::kOutRows * (TN / 4) / kThreads;
+    const bool early = a.residual != nullptr && out.wide_res && mine > 0;
+    u32x4_t res[kBatch];
+    if (early && a.out_f32) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) res[u] = raw_residual<true>(a, out, top + min(tid / quads + u * step, mine - 1));
+    } else if (early) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) res[u] = raw_residual<false>(a, out, top + min(tid / quads + u * step, mine - 1));
+    }
+    lds_barrier();
 #pragma unroll
     for (int g = 0; g < MG; ++g) {
       const int t = wm * MG + g - pass * kGroups;  // token group in this pass
@@ -231,29 +342,26 @@ __device__ __forceinline__ void run_item(const LinearArgs& a, uint8_t* lds, int 
         *reinterpret_cast<f32x4_t*>(sums + (t * 16 + (tid & 15)) * S::kPitch + w_row(n) + (tid >> 4 & 3) * 4) =
             acc[g][n];
     }
-    __syncthreads();
-    // A thread has four neighbouring outputs of every kThreads / quads-th row, kBatch of
-    // them at a time, so that their residuals are on their way together.
-    constexpr int kBatch = 4;
-    const int quads = outs / 4, step = kThreads / quads;
-    const int o = (tid & (quads - 1)) * 4;
-    const float* p = sums + o;
-    const OutQuad out = out_quad(a, first + o);
-    const int mine = min(rows - pass * S::kOutRows, S::kOutRows);
-    if (out.left > 0) {
-      for (int r = tid / quads; r < mine; r += kBatch * step) {
-        f32x4_t res[kBatch];
+    lds_barrier();
+    constexpr int kRead = kBatch < 4 ? kBatch : 4;
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-          if (r + u * step < mine) res[u] = out_residual(a, out, m0 + pass * S::kOutRows + r + u * step);
+    for (int u0 = 0; u0 < kBatch; u0 += kRead) {
+      f32x4_t z[kRead], up[kRead];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          if (r + u * step >= mine) continue;
-          const float* v = p + (r + u * step) * S::kPitch;
-          const f32x4_t z = *reinterpret_cast<const f32x4_t*>(v);
-          const f32x4_t up = *reinterpret_cast<const f32x4_t*>(a.gated ? v + TN / 2 : v);
-          out_store(a, out, m0 + pass * S::kOutRows + r + u * step, z, up, res[u]);
-        }
+      for (int u = 0; u < kRead; ++u) {
+        // (gated: half of the rows are behind the last)
+        const float* v = sums + o + ((tid / quads + (u0 + u) * step) & (S::kOutRows - 1)) * S::kPitch;
+        z[u] = *reinterpret_cast<const f32x4_t*>(v);
+        up[u] = *reinterpret_cast<const f32x4_t*>(a.gated ? v + TN / 2 : v);
+      }
+#pragma unroll
+      for (int u = 0; u < kRead; ++u) {
+        const int r = tid / quads + (u0 + u) * step;
+        if (r >= mine) continue;
+        f32x4_t more = {0.f, 0.f, 0.f, 0.f};
+        if (early) more = residual_value(a, res[u0 + u]);
+        else if (a.residual != nullptr) more = out_residual(a, out, top + r);
+        out_store(a, out, top + r, z[u], up[u], more);
       }
     }
   }
@@ -262,23 +370,38 @@ __device__ __forceinline__ void run_item(const LinearArgs& a, uint8_t* lds, int 
 // Persistent workgroups; workgroup b runs on XCD b % 8.  Runs of consecutive items go
 // to one XCD at a time, and items walk blocks of 8 token tiles slice by slice, so
 // those that run together share few token tiles and few slices through their L2.
-template <bool F16, int WM, int WN, int MG, int NT, int XS, int WS, int OCC>
+// CUT: items that fill no more than half a round are cut by rows into two (8192 x 7168
+// outputs are 3.5 rounds).
+template <bool F16, int WM, int WN, int MG, int NT, int XS, int WS, int OCC, bool CUT>
 __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile(LinearArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   using S = Shape<WM, WN, MG, NT, XS, WS>;
   const int outs = a.gated ? S::kTN / 2 : S::kTN;
   const int slices = (a.N + outs - 1) / outs;
-  const int64_t tiles = (a.M + S::kTM - 1) / S::kTM, whole = tiles * slices;
+  const int64_t tiles = (a.M + S::kTM - 1) / S::kTM, whole = tiles * slices, items = whole * a.parts;
   // (The grid is a multiple of 8.  Fewer items than workgroups spread over all XCDs.)
-  const int run = (int)min((int64_t)gridDim.x / kXcds, (whole * a.parts + kXcds - 1) / kXcds);
-  if ((int)(blockIdx.x / kXcds) >= run) return;
-  for (int64_t i = (int64_t)(blockIdx.x % kXcds) * run + blockIdx.x / kXcds; i < whole * a.parts; i += kXcds * run) {
+  const int64_t last = items / gridDim.x * gridDim.x, rest = items - last;
+  const bool cut = CUT && rest > 0 && 2 * rest <= gridDim.x;
+  const int xcd = blockIdx.x % kXcds, local = blockIdx.x / kXcds;
+  for (int64_t begin = 0; begin < items; begin += gridDim.x) {
+    const bool halves = cut && begin == last;
+    const int64_t here = min((int64_t)gridDim.x, halves ? 2 * rest : items - begin);
+    const int run = (int)((here + kXcds - 1) / kXcds), mine = xcd * run + local;
+    if (local >= run || mine >= here) continue;  // (a last round: uniform over the workgroup)
+    const int64_t i = begin + (halves ? mine >> 1 : mine);
     const int64_t u = i % whole, block = u / (8 * slices);
     const int wide = (int)min((int64_t)8, tiles - block * 8);
-    const int rest = (int)(u - block * 8 * slices);
-    __syncthreads();  // the last item's epilogue has left LDS
-    run_item<F16, WM, WN, MG, NT, XS, WS>(a, lds, uniform((int)(block * 8) + rest % wide), uniform(rest / wide),
-                                  uniform((int)(i / whole)));
+    const int at = (int)(u - block * 8 * slices);
+    const int tile = uniform((int)(block * 8) + at % wide), slice = uniform(at / wide), part = uniform((int)(i / whole));
+    lds_barrier();  // the last item's epilogue has left LDS
+    if constexpr (CUT) {
+      if (halves) {
+        if ((int64_t)(2 * tile + (mine & 1)) * (S::kTM / 2) < a.M)
+          run_item<F16, WM, WN, MG / 2, NT, XS, WS>(a, lds, 2 * tile + (mine & 1), slice, part);
+        continue;
+      }
+    }
+    run_item<F16, WM, WN, MG, NT, XS, WS>(a, lds, tile, slice, part);
   }
 }
 
@@ -286,24 +409,23 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile(LinearArgs a) {
 
 hipError_t launch_linear_tile(const LinearArgs& a, int shape, hipStream_t stream) {
   const int cus = a.num_cus >= 8 ? a.num_cus / 8 * 8 : 8;
-  auto run = [&](auto kernel, int waves, int per_cu, size_t lds) {
+  auto run = [&](auto kernel, int waves, size_t lds) {
     const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(cus * per_cu)), dim3(64 * waves), lds, stream, a);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)cus), dim3(64 * waves), lds, stream, a);
     return hipGetLastError();
   };
-// (PER: workgroups of a CU)
-#define CHORD_LINEAR_SHAPE(WM, WN, MG, NT, XS, WS, PER)                                                      \
-  return a.f16 ? run(linear_tile<true, WM, WN, MG, NT, XS, WS, PER * WM * WN / 4>, WM * WN, PER,              \
+#define CHORD_LINEAR_SHAPE(WM, WN, MG, NT, XS, WS, CUT)                                                      \
+  return a.f16 ? run(linear_tile<true, WM, WN, MG, NT, XS, WS, WM * WN / 4, CUT>, WM * WN,                    \
                      Shape<WM, WN, MG, NT, XS, WS>::kLds)                                                    \
-               : run(linear_tile<false, WM, WN, MG, NT, XS, WS, PER * WM * WN / 4>, WM * WN, PER,             \
+               : run(linear_tile<false, WM, WN, MG, NT, XS, WS, WM * WN / 4, CUT>, WM * WN,                   \
                      Shape<WM, WN, MG, NT, XS, WS>::kLds)
   switch (shape) {
-    case kLin256x256: CHORD_LINEAR_SHAPE(2, 4, 8, 4, 3, 2, 1);
-    case kLin128x256: CHORD_LINEAR_SHAPE(2, 4, 4, 4, 3, 3, 1);
-    case kLin128x128: CHORD_LINEAR_SHAPE(2, 4, 4, 2, 4, 4, 1);
-    default: CHORD_LINEAR_SHAPE(2, 4, 2, 2, 6, 6, 1);
+    case kLin256x256: CHORD_LINEAR_SHAPE(2, 4, 8, 4, 3, 2, true);
+    case kLin128x256: CHORD_LINEAR_SHAPE(2, 4, 4, 4, 3, 3, false);
+    case kLin128x128: CHORD_LINEAR_SHAPE(2, 4, 4, 2, 4, 4, false);
+    default: CHORD_LINEAR_SHAPE(2, 4, 2, 2, 6, 6, false);
   }
 #undef CHORD_LINEAR_SHAPE
 }
