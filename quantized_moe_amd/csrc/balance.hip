@@ -17,35 +17,61 @@ namespace {
 
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
+constexpr int kFinishThreads = 1024;
 constexpr float kOff = -INFINITY;
 
+// Over a wave, in every lane: neighbours 1, 2, 4 and 8 away inside the rows of 16
+// lanes (a lane without one keeps its own), then the four rows' last lanes.
+template <int CTRL, typename F>
+__device__ __forceinline__ float with_neighbour(float x, float none, F f) {
+  return f(x, __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(none), __float_as_int(x), CTRL, 0xF, 0xF, false)));
+}
+template <typename F>
+__device__ __forceinline__ float over_wave(float x, float none, F f) {
+  x = with_neighbour<0x111>(x, none, f);
+  x = with_neighbour<0x112>(x, none, f);
+  x = with_neighbour<0x114>(x, none, f);
+  x = with_neighbour<0x118>(x, none, f);
+  auto lane = [&](int l) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), l)); };
+  return f(f(lane(15), lane(31)), f(lane(47), lane(63)));
+}
 __device__ __forceinline__ float wave_add(float x) {
-  for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d, 64);
-  return x;
+  return over_wave(x, 0.f, [](float a, float b) { return a + b; });
 }
 __device__ __forceinline__ float wave_top(float x) {
-  for (int d = 1; d < 64; d <<= 1) x = fmaxf(x, __shfl_xor(x, d, 64));
-  return x;
+  return over_wave(x, kOff, [](float a, float b) { return fmaxf(a, b); });
 }
 // As the router has it: -inf and NaN are not available, +inf is the largest number.
 __device__ __forceinline__ float clamp_in(float x) {
   return x > kOff ? fminf(x, 3.402823466e38f) : kOff;
 }
 
-// Adds the slots first + [0, n) of a sequence's ids, n a multiple of k, to the counts
-// in LDS.
-__device__ __forceinline__ void count_slots(const BalanceArgs& a, const int32_t* ids, int64_t n, int32_t* counts,
+// Adds the slots of `rows` rows of ids to the counts in LDS, and the rows with an expert
+// to *tokens.
+__device__ __forceinline__ void count_slots(const BalanceArgs& a, const int32_t* ids, int64_t rows, int32_t* counts,
                                             int32_t* tokens) {
-  const int64_t rows = n / a.k;
+  auto slot = [&](int id) {
+    const bool in = (uint32_t)id < (uint32_t)a.E;
+    if (in) atomicAdd(&counts[id], 1);
+    return in;
+  };
+  const bool fours = a.k % 4 == 0 && reinterpret_cast<uintptr_t>(ids) % 16 == 0;
   int real = 0;
+#pragma unroll 2
   for (int64_t t = threadIdx.x; t < rows; t += kThreads) {
     bool any = false;
-    for (int j = 0; j < a.k; ++j) {
-      const uint32_t e = (uint32_t)ids[t * a.k + j];
-      if (e < (uint32_t)a.E) {
-        atomicAdd(&counts[e], 1);
-        any = true;
+    if (fours) {
+      const int4* p = reinterpret_cast<const int4*>(ids + t * a.k);
+#pragma unroll 2
+      for (int j = 0; j < a.k / 4; ++j) {
+        const int4 v = p[j];
+        any |= slot(v.x);
+        any |= slot(v.y);
+        any |= slot(v.z);
+        any |= slot(v.w);
       }
+    } else {
+      for (int j = 0; j < a.k; ++j) any |= slot(ids[t * a.k + j]);
     }
     real += any ? 1 : 0;
   }
@@ -59,31 +85,49 @@ __global__ __launch_bounds__(kThreads) void balance_count(BalanceArgs a) {
   __syncthreads();
   const int64_t rows = (a.L + a.parts - 1) / a.parts, first = min(a.L, rows * blockIdx.x);
   const int64_t mine = min(rows, a.L - first);
-  count_slots(a, a.ids + ((int64_t)blockIdx.y * a.L + first) * a.k, mine * a.k, counts, &counts[a.E]);
+  count_slots(a, a.ids + ((int64_t)blockIdx.y * a.L + first) * a.k, mine, counts, &counts[a.E]);
   __syncthreads();
   int32_t* out = a.part_counts + ((int64_t)blockIdx.y * a.parts + blockIdx.x) * (a.E + 1);
   for (int e = threadIdx.x; e <= a.E; e += kThreads) out[e] = counts[e];
 }
 
-// The sum over chunks of P, and the loss, of a sequence.
+// The sum over chunks of P, and the loss, of a sequence, by THREADS threads.  They
+// take an expert each; where there are enough for several of each, those share the
+// chunks.
+template <int THREADS>
 __device__ __forceinline__ void finish(const BalanceArgs& a, int s, const float* part, int chunks,
                                        const int32_t* counts, int n, double* tmp) {
+  const int wide = (a.E + 63) / 64 * 64, groups = THREADS / wide > 0 ? THREADS / wide : 1;
+  const int group = threadIdx.x / wide, me = threadIdx.x % wide;
+  const int c0 = chunks * group / groups, c1 = chunks * (group + 1) / groups;
   const double inv = n > 0 ? 1.0 / n : 0.0;
   double loss = 0.0;
-  for (int e = threadIdx.x; e < a.E; e += kThreads) {
+  for (int e0 = 0; e0 < a.E; e0 += THREADS) {  // (once, but for E over THREADS)
+    const int e = e0 + me;
     double p = 0.0;
+    if (group < groups && e < a.E) {
 #pragma unroll 8
-    for (int c = 0; c < chunks; ++c) p += part[(int64_t)c * a.E + e];
-    p *= inv;
-    a.probs[(int64_t)s * a.E + e] = (float)p;
-    loss += p * counts[e];
+      for (int c = c0; c < c1; ++c) p += part[(int64_t)c * a.E + e];
+    }
+    if (groups > 1) {
+      if (group < groups) tmp[group * wide + me] = p;
+      __syncthreads();
+      if (group == 0)
+        for (int g = 1; g < groups; ++g) p += tmp[g * wide + me];
+      __syncthreads();
+    }
+    if (group == 0 && e < a.E) {
+      p *= inv;
+      a.probs[(int64_t)s * a.E + e] = (float)p;
+      loss += p * counts[e];
+    }
   }
   for (int d = 1; d < 64; d <<= 1) loss += __shfl_xor(loss, d, 64);
   if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = loss;
   __syncthreads();
   if (threadIdx.x == 0) {
     double t = 0.0;
-    for (int w = 0; w < kWaves; ++w) t += tmp[w];
+    for (int w = 0; w < THREADS / 64; ++w) t += tmp[w];
     a.loss[s] = (float)(t * a.E / a.k * inv);
   }
 }
@@ -92,7 +136,7 @@ template <int V, bool SIGMOID>
 __global__ __launch_bounds__(kThreads) void balance_rows(BalanceArgs a) {
   __shared__ int32_t counts[kMaxExperts + 1];
   __shared__ float sums[kWaves][V * 64];
-  __shared__ double tmp[kWaves];
+  __shared__ double tmp[kThreads];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int s = blockIdx.y, chunk = blockIdx.x;
   const int64_t row0 = (int64_t)s * a.L;
@@ -103,7 +147,7 @@ __global__ __launch_bounds__(kThreads) void balance_rows(BalanceArgs a) {
   }
   __syncthreads();
   if (a.parts == 0) {
-    count_slots(a, a.ids + row0 * a.k, a.L * a.k, counts, &counts[a.E]);
+    count_slots(a, a.ids + row0 * a.k, a.L, counts, &counts[a.E]);
     __syncthreads();
   }
   const int n = counts[a.E];
@@ -119,27 +163,37 @@ __global__ __launch_bounds__(kThreads) void balance_rows(BalanceArgs a) {
     sum[i] = 0.f;
   }
   const int64_t first = chunk * a.rows, last = min(a.L, first + a.rows);
-  for (int64_t t = first + wave; t < last; t += kWaves) {
+  // A row's logits and first 64 ids, one row ahead.
+  float raw[V];
+  int id = -1;
+  auto load = [&](int64_t t) {
     const int64_t row = row0 + t;
-    bool any = false;
-    for (int j = lane; j < a.k; j += 64) any |= (uint32_t)a.ids[row * a.k + j] < (uint32_t)a.E;
+    id = lane < a.k ? a.ids[row * a.k + lane] : -1;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int64_t at = row * a.ld + min(i * 64 + lane, a.E - 1);
+      if (a.dtype == CHORD_DTYPE_F32) raw[i] = static_cast<const float*>(a.logits)[at];
+      else raw[i] = __uint_as_float(static_cast<const uint16_t*>(a.logits)[at]);
+    }
+  };
+  int64_t t = first + __builtin_amdgcn_readfirstlane(wave);
+  if (t < last) load(t);
+  for (; t < last; t += kWaves) {
+    const int64_t row = row0 + t;
+    bool any = (uint32_t)id < (uint32_t)a.E;
+    for (int j = lane + 64; j < a.k; j += 64) any |= (uint32_t)a.ids[row * a.k + j] < (uint32_t)a.E;
     const bool real = __builtin_amdgcn_ballot_w64(any) != 0;
     float* out = a.grad != nullptr ? a.grad + row * a.E : nullptr;
-    float p[V], rest[V];
-    if (real) {
-      float l[V];
+    float l[V], p[V], rest[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int64_t at = row * a.ld + min(i * 64 + lane, a.E - 1);
-        float x;
-        if (a.dtype == CHORD_DTYPE_F32) {
-          x = static_cast<const float*>(a.logits)[at];
-        } else {
-          const uint16_t h = static_cast<const uint16_t*>(a.logits)[at];
-          x = a.dtype == CHORD_DTYPE_BF16 ? bf16_to_f32(h) : (float)__builtin_bit_cast(_Float16, h);
-        }
-        l[i] = there[i] ? clamp_in(x) : kOff;
-      }
+    for (int i = 0; i < V; ++i) {
+      const uint32_t h = __float_as_uint(raw[i]);
+      const float x = a.dtype == CHORD_DTYPE_F32 ? raw[i]
+                      : a.dtype == CHORD_DTYPE_BF16 ? bf16_to_f32(h) : (float)__builtin_bit_cast(_Float16, (uint16_t)h);
+      l[i] = there[i] ? clamp_in(x) : kOff;
+    }
+    if (t + kWaves < last) load(t + kWaves);
+    if (real) {
       float top = 0.f;
       if (!SIGMOID) {
         top = l[0];
@@ -161,11 +215,11 @@ __global__ __launch_bounds__(kThreads) void balance_rows(BalanceArgs a) {
         p[i] = l[i] > kOff ? p[i] : 0.f;
         total += p[i];
       }
-      total = wave_add(total) + 1e-20f;
+      const float inv = 1.f / (wave_add(total) + 1e-20f);
       float mean = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        p[i] /= total;
+        p[i] *= inv;
         sum[i] += p[i];
         mean += f[i] * p[i];
       }
@@ -196,14 +250,14 @@ __global__ __launch_bounds__(kThreads) void balance_rows(BalanceArgs a) {
     for (int e = threadIdx.x; e < a.E; e += kThreads) a.counts[(int64_t)s * a.E + e] = counts[e];
     if (threadIdx.x == 0) a.tokens[s] = n;
   }
-  if (only) finish(a, s, sums[0], 1, counts, n, tmp);
+  if (only) finish<kThreads>(a, s, sums[0], 1, counts, n, tmp);
 }
 
-__global__ __launch_bounds__(kThreads) void balance_finish(BalanceArgs a) {
-  __shared__ double tmp[kWaves];
+__global__ __launch_bounds__(kFinishThreads) void balance_finish(BalanceArgs a) {
+  __shared__ double tmp[kFinishThreads];
   const int s = blockIdx.x;
-  finish(a, s, a.part_probs + (int64_t)s * a.chunks * a.E, a.chunks, a.counts + (int64_t)s * a.E, a.tokens[s],
-         tmp);
+  finish<kFinishThreads>(a, s, a.part_probs + (int64_t)s * a.chunks * a.E, a.chunks, a.counts + (int64_t)s * a.E,
+                         a.tokens[s], tmp);
 }
 
 }  // namespace
@@ -229,7 +283,7 @@ hipError_t launch_balance(const BalanceArgs& a, hipStream_t stream) {
   };
   const hipError_t e = a.sigmoid ? rows(std::true_type{}) : rows(std::false_type{});
   if (e != hipSuccess || a.chunks == 1) return e;
-  hipLaunchKernelGGL(balance_finish, dim3(a.n_seq), block, 0, stream, a);
+  hipLaunchKernelGGL(balance_finish, dim3(a.n_seq), dim3(kFinishThreads), 0, stream, a);
   return hipGetLastError();
 }
 

@@ -439,9 +439,9 @@ hipError_t launch(const NormArgs& args, hipStream_t stream) {
   auto run = [&](auto full, auto tail) {
     constexpr bool F = decltype(full)::value, L = decltype(tail)::value;
     auto go = [&](auto kernel) {
-      if (lds > 0) {
+      if (lds > 0) {  // (the same limit in every call: calls of several threads set it at once)
         const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)lds);
+                                                 kColumnsPerCu);
         if (e != hipSuccess) return e;
       }
       hipLaunchKernelGGL(kernel, grid, block, lds, stream, a);
