@@ -114,19 +114,21 @@ struct LinearPlan {
 const struct {
   int rows, outs;
   double us;
-} kLinearShapes[] = {{256, 256, 1.15}, {128, 256, 0.70}, {128, 128, 0.40}, {64, 128, 0.28}};
+} kLinearShapes[] = {{256, 256, 1.15}, {128, 256, 0.60}, {128, 128, 0.40}, {64, 128, 0.28}};
 
 // The cheapest by estimate, in us on an MI355X with 256 workgroups a round (one a CU in
 // every form).  Streaming: a launch 3.4; a step of its 8 waves is bound by the lines that
 // a CU takes, (16 + tokens) x 128 bytes a wave, less alone than beside 255 others; or the
 // weights' bytes at 6.5 TB/s.  Tiles: a launch and a round's start, chunks, up to 30 %
-// slower on a full chip, and for parts another launch and their bytes.  Over 45 sizes
-// with both sides measured (M = 1 .. 128; N x K = 384 x 7168, 2112 x 7168, 4096 x 7168,
-// 7168 x 2048, 1024 x 1024) what it picks takes 1.5 % more than the best on average.
-// Streaming with 16, 32, 64 tokens / best tiles: M=16 N=384 K=7168 6.6 8.1 11.6 / 9.7, N=4096
-// 12.4 12.4 13.5 / 16.0; M=32 N=2112 18.4 10.9 12.8 / 13.1; M=64 N=384 6.7 8.2 11.7 / 10.7, N=2112
-// 28.3 21.1 15.2 / 14.2, N=4096 41.2 23.5 16.6 / 18.4; M=100 N=2112 43.4 32.3 28.4 / 17.0.
-// Tiles of M=8192 N=384 K=7168: 256x256 130, in 4 parts 63, 128x256 80, 128x128 56, 64x128 66.
+// slower on a full chip, and for parts another launch and their bytes.  Over 50 sizes
+// with every form measured (M = 1, 16, 32, 64, 100, 128, 256, 512, 1024, 2048; N x K =
+// 384 x 7168, 2112 x 7168, 4096 x 7168, 7168 x 2048, 1024 x 1024) what it picks takes 0.2 %
+// more than the best on average.  Streaming with 16, 32, 64 tokens / best tiles, us: M=16
+// N=4096 K=7168 13.0 13.3 14.1 / 16.9; M=32 N=2112 19.0 11.7 13.7 / 14.2; M=64 N=384 7.5 8.8
+// 12.3 / 11.5, N=2112 32.7 25.4 19.5 / 15.3, N=4096 42.3 24.1 17.3 / 18.9; M=100 N=2112 43.9
+// 33.0 29.2 / 17.7.  Tiles: M=512 N=4096 64x128 40.8, 128x128 in 2 41.2, 128x256 in 4 41.9,
+// 256x256 in 4 43.0; M=2048 N=2112 128x256 77.2, 256x256 84.4; M=8192 N=384 256x256 130, in
+// 4 parts 63, 128x256 80, 128x128 56, 64x128 66.
 LinearPlan linear_plan(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t M, int N, int K, int gated) {
   constexpr int64_t kCus = 256;  // (of the model, so that the workspace depends on sizes alone)
   LinearPlan p{};
