@@ -805,7 +805,7 @@ size_t chord_linear_workspace_bytes(const void* x, int64_t ldx, const void* w, i
  * bias:     device [N] ([2N]) of bias_dtype (dtype or fp32), or NULL.
  * residual: device [M, ldr] of out_dtype, or NULL; may be `out` with its row stride.
  * out:      device [M, ldo] of out_dtype (dtype or fp32); columns from N on stay as
- *           they are.
+ *           they are.  It must not overlap x, w or bias.
  * workspace: chord_linear_workspace_bytes(...) bytes, 256-byte aligned, caller-owned
  *           (NULL where that is 0); calls that may overlap need one each.
  * 16-byte aligned rows with K % 8 == 0 are read in place; others are first copied to

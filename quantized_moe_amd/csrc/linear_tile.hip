@@ -21,6 +21,12 @@
 //
 // Sums leave from registers, rounded, 16 bytes a lane.  Outputs that do not lie so, and
 // the long code of GELU, go through LDS to a short loop over neighbouring outputs.
+//
+// 8192 tokens through 4096 x 7168 take 346 us (1.39 PFLOP/s; the library's plain product
+// 345), with the matrix units busy for 71 % of a clock that they hold to 1.8 GHz; 8192
+// through 7168 x 2048 with a residual 223 us (1.08 PFLOP/s; the library's plain product
+// 186): 32 chunks an item leave the epilogue, 670 MB in all, little to hide
+// behind.
 #include <type_traits>
 
 #include "linear_common.h"
