@@ -248,14 +248,17 @@ __global__ __launch_bounds__(kThreads) void balance_rows(BalanceArgs a) {
     float t = sums[0][e];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) t += sums[w][e];
-    if (only) sums[0][e] = t;  // (read by this thread alone until the barrier)
+    if (only) sums[0][e] = t;  // (no other thread reads it before the barrier)
     else a.part_probs[((int64_t)s * a.chunks + chunk) * a.E + e] = t;
   }
   if (chunk == 0) {
     for (int e = threadIdx.x; e < a.E; e += kThreads) a.counts[(int64_t)s * a.E + e] = counts[e];
     if (threadIdx.x == 0) a.tokens[s] = n;
   }
-  if (only) finish<kThreads>(a, s, sums[0], 1, counts, n, tmp);
+  if (only) {
+    __syncthreads();  // (where threads share an expert's chunks, another one takes the sum)
+    finish<kThreads>(a, s, sums[0], 1, counts, n, tmp);
+  }
 }
 
 __global__ __launch_bounds__(kFinishThreads) void balance_finish(BalanceArgs a) {

@@ -226,3 +226,16 @@ def test_two_graphs_of_one_pool(C):
         want = C.chord_moe_balance(logits, ids, want_grad=True)
         assert torch.equal(b.loss, want.loss) and torch.equal(b.grad, want.grad)
         assert torch.equal(z, C.chord_linear(x, w, act=C.ACT_RELU))
+
+
+@pytest.mark.parametrize("E", [1, 64, 65, 128, 200, 256, 257, 512])
+def test_one_workgroup_balances(C, E):
+    """Sequences that one workgroup finishes, several threads to an expert: the sums of
+    P come from other threads than those that use them."""
+    for T in (1, 7, 8, 9, 64):
+        logits, ids = test_gpu_balance.draw(T, E, min(E, 3), T + E)
+        for sigmoid in (False, True):
+            first = test_gpu_balance.check(C, logits.cuda(), ids.cuda(), sigmoid)
+            many = [C.chord_moe_balance(logits.cuda(), ids.cuda(), int(sigmoid)) for _ in range(8)]
+            torch.cuda.synchronize()
+            assert all(torch.equal(m.loss, first.loss) and torch.equal(m.probs, first.probs) for m in many)
