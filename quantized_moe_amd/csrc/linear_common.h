@@ -21,9 +21,11 @@ __device__ __forceinline__ f32x4_t mfma16(u32x4_t a, u32x4_t b, f32x4_t c) {
                                                    __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
 }
 
-// Buffer over `rows` rows (0: empty) of K values, `ld` apart.
+// Buffer over `rows` rows of K values, `ld` apart.  Without rows, whose lanes all ask for
+// kLinNothing, it is as long as one: a load's range check takes the offset of its chunk
+// off the length, which has to stay positive.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const uint16_t* p, int64_t rows, int64_t ld, int K) {
-  const int64_t bytes = rows > 0 ? ((rows - 1) * ld + K) * 2 : 0;
+  const int64_t bytes = ((rows > 0 ? rows - 1 : 0) * ld + K) * 2;
   return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)bytes, kLinRsrcWord3);
 }
 
