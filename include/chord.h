@@ -730,7 +730,7 @@ typedef enum { CHORD_NORM_RMS = 0, CHORD_NORM_LAYER = 1 } chord_norm_kind;
 typedef struct {
   int32_t kind;        /* chord_norm_kind */
   int32_t dtype;       /* chord_dtype of weight and bias */
-  float eps;           /* finite, >= 0 */
+  float eps;           /* a positive normal number */
   float offset;        /* finite; 1 for weights that are held less one */
   const void* weight;  /* device [H] */
   const void* bias;    /* device [H], or NULL */
