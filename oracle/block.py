@@ -182,6 +182,11 @@ def balance(logits, ids, sigmoid, n_seq=1, bias=None, grad_loss=None):
         big = np.abs(f - 1) + 2 * U32 * f
         e_less = 3 * U32 * f + 2 * U32 * np.abs(f - 1) + (
             (p[rows] * (big * rel[rows] + 3 * U32 * f)).sum(axis=1) + 24 * 2.0 ** -23 * (p[rows] @ big))[:, None]
+        if sigmoid:
+            # f - sum f p is (f - 1) - (sum (f - 1) p) + (1 - sum p), and the last is 1e-20 over
+            # the scores' sum: a constant, a quotient, a product and an addition to the mean.
+            short = 1e-20 / (e[rows].sum(axis=1, keepdims=True) + 1e-20)
+            e_less = e_less + short * (rel[rows].max(axis=1, keepdims=True) + 4 * U32)
         t = g * p[rows] * slope[rows]
         grad[rows] = t * less
         # Scores, slopes and products below 2^-126 are off by up to 2^-150 each instead;

@@ -5,8 +5,10 @@
 // of each sequence, and its gradient g / n p (f - sum f p) [* (1 - sigmoid)], f
 // constant.
 //
-// f - sum f p is taken of f - 1, as sum p = 1: near balance both are small there and
-// nothing cancels.  No sum depends on an order that changes: counts are whole
+// f - sum f p is taken as (f - 1) - sum (f - 1) p + (1 - sum p): near balance all of these
+// are small and nothing cancels.  The last is 0 for a softmax and 1e-20 / (sum + 1e-20)
+// for sigmoids, which counts where a row's are all small (from logits of -36 on with
+// eight experts).  No sum depends on an order that changes: counts are whole
 // numbers, P is added per wave, wave by wave, and chunk by chunk.
 //
 // 8192 rows of 384 with the gradient (25 MB, 5.0 us at a copy's rate) take 15.4 us for the
@@ -230,6 +232,7 @@ __global__ __launch_bounds__(kThreads) void balance_rows(BalanceArgs a) {
       }
       if (out != nullptr) {
         mean = wave_add(mean);
+        if (SIGMOID) mean -= 1e-20f * inv;  // (1 - sum p)
 #pragma unroll
         for (int i = 0; i < V; ++i)
           if (i * 64 + lane < a.E) out[i * 64 + lane] = g * p[i] * (f[i] - mean) * rest[i];

@@ -1,0 +1,55 @@
+"""Balance where its arithmetic is at an edge: scores that are all small beside the 1e-20
+of their sum.  Bounds are those of the operator's own tests."""
+
+import numpy as np
+import pytest
+import torch
+
+from tests import test_gpu_balance
+from tests.gpu_util import banner
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def C():
+    from quantized_moe_amd import chord
+    return chord
+
+
+# ---- balance: sigmoids whose sum is near 1e-20 -----------------------------------
+@pytest.mark.parametrize("level", [-20, -30, -36, -40, -44, -46, -48, -50, -60, -80])
+@pytest.mark.parametrize("E,left", [(4, 4), (8, 8), (256, 256), (384, 5)])
+def test_small_sigmoids(C, level, E, left):
+    """All scores of a row are small, so they do not add up to 1.  (`left` experts are
+    in service.)"""
+    T, k = 24, 2
+    banner(f"balance of logits near {level}, {left} of {E} experts")
+    for dtype in (F32, BF16):
+        logits, ids = test_gpu_balance.draw(T, E, k, E - level, dtype)
+        logits = (0.3 * logits.float() + level).to(dtype)
+        logits[7] = logits[7].abs()  # a row among them whose scores do
+        logits[:, left:] = -np.inf
+        ids %= left
+        ids[3] = -1
+        for n_seq in (1, 4):
+            up = torch.linspace(0.5, 2, n_seq).cuda()
+            test_gpu_balance.check(C, logits.cuda(), ids.cuda(), True, n_seq, grad_loss=up)
+            test_gpu_balance.check(C, logits.cuda(), ids.cuda(), False, n_seq, grad_loss=up)
+
+
+def test_gradient_of_small_sigmoids_against_differences(C):
+    """As test_gradient_against_differences has it, at scores of some 1e-20."""
+    logits, ids = test_gpu_balance.draw(48, 32, 2, 9)
+    logits = 0.3 * logits - 49
+    r = C.chord_moe_balance(logits.cuda(), ids.cuda(), C.SCORE_SIGMOID, want_grad=True)
+    g = r.grad.double()
+    size = g.norm().item()
+    step = 0.5 * g / size
+    two = [C.chord_moe_balance((logits.cuda().double() + s * step).float(), ids.cuda(), C.SCORE_SIGMOID).loss.item()
+           for s in (1, -1)]
+    # (Logits of 49 are rounded to 2^-19, the steps with them: 2^-19 sqrt(48 * 32) |g| at most.)
+    assert size > 0.01
+    assert abs((two[0] - two[1]) - size) < 0.05 * size + 2.0 ** -22 + 2.0 ** -18 * 40 * size
