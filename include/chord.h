@@ -748,8 +748,8 @@ typedef struct {
  *
  * Everything between is fp32: y comes from s before its rounding, the codes from
  * y before its own (so next to a border of two codes they may differ from those of
- * the rounded `out`).  A row whose squares overflow fp32 is scaled first, so finite
- * rows have finite norms.
+ * the rounded `out`).  A row whose sums or squares overflow fp32 is scaled first,
+ * so finite rows have finite norms.
  *
  * x:        device [T, ldx] of dtype, ldx >= H.
  * post:     host struct, or NULL: no norm behind the block.

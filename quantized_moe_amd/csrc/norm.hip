@@ -198,8 +198,9 @@ __device__ __forceinline__ float centre(float (&v)[V][8], const int (&n)[V], con
   float total = layer ? sum.spread<V, TAIL>(v, n, H, &mean) : sum.squares<V>(v);
   if (!__builtin_isfinite(total + mean)) {
     // (Uniform over the row's threads.  A row with an infinity or NaN stays so in small
-    // values, too.)
-    eps *= kShrink * kShrink;
+    // values, too.  A usual eps vanishes beside any row with squares of its own; a row of one
+    // value has none, and its zeros stay zeros as long as what they are divided by is not.)
+    eps = fmaxf(eps * kShrink * kShrink, 0x1p-126f);
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll

@@ -1,11 +1,12 @@
-"""Balance where its arithmetic is at an edge: scores that are all small beside the 1e-20
-of their sum.  Bounds are those of the operator's own tests."""
+"""Balance and norms where their arithmetic is at an edge: scores that are all small beside
+the 1e-20 of their sum, rows of one huge value.  Bounds are those of the operators' own
+tests."""
 
 import numpy as np
 import pytest
 import torch
 
-from tests import test_gpu_balance
+from tests import test_gpu_balance, test_gpu_norm
 from tests.gpu_util import banner
 
 pytestmark = pytest.mark.gpu
@@ -53,3 +54,38 @@ def test_gradient_of_small_sigmoids_against_differences(C):
     # (Logits of 49 are rounded to 2^-19, the steps with them: 2^-19 sqrt(48 * 32) |g| at most.)
     assert size > 0.01
     assert abs((two[0] - two[1]) - size) < 0.05 * size + 2.0 ** -22 + 2.0 ** -18 * 40 * size
+
+
+# ---- norms: rows of one huge value -------------------------------------------------
+@pytest.mark.parametrize("H", [1, 384, 512, 5000, 7113, 20001])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_constant_rows(C, H, dtype):
+    """Rows of one value, up to those whose sums or squares leave fp32.  Their layer norm
+    is the bias: powers of two add up exactly, so it is that to the bit, also as the
+    norm behind a block."""
+    values = [2.5, 2.0 ** 60, 2.0 ** 100, -2.0 ** 116, 2.0 ** 120, 2.0 ** 125, -2.0 ** 127, 3e38, -3.38e38]
+    T = len(values)
+    banner(f"constant rows H={H} {dtype}")
+    x = torch.tensor(values).to(dtype)[:, None].repeat(1, H).cuda()
+    exact = [t for t in range(T) if np.log2(abs(values[t])) % 1 == 0]
+    for kind in ("rms", "layer"):
+        p = test_gpu_norm.Part(C, H, kind, F32, bias=kind == "layer")
+        r = test_gpu_norm.check(C, x, p, codes=True)
+        assert torch.isfinite(r.out).all()
+        res = test_gpu_norm.rows(T, H, F32, 3).cuda()
+        behind = C.chord_norm(x, post=p.gpu, residual=res).sum
+        torch.cuda.synchronize()
+        assert torch.isfinite(behind).all()
+        if kind == "layer":
+            assert torch.equal(r.out[exact], p.gpu.bias.to(dtype).expand(T, H)[exact])
+            assert torch.equal(behind[exact], (res + p.gpu.bias)[exact])
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_eps_beside_squares_that_overflow(C, kind):
+    """An eps of the size of the squares' mean counts, though their sum leaves fp32."""
+    banner(f"large eps {kind}")
+    for H in (384, 5000):
+        p = test_gpu_norm.Part(C, H, kind, F32, eps=1e37)
+        x = torch.cat([test_gpu_norm.rows(4, H, F32, 1, 2.0 ** e) for e in (50, 60, 62, 70)]).cuda()
+        test_gpu_norm.check(C, x, p)
