@@ -355,19 +355,25 @@ __global__ __launch_bounds__(1024, TAIL && V == 1 && !FULL ? 8 : 4) void norm_ke
       if (p.bias != nullptr) b.each(0, col, n, [&](int i, int j, float f) { v[i][j] += f; });
     };
     if (FULL && a.post.weight != nullptr) norm(a.post, post_w, post_b);
-    float scale = a.scale;
     if (FULL && a.gate != nullptr) {
       const int64_t row = t * a.gate_row;
-      if (a.gate_col == 0)
-        scale *= gated(a.gate_dtype == CHORD_DTYPE_F32 ? one_value<CHORD_DTYPE_F32>(a.gate, row)
-                                                       : one_value<XT>(a.gate, row));
-      else
+      if (a.gate_col == 0) {
+        // (Before the scale: the product of the two may leave fp32 where what they make of
+        // the value does not.)
+        const float g = gated(a.gate_dtype == CHORD_DTYPE_F32 ? one_value<CHORD_DTYPE_F32>(a.gate, row)
+                                                              : one_value<XT>(a.gate, row));
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[i][j] *= g;
+      } else {
         gate.each(row, col, n, [&](int i, int j, float g) { v[i][j] *= gated(g); });
+      }
     }
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = __builtin_fmaf(v[i][j], scale, raw_value<ST>(r[i], j));
+      for (int j = 0; j < 8; ++j) v[i][j] = __builtin_fmaf(v[i][j], a.scale, raw_value<ST>(r[i], j));
     if (more) load_r(t + step);
     if (a.sum != nullptr) {
 #pragma unroll

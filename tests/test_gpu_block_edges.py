@@ -1,6 +1,6 @@
 """Balance and norms where their arithmetic is at an edge: scores that are all small beside
-the 1e-20 of their sum, rows of one huge value.  Bounds are those of the operators' own
-tests."""
+the 1e-20 of their sum, rows of one huge value, factors that leave fp32 before they meet.
+Bounds are those of the operators' own tests."""
 
 import numpy as np
 import pytest
@@ -89,3 +89,18 @@ def test_eps_beside_squares_that_overflow(C, kind):
         p = test_gpu_norm.Part(C, H, kind, F32, eps=1e37)
         x = torch.cat([test_gpu_norm.rows(4, H, F32, 1, 2.0 ** e) for e in (50, 60, 62, 70)]).cuda()
         test_gpu_norm.check(C, x, p)
+
+
+# ---- norms: factors that leave fp32 before they meet --------------------------------
+@pytest.mark.parametrize("shape", ["token", "column", "full"])
+@pytest.mark.parametrize("H", [200, 7168])
+def test_scale_and_gate_meet_the_value_one_by_one(C, shape, H):
+    """scale * gate is beyond fp32 both ways, scale * (gate * u) is not."""
+    T = 5
+    banner(f"far gates by {shape} H={H}")
+    gate = {"token": (T, 1), "column": (H,), "full": (T, H)}[shape]
+    for e in (-75, 70):
+        x = (test_gpu_norm.rows(T, H, F32, 1) * 2.0 ** -e).cuda()
+        g = torch.full(gate, 2.0 ** e, dtype=F32).cuda()
+        r = test_gpu_norm.check(C, x, gate=g, scale=1.5 * 2.0 ** e)
+        assert torch.isfinite(r.sum).all() and r.sum.abs().max() > 2.0 ** (e - 1)
