@@ -308,7 +308,12 @@ __global__ __launch_bounds__(1024, TAIL && V == 1 && !FULL ? 8 : 4) void norm_ke
   }
   RowSum sum{part, alone ? a.threads >> 6 : 1, 0, wave_sum((float)held), 0.f};
   if (alone) sum.count = sum.share(sum.own, 0.f).x;
-  auto gated = [&](float g) { return a.gate_sigmoid ? 1.f / (1.f + expf(-g)) : g; };
+  // (e^-|g|: e^-g leaves fp32 below -88, where the sigmoid is still there.)
+  auto gated = [&](float g) {
+    if (!a.gate_sigmoid) return g;
+    const float e = expf(-fabsf(g)), d = 1.f / (1.f + e);
+    return g < 0.f ? e * d : d;
+  };
   // (Whole waves leave, where a wave has a row; else the workgroup's rows are there
   // for all of its waves.)
   const uint32_t of = alone ? 1 : blockDim.x >> 6, mine = alone ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

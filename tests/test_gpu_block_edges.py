@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import block as B
 from tests import test_gpu_balance, test_gpu_norm
 from tests.gpu_util import banner
 
@@ -104,3 +105,23 @@ def test_scale_and_gate_meet_the_value_one_by_one(C, shape, H):
         g = torch.full(gate, 2.0 ** e, dtype=F32).cuda()
         r = test_gpu_norm.check(C, x, gate=g, scale=1.5 * 2.0 ** e)
         assert torch.isfinite(r.sum).all() and r.sum.abs().max() > 2.0 ** (e - 1)
+
+
+@pytest.mark.parametrize("shape", ["token", "column", "full"])
+def test_sigmoid_gates_far_from_zero(C, shape):
+    """Gates of -120 to 120: e^120 is beyond fp32, the sigmoid beside it only small (from
+    2^-126 down to nothing in steps of 2^-149)."""
+    T, H = 61, 264
+    banner(f"far sigmoid gates by {shape}")
+    x = test_gpu_norm.rows(T, H, F32, 1)
+    g = torch.linspace(-120, 120, T)[:, None].expand(T, H)
+    if shape == "column":
+        g = torch.linspace(-120, 120, H)[None, :].expand(T, H)
+    gpu = {"token": g[:, :1], "column": g[0], "full": g}[shape].contiguous().cuda()
+    r = C.chord_norm(x.cuda(), gate=gpu, gate_sigmoid=True)
+    torch.cuda.synchronize()
+    g = g.double().numpy()
+    s, err, _, _ = B.block_norm(x.double().numpy(), gate=g, gate_sigmoid=True)
+    # A sigmoid below 2^-126 is off by a step of 2^-149 instead, for its value's size.
+    err = err + 2.0 ** -149 * np.abs(x.double().numpy()) * (g < -80)
+    test_gpu_norm.close(r.sum, s, err, F32, "sum")
