@@ -1,18 +1,19 @@
-"""Balance and norms where their arithmetic is at an edge: scores that are all small beside
-the 1e-20 of their sum, rows of one huge value, factors that leave fp32 before they meet.
-Bounds are those of the operators' own tests."""
+"""Balance, norms and the 16-bit product where their arithmetic or their schedule is at an
+edge: scores that are all small beside the 1e-20 of their sum, rows of one huge value,
+factors that leave fp32 before they meet, products whose workgroups go through several
+items.  Bounds are those of the operators' own tests."""
 
 import numpy as np
 import pytest
 import torch
 
 from oracle import block as B
-from tests import test_gpu_balance, test_gpu_norm
+from tests import test_gpu_balance, test_gpu_linear, test_gpu_norm
 from tests.gpu_util import banner
 
 pytestmark = pytest.mark.gpu
 
-BF16, F32 = torch.bfloat16, torch.float32
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
 
 
 @pytest.fixture(scope="module")
@@ -125,3 +126,71 @@ def test_sigmoid_gates_far_from_zero(C, shape):
     # A sigmoid below 2^-126 is off by a step of 2^-149 instead, for its value's size.
     err = err + 2.0 ** -149 * np.abs(x.double().numpy()) * (g < -80)
     test_gpu_norm.close(r.sum, s, err, F32, "sum")
+
+
+# ---- products: several items a workgroup --------------------------------------------
+CUS, TILE = 256, 256
+ROUNDS = [
+    # M, rows of W, K, whole rounds of tiles of 256 x 256, items behind them
+    (2000, 4104, 584, 0, 136),   # one round of whole tiles, nine chunks and an eighth
+    (4300, 4104, 264, 1, 33),    # ... and a last one in halves; five chunks
+    (4200, 4104, 328, 1, 33),    # ... of which the last token tile's second has no rows
+    (5300, 5128, 264, 1, 185),   # ... of whole tiles
+    (5700, 5640, 264, 2, 17),
+]
+
+
+@pytest.mark.parametrize("M,R,K,rounds,rest", ROUNDS)
+def test_rounds_of_large_tiles(C, M, R, K, rounds, rest):
+    """Outputs that go straight to memory and through LDS, plain and gated."""
+    assert torch.cuda.get_device_properties(0).multi_processor_count == CUS
+    tiles = -(-M // TILE)
+    for dtype, rows, kw in ((BF16, R, dict(residual=True)),
+                            (F16, R - 2, dict(out=F32, bias=F16, act="relu")),
+                            (BF16, R - 6, dict(act="gelu_tanh", residual=True, scale=0.5)),
+                            (BF16, R, dict(gated=True, act="silu", bias=F32, residual=True, scale=0.7)),
+                            (F16, R - 4, dict(gated=True, act="silu", residual=True))):
+        items = tiles * -(-rows // TILE)
+        assert items == rounds * CUS + rest
+        test_gpu_linear.check(C, M, rows // (1 + kw.get("gated", False)), K, dtype, **kw)
+        assert C.last_plan() == "linear: tiles of 256 x 256, K in 1"
+
+
+def test_rounds_of_large_tiles_through_the_long_activation(C):
+    for M, R, K in ((2000, 4104, 328), (4300, 4104, 264)):
+        test_gpu_linear.check(C, M, R, K, act="gelu", residual=True)
+        assert C.last_plan() == "linear: tiles of 256 x 256, K in 1"
+
+
+@pytest.mark.parametrize("M,R,K,form", [
+    (3723, 264, 5704, "tiles of 256 x 256, K in 4"),     # 120 items: halves of parts
+    (6773, 522, 19448, "tiles of 256 x 256, K in 4"),    # 324: and a round of whole ones in front
+    (4948, 3080, 328, "tiles of 128 x 256, K in 1"),     # 507
+    (4098, 5658, 264, "tiles of 128 x 256, K in 1"),     # 759
+    (5481, 1292, 520, "tiles of 128 x 128, K in 1"),     # 473
+    (5897, 2570, 1032, "tiles of 128 x 128, K in 1"),    # 987
+])
+def test_rounds_of_other_tiles(C, M, R, K, form):
+    for dtype, gated, kw in ((BF16, False, dict(residual=True)), (F16, True, dict(act="silu", bias=F32))):
+        test_gpu_linear.check(C, M, R // (1 + gated), K, dtype, gated=gated, **kw)
+        assert C.last_plan() == "linear: " + form
+
+
+def test_equal_calls_of_several_rounds(C):
+    """Equal bits, also beside a second stream's call and from a graph."""
+    x, w = test_gpu_linear.rows(4300, 264, BF16, 1).cuda(), test_gpu_linear.rows(4104, 264, BF16, 2, 0.06).cuda()
+    res = test_gpu_linear.rows(4300, 4104, BF16, 3).cuda()
+    want = C.chord_linear(x, w, residual=res, act=C.ACT_SILU)
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    got = [C.chord_linear(x, w, residual=res, act=C.ACT_SILU, stream=s) for _ in range(4) for s in sides]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = C.chord_linear(x, w, residual=res, act=C.ACT_SILU)
+    for seed in range(3):
+        x.copy_(test_gpu_linear.rows(4300, 264, BF16, 10 + seed))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, C.chord_linear(x, w, residual=res, act=C.ACT_SILU))
