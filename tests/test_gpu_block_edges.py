@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from oracle import block as B
-from tests import test_gpu_balance, test_gpu_linear, test_gpu_norm
+from tests import test_gpu_balance, test_gpu_block_sizes, test_gpu_linear, test_gpu_norm
 from tests.gpu_util import banner
 
 pytestmark = pytest.mark.gpu
@@ -194,3 +194,19 @@ def test_equal_calls_of_several_rounds(C):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, C.chord_linear(x, w, residual=res, act=C.ACT_SILU))
+
+
+# ---- balance: drawn from the seed alone ---------------------------------------------
+@pytest.mark.parametrize("seed", range(30))
+def test_drawn_balances_of_a_seed(C, seed):
+    """Everything that is drawn, experts out of service and upstream gradients among it,
+    comes from the seed."""
+    rng = np.random.Generator(np.random.PCG64(500 + seed))
+    n_seq, E = test_gpu_block_sizes.drawn(rng, 1, 40), test_gpu_block_sizes.drawn(rng, 1, 1024)
+    T, k = n_seq * test_gpu_block_sizes.drawn(rng, 1, 300), test_gpu_block_sizes.drawn(rng, 1, min(E, 64))
+    banner(f"balance seed={seed} T={T} E={E} k={k} n_seq={n_seq}")
+    logits, ids = test_gpu_balance.draw(T, E, k, seed, (F32, BF16, F16)[rng.integers(3)], 0.2 * rng.integers(2))
+    bias = torch.from_numpy(np.where(rng.random(E) < 0.1, -np.inf, 0.0).astype(np.float32)).cuda()
+    up = torch.from_numpy((rng.random(n_seq) + 0.5).astype(np.float32)).cuda()
+    test_gpu_balance.check(C, logits.cuda(), ids.cuda(), bool(rng.integers(2)), n_seq, bias if rng.integers(2) else None,
+                           up if rng.integers(2) else None)
