@@ -123,6 +123,20 @@ __device__ __forceinline__ float first_lanes_sum(float x) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 15));
 }
 
+// Of e^-|g|, as e^-g leaves fp32 below -88, where the sigmoid is still there.  The
+// exponential of what is not positive needs one limit (e^-104 is nothing; a NaN passes)
+// where expf has two: with that 4096 rows of 7168 with a gate for each value take 66.5 us,
+// with expf 68.3, with expf of e^-g 66.4.
+__device__ __forceinline__ float sigmoid(float g) {
+#pragma clang fp contract(off)  // (whole is the rounded product, rest what it leaves)
+  constexpr float kLog2e = 0x1.715476p+0f, kRest = 0x1.4ae0cp-26f;  // of log2 e
+  const float x = fabsf(g) > 104.f ? -104.f : -fabsf(g);
+  const float whole = x * kLog2e, n = rintf(whole);
+  const float rest = __builtin_fmaf(x, kRest, __builtin_fmaf(x, kLog2e, -whole));
+  const float e = ldexpf(__builtin_amdgcn_exp2f((whole - n) + rest), (int)n);
+  return (g < 0.f ? e : 1.f) / (1.f + e);
+}
+
 // x where value j of a thread's eight is one of the row's (n of them are; without TAIL
 // all or none), else 0: what stands behind a row is 0 and stays so.
 template <bool TAIL>
@@ -308,12 +322,7 @@ __global__ __launch_bounds__(1024, TAIL && V == 1 && !FULL ? 8 : 4) void norm_ke
   }
   RowSum sum{part, alone ? a.threads >> 6 : 1, 0, wave_sum((float)held), 0.f};
   if (alone) sum.count = sum.share(sum.own, 0.f).x;
-  // (e^-|g|: e^-g leaves fp32 below -88, where the sigmoid is still there.)
-  auto gated = [&](float g) {
-    if (!a.gate_sigmoid) return g;
-    const float e = expf(-fabsf(g)), d = 1.f / (1.f + e);
-    return g < 0.f ? e * d : d;
-  };
+  auto gated = [&](float g) { return a.gate_sigmoid ? sigmoid(g) : g; };
   // (Whole waves leave, where a wave has a row; else the workgroup's rows are there
   // for all of its waves.)
   const uint32_t of = alone ? 1 : blockDim.x >> 6, mine = alone ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
