@@ -94,7 +94,9 @@ def activation(z, act):
     if act == "gelu":
         return 0.5 * z * _erfc(-z / math.sqrt(2.0)).astype(np.float64)
     if act == "gelu_tanh":
-        return 0.5 * z * (1.0 + np.tanh(math.sqrt(2.0 / math.pi) * (z + 0.044715 * z ** 3)))
+        # (1 + tanh a) / 2 = 1 / (1 + e^-2a), where nothing cancels.
+        with np.errstate(over="ignore"):
+            return z / (1.0 + np.exp(-2.0 * math.sqrt(2.0 / math.pi) * (z + 0.044715 * z ** 3)))
     return z
 
 

@@ -37,9 +37,12 @@ __device__ __forceinline__ void lds_barrier() {
 }
 
 // z / (1 + e^-y) with the hardware's exponential and reciprocal (about a unit of 2^-24
-// each, and of the exponent's argument y one for each unit of y).
+// each, and of the exponent's argument y one for each unit of y).  Of h = e^(-|y| / 2),
+// below 0 as z h h / (1 + h h): e^-y leaves fp32 below -88, and its reciprocal the normal
+// numbers before that, where the result is still there.
 __device__ __forceinline__ float gate_of(float z, float y) {
-  return z * __builtin_amdgcn_rcpf(1.f + __expf(-y));
+  const float h = __expf(-0.5f * fabsf(y)), r = __builtin_amdgcn_rcpf(__builtin_fmaf(h, h, 1.f));
+  return (y < 0.f ? z * h * h : z) * r;
 }
 // The activations of a few instructions (all but GELU).
 __device__ __forceinline__ float activate_short(int act, float z) {

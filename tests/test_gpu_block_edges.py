@@ -210,3 +210,33 @@ def test_drawn_balances_of_a_seed(C, seed):
     up = torch.from_numpy((rng.random(n_seq) + 0.5).astype(np.float32)).cuda()
     test_gpu_balance.check(C, logits.cuda(), ids.cuda(), bool(rng.integers(2)), n_seq, bias if rng.integers(2) else None,
                            up if rng.integers(2) else None)
+
+
+# ---- products: activations far below 0 ----------------------------------------------
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh", "gelu"])
+@pytest.mark.parametrize("M,K,gated", [(3, 8, False), (40, 16, True), (300, 8, False), (700, 72, True)])
+def test_activations_that_nearly_vanish(C, act, M, K, gated):
+    """z of -120 to 0 (exact: one product of a power of two each), where e^-z leaves fp32 and
+    the result does not: it is off by 8 units and some for each of the exponent's, or by a
+    step or two of 2^-149.  The exponential rounds its argument times log2 e, itself
+    rounded: 2 units for each of the argument's, and erfc takes no more than twice that.
+    GELU_TANH's argument c (z + d z z z) has its own roundings, of d, of three products, of
+    the sum, of c and of the last product: 7 more."""
+    N = 512
+    banner(f"{act} far below 0, M={M} K={K} gated={gated}")
+    z = torch.linspace(-120 if act == "silu" else -15, 0, N).to(BF16)
+    x = torch.zeros((M, K), dtype=BF16)
+    x[:, 0], x[:, 1] = 1, 2
+    w = torch.zeros((N * (1 + gated), K), dtype=BF16)
+    w[:N, 0] = z
+    w[N:, 1] = 0.5
+    got = C.chord_linear(x.cuda(), w.cuda(), act=getattr(C, "ACT_" + act.upper()), gated=gated, out_dtype=F32)
+    torch.cuda.synchronize()
+    z = z.double().numpy()
+    ref = B.activation(z, act)
+    u = {"silu": np.abs(z), "gelu": z * z / 2, "gelu_tanh": np.abs(1.6 * (z + 0.045 * z ** 3))}[act]
+    # Half a step each of z h, z h h and the last product; of GELU's erfc a step for each unit of z.
+    each = 9 if act == "gelu_tanh" else 4
+    bound = (8 + each * u) * B.U32 * np.abs(ref) + 2.0 ** -149 * (2 + np.abs(z))
+    err = np.abs(got.double().cpu().numpy() - ref)
+    assert np.all(err <= bound), (np.argwhere(err > bound)[:4], z[(err > bound).any(axis=0)][:4])
