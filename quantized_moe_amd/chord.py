@@ -723,6 +723,14 @@ class Norm:
     fp16.  `offset` is added to the weights (1 for weights held less one)."""
 
     def __init__(self, weight, bias=None, eps: float = 1e-6, kind: int = NORM_RMS, offset: float = 0.0):
+        self.weight, self.bias = weight, bias
+        self.handle = NormWeight(kind, 0, eps, offset, None, None)
+        self.ref = ctypes.byref(self.handle)
+        self._bind()
+
+    def _bind(self):
+        """Takes the tensors as they are now (again, if they have got other memory)."""
+        weight, bias = self.weight, self.bias
         if not isinstance(weight, torch.Tensor) or not weight.is_cuda or weight.dim() != 1:
             _refuse("weight must be a vector on the GPU")
         dtype = _DTYPES.get(weight.dtype)
@@ -732,10 +740,9 @@ class Norm:
         _tensor(weight, "weight", weight.dtype, (self.H,), self.device)
         if bias is not None:
             _tensor(bias, "bias", weight.dtype, (self.H,), self.device)
-        self.weight, self.bias = weight, bias
-        self.handle = NormWeight(kind, dtype, eps, offset, weight.data_ptr(),
-                                 None if bias is None else bias.data_ptr())
-        self.ref = ctypes.byref(self.handle)
+        self.handle.dtype = dtype
+        self.handle.weight = self.weight_at = weight.data_ptr()
+        self.handle.bias = self.bias_at = None if bias is None else bias.data_ptr()
 
 
 class NormResult(NamedTuple):
@@ -748,6 +755,9 @@ class NormResult(NamedTuple):
 def _norm(n, name: str, H: int, device: int):
     if not isinstance(n, Norm):
         _refuse(f"{name} must be a Norm")
+    # (A weight that has moved, as an optimiser's or a loader's `.data = ` makes it.)
+    if n.weight.data_ptr() != n.weight_at or (None if n.bias is None else n.bias.data_ptr()) != n.bias_at:
+        n._bind()
     if n.H != H or n.device != device:
         _refuse(f"{name} has {n.H} weights on GPU {n.device}, expected {H} on {device}")
     return n.ref

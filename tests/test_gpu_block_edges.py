@@ -93,6 +93,29 @@ def test_eps_beside_squares_that_overflow(C, kind):
         test_gpu_norm.check(C, x, p)
 
 
+# ---- norms: weights that have moved --------------------------------------------------
+def test_weights_that_have_moved(C):
+    """A norm reads its tensors where they are at the call."""
+    banner("weights that have moved")
+    H = 200
+    x = test_gpu_norm.rows(3, H, BF16, 1).cuda()
+    for bias in (False, True):
+        p, q = (test_gpu_norm.Part(C, H, "layer", BF16, bias, seed=s) for s in (1, 2))
+        n = p.gpu
+        before = [n.weight.data, n.bias.data if bias else None]   # (kept, so that nothing is freed)
+        n.weight.data = q.gpu.weight.clone()
+        if bias:
+            n.bias.data = q.gpu.bias.clone()
+        assert torch.equal(C.chord_norm(x, n).out, C.chord_norm(x, q.gpu).out)
+        n.weight = before[0].float()
+        n.bias = before[1].float() if bias else None
+        want = C.chord_norm(x, C.Norm(n.weight, n.bias, 1e-6, C.NORM_LAYER)).out
+        assert torch.equal(C.chord_norm(x, n).out, want)
+        n.weight = before[0][::2]
+        with pytest.raises(C.ChordError):
+            C.chord_norm(x, n)
+
+
 # ---- norms: factors that leave fp32 before they meet --------------------------------
 @pytest.mark.parametrize("shape", ["token", "column", "full"])
 @pytest.mark.parametrize("H", [200, 7168])
