@@ -52,11 +52,13 @@ BalancePlan balance_plan(int T, int E, int k, int n_seq) {
   const int64_t slots = L * k;
   p.parts = slots <= 16384 ? 0 : (int)std::min<int64_t>(16, (slots + 16383) / 16384);
   // Rows of a workgroup: one a wave, up to four where that fills the CUs, and more where
-  // there would be over 1024 workgroups; sequences of up to 64 rows in one, which then
-  // needs no second launch (64 rows of 256 experts: 15 us a call for 20, of which the
-  // second launch and its workspace take 5 on the host).
+  // there would be over 1024 workgroups.  Short sequences in one, which then needs no second
+  // launch: a wave goes through its rows one after the other, the longer each the more
+  // experts it has, so up to 64 rows and 384 groups of 64 logits.  us a call (the launches
+  // alone), one / two launches: 64 rows of 256 experts 14.5 (14.3) / 18.1 (9.6), of 384 17.0
+  // (16.9) / 18.2 (10.5), of 1024 36.3 (36.3) / 18.4 (15.5); 16 of 1024 16.0 (15.7) / 18.3.
   p.rows = std::max<int64_t>({8, std::min<int64_t>(32, (T + 255) / 256), (T + 1023) / 1024});
-  if (L <= 64) p.rows = std::max<int64_t>(p.rows, 64);
+  if (L <= 64 && L * ((E + 63) / 64) <= 384) p.rows = std::max<int64_t>(p.rows, 64);
   p.chunks = (int)std::max<int64_t>(1, (L + p.rows - 1) / p.rows);
   size_t off = 0;
   if (p.parts > 0) off += ((size_t)n_seq * p.parts * (E + 1) * 4 + 15) & ~(size_t)15;

@@ -263,3 +263,17 @@ def test_activations_that_nearly_vanish(C, act, M, K, gated):
     bound = (8 + each * u) * B.U32 * np.abs(ref) + 2.0 ** -149 * (2 + np.abs(z))
     err = np.abs(got.double().cpu().numpy() - ref)
     assert np.all(err <= bound), (np.argwhere(err > bound)[:4], z[(err > bound).any(axis=0)][:4])
+
+
+@pytest.mark.parametrize("E,rows", [(384, 64), (385, 54), (512, 48), (1000, 24), (1024, 24)])
+def test_both_sides_of_one_launch(C, E, rows):
+    """Rows that one launch takes, and one more."""
+    for L in (rows, rows + 1):
+        for n_seq in (1, 3):
+            banner(f"balance n_seq={n_seq} rows={L} E={E}")
+            logits, ids = test_gpu_balance.draw(n_seq * L, E, 7, E + L, BF16, 0.1)
+            for sigmoid in (False, True):
+                a = test_gpu_balance.check(C, logits.cuda(), ids.cuda(), sigmoid, n_seq)
+                b = C.chord_moe_balance(logits.cuda(), ids.cuda(), int(sigmoid), n_seq=n_seq, want_grad=True)
+                torch.cuda.synchronize()
+                assert all(torch.equal(p, q) for p, q in zip(a, b))
