@@ -130,7 +130,9 @@ const struct {
 // 12.3 / 11.5, N=2112 32.7 25.4 19.5 / 15.3, N=4096 42.3 24.1 17.3 / 18.9; M=100 N=2112 43.9
 // 33.0 29.2 / 17.7.  Tiles: M=512 N=4096 64x128 40.8, 128x128 in 2 41.2, 128x256 in 4 41.9,
 // 256x256 in 4 43.0; M=2048 N=2112 128x256 77.2, 256x256 84.4; M=8192 N=384 256x256 130, in
-// 4 parts 63, 128x256 80, 128x128 56, 64x128 66.
+// 4 parts 63, 128x256 80, 128x128 56, 64x128 66.  All of it with inputs that the caches
+// hold: x of 8192 rows from HBM takes 77 with 128x128, where 256x256 in 4 parts takes 74 and
+// 128x256 in 2 parts 71.
 LinearPlan linear_plan(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t M, int N, int K, int gated) {
   constexpr int64_t kCus = 256;  // (of the model, so that the workspace depends on sizes alone)
   LinearPlan p{};

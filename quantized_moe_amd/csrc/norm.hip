@@ -8,9 +8,9 @@
 // it has: 8192 rows of 7168 in bf16 with a residual (470 MB) take 84 us, 5.6 TB/s, where
 // a copy reaches 5.1, with the vector units busy for 31 %; 4099 rows of 7112 between two
 // layer norms with a gate and an fp32 stream (350 MB) 88 us, 4.0 TB/s, vector units 41 %.
-// There the row's chain bounds it: four sums over a workgroup one after the other,
-// with only the other workgroups' rows to fill the gaps.  Below some 100 rows it is one
-// row's chain alone: 4 us for one row, 8 with both norms.
+// There the row's chain bounds it: two norms one after the other, each with sums over its
+// waves and an exchange between them, and only the other workgroup's rows to fill the gaps.
+// Below some 100 rows it is one row's chain alone: 4 us for one row, 8 with both norms.
 #include <type_traits>
 
 #include "f8_common.h"
